@@ -95,6 +95,7 @@ typedef enum lmh_status {
 #define LMH_ENTRY_VP_SUPPORT_PARTIALS 9
 #define LMH_ENTRY_VP_SUPPORT_COMBINE 10
 #define LMH_ENTRY_VP_SUPPORT_BWD 11
+#define LMH_ENTRY_RMS_NORM_BWD 12 /* reads N and d of the shape */
 
 /* objectives of lmh_loss_bwd */
 #define LMH_BWD_CE 0              /* L = sum_i g_i loss_i                                */
@@ -520,6 +521,57 @@ LMH_API lmh_status lmh_reduce_ranks_f32(int R, int64_t n, const float* parts, fl
  * lmh_support_kl_fwd_bwd) computed for g = 1, with no host synchronisation.
  */
 LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* stream);
+
+/*
+ * The entries around the head. The pages' ops end at the loss; these make its input (the final
+ * norm) and serve the same head: lmh_rms_norm gives H as bf16 or as 8-bit values, which
+ * lmh_quantize_fp8 gives of W.
+ *
+ * 8-bit matrices: e4m3 values [rows, d], row-major and contiguous, d a multiple of 64, with fp32
+ * scales [ceil(rows / B), ceil(d / 128)], one per block of B x 128 values (B = 1 for hidden
+ * states, 128 for weights; the last block of a row or column may be partial). The value stood
+ * for is q * scale. A block of values v has scale = max(amax |v|, 2^-100) / 448 and q = v /
+ * scale rounded to nearest even, so its largest value becomes +-448. A block that holds a NaN
+ * gets NaN scale and values; one that holds an infinity has an infinite scale, NaN at the
+ * infinities and 0 elsewhere.
+ *
+ * lmh_rms_norm — the RMS norm of x + residual: r = bf16(x + residual) (round to nearest even;
+ * r = x without a residual), rstd = 1 / sqrt(mean_j r_j^2 + eps), y = weight_j r_j rstd. The
+ * norm is that of the rounded r, the stream as it is stored. All arithmetic is fp32; y is
+ * rounded once, to bf16 or (not by way of bf16) to e4m3.
+ *   x [N, d], weight [d] bf16; residual [N, d] bf16, nullable. d a multiple of 64, at most
+ *   16384; 0 <= N < 2^31; eps finite and >= 0.
+ *   sum [N, d] bf16 out, nullable: r. It may be x or residual themselves (in place).
+ *   y [N, d] bf16 out, and q [N, d] e4m3 with scale [N, ceil(d / 128)] fp32 out: either or both;
+ *   these overlap no input. rstd [N] fp32 out, nullable. No workspace.
+ *   A row that holds a NaN gives NaN; one that holds an infinity gives NaN there and 0
+ *   elsewhere. A row of finite values whose fp32 sum of squares overflows (|r| around 1e18 and
+ *   more) gives 0.
+ *
+ * lmh_rms_norm_bwd — its gradients, from sum = r and rstd as the forward gave them: with
+ * n_j = r_j rstd and c = mean_j(weight_j dy_j n_j),
+ *   dx = rstd (weight dy - n c) + dsum   (the gradient of x and of residual alike),
+ *   dweight_j = sum over the rows of dy_j n_j.
+ *   dy [N, d] bf16: dL/dy. dsum [N, d] bf16, nullable: the gradient that reaches r by another
+ *   way than y. dx [N, d] and dweight [d] bf16 out, each nullable but not both; dx may be dy or
+ *   dsum themselves. dweight is summed in fp32 over fixed slices of the rows (a function of N),
+ *   in a fixed order, and rounded once; N = 0 gives 0. Workspace: lmh_workspace_size(shape,
+ *   LMH_ENTRY_RMS_NORM_BWD) with N and d in the shape (V any valid value).
+ *
+ * lmh_quantize_fp8 — x [rows, d] bf16 as an 8-bit matrix q, scale with blocks of block_rows x 128
+ * (block_rows 1 or 128). No workspace.
+ */
+LMH_API lmh_status lmh_rms_norm(int64_t N, int64_t d, const lmh_bf16* x,
+                                const lmh_bf16* residual, const lmh_bf16* weight, float eps,
+                                lmh_bf16* sum, lmh_bf16* y, uint8_t* q, float* scale,
+                                float* rstd, void* stream);
+LMH_API lmh_status lmh_rms_norm_bwd(int64_t N, int64_t d, const lmh_bf16* sum,
+                                    const lmh_bf16* weight, const float* rstd,
+                                    const lmh_bf16* dy, const lmh_bf16* dsum, lmh_bf16* dx,
+                                    lmh_bf16* dweight, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+LMH_API lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_rows,
+                                    const lmh_bf16* x, uint8_t* q, float* scale, void* stream);
 
 /*
  * lmh_read_errors — synchronises `stream`, then copies the device error word of the last

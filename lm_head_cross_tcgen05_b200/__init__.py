@@ -8,6 +8,7 @@ not been built (``python lm_head_cross_tcgen05_b200/build.py``).
 
 The lower-case helpers (``loss_fwd``, ``loss_bwd``, ``logprob``, ``support_logprob``,
 ``support_kl``) allocate the outputs and the workspace with torch and call the same entries.
+The entries around the head (the norm, the 8-bit head) are in ``serving.py`` and offered here.
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ from ._abi import (BWD_CE, BWD_LOGPROB, BWD_SUPPORT_KL, BWD_SUPPORT_LOGPROB, DEV
                    DEVERR_NONFINITE, DEVERR_TEMPERATURE, DEVERR_TIMEOUT, ENTRY_LOGPROB, ENTRY_LOSS_BWD,
                    ENTRY_LOSS_FWD, ENTRY_SUPPORT_KL, ENTRY_SUPPORT_LOGPROB, ENTRY_VP_BWD,
                    ENTRY_LOSS_FWD_BWD, ENTRY_VP_COMBINE, ENTRY_VP_PARTIALS,
+                   ENTRY_RMS_NORM_BWD,
                    ENTRY_VP_SUPPORT_BWD, ENTRY_VP_SUPPORT_COMBINE, ENTRY_VP_SUPPORT_PARTIALS,
                    F_DW_ACC_GIVEN, F_DW_ACC_STORE,
                    F_GRAD_SCALAR, lmh_vp_dest,
@@ -43,6 +45,8 @@ __all__ = [
     "lmh_vp_support_partials", "lmh_vp_support_combine", "lmh_vp_support_bwd",
     "F_DW_ACC_STORE", "lmh_count_valid", "lmh_reduce_ranks_f32", "lmh_dp_loss_fwd_bwd",
     "lmh_peer_barrier",
+    "ENTRY_RMS_NORM_BWD", "lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8",
+    "rms_norm", "rms_norm_bwd", "quantize_fp8",
 ]
 
 lib()  # load now: a missing library is an import error, never a silent fallback
@@ -612,3 +616,7 @@ def support_kl(H, W, ids, ref_logp, *, chunk_rows: int = 0, temperature=None,
                        out["lse"], workspace=ws, stream=stream)
     out["workspace"] = ws
     return out
+
+
+from .serving import (lmh_quantize_fp8, lmh_rms_norm, lmh_rms_norm_bwd, quantize_fp8,  # noqa: E402
+                      rms_norm, rms_norm_bwd)

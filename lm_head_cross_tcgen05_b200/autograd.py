@@ -23,10 +23,10 @@ from __future__ import annotations
 import torch
 
 from . import (BWD_CE, BWD_LOGPROB, BWD_SUPPORT_KL, BWD_SUPPORT_LOGPROB, lmh_scale_bf16,
-               logprob, loss_bwd, loss_fwd, support_kl as _support_kl,
-               support_logprob as _support_logprob)
+               logprob, loss_bwd, loss_fwd, rms_norm as _rms_norm, rms_norm_bwd,
+               support_kl as _support_kl, support_logprob as _support_logprob)
 
-__all__ = ["log_probs", "cross_entropy", "support_log_probs", "support_kl"]
+__all__ = ["log_probs", "cross_entropy", "support_log_probs", "support_kl", "rms_norm"]
 
 
 def _grads(ctx, mode, targets, g, ref=None, *, mean=False, scalar=False, renorm=False):
@@ -167,3 +167,31 @@ def support_kl(H, W, ids, ref_logp, *, reduction: str = "mean", chunk_rows: int 
     if reduction not in ("none", "mean"):
         raise ValueError(f"reduction must be none or mean, got {reduction!r}")
     return _SupportKL.apply(H, W, ids, ref_logp, reduction, chunk_rows, temperature, renorm)
+
+
+class _RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        out = _rms_norm(x, weight, residual, eps=eps)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(out["sum"], weight, out["rstd"])
+        return out["y"] if residual is None else (out["y"], out["sum"])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy, dsum=None):
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        if dy is None:  # y took no part in the loss
+            return dsum if need_x else None, None, dsum if need_r else None, None
+        total, weight, rstd = ctx.saved_tensors
+        out = rms_norm_bwd(total, weight, rstd, dy.contiguous(),
+                           None if dsum is None else dsum.contiguous(), want_dx=need_x or need_r,
+                           want_dweight=need_w)
+        return (out["dx"] if need_x else None, out["dweight"], out["dx"] if need_r else None,
+                None)
+
+
+def rms_norm(x, weight, residual=None, *, eps: float = 1e-6):
+    """RMS norm of x + residual (rows of d), differentiable in x, weight and residual: y, or with
+    a residual (y, sum), sum being the stream x + residual that a next layer adds to."""
+    return _RMSNorm.apply(x, weight, residual, eps)

@@ -161,6 +161,16 @@ Plan make_plan(const lmh_shape* s, int entry, bool fused, bool dw_without_acc) {
   return p;
 }
 
+// ------------------------------------------------------------------------ norm plan
+bool norm_shape_ok(int64_t N, int64_t d) {
+  return N >= 0 && N <= 0x7fffffffLL && d > 0 && d % 64 == 0 && d <= kNormMaxD;
+}
+// Row slices of the norm's backward pass, each with an fp32 share of dweight: by N alone.
+int norm_slices(int64_t N) { return static_cast<int>(N < kNormSlices ? N : kNormSlices); }
+size_t norm_bwd_bytes(int64_t N, int64_t d) {
+  return norm_shape_ok(N, d) ? align_up(sizeof(WsHeader) + static_cast<size_t>(norm_slices(N)) * d * 4) : 0;
+}
+
 // ------------------------------------------------------------------------ device state
 struct DevState {
   bool init = false;
@@ -200,7 +210,8 @@ enum KernelId {
   KID_SUPPORT_OUT, KID_BWD_COEF, KID_CAST, KID_SUPPORT_DOTS, KID_SUPPORT_LSE,
   KID_SUPPORT_DH, KID_SUPPORT_DW, KID_SPLIT_SUM, KID_VP_LABELS, KID_VP_FINALIZE,
   KID_VP_COMBINE, KID_VP_REDUCE, KID_VP_SCALE, KID_FIX_CANDS, KID_SCALE, KID_COUNT_VALID,
-  KID_REDUCE_RANKS, KID_ZERO_SLOTS, KID_PEER_BARRIER, KID_COUNT
+  KID_REDUCE_RANKS, KID_ZERO_SLOTS, KID_PEER_BARRIER, KID_RMS_NORM, KID_RMS_NORM_BWD,
+  KID_NORM_DWEIGHT, KID_QUANTIZE, KID_COUNT
 };
 const char* const kKernelNames[KID_COUNT] = {
     "count_labels", "prep_cands", "gemm_logits_stats", "gemm_logits_stats_store",
@@ -208,7 +219,8 @@ const char* const kKernelNames[KID_COUNT] = {
     "mean", "support_out", "bwd_coef", "cast_bf16", "support_dots", "support_lse",
     "support_grad_dh", "support_dw", "split_sum", "vp_local_labels", "vp_finalize",
     "vp_combine", "vp_reduce_rows", "vp_scale", "fix_cands", "scale_bf16", "count_valid",
-    "reduce_ranks", "zero_slots", "peer_barrier"};
+    "reduce_ranks", "zero_slots", "peer_barrier", "rms_norm", "rms_norm_bwd", "norm_dweight",
+    "quantize_fp8"};
 
 struct ProfRec {
   int id;

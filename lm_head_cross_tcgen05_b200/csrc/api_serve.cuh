@@ -1,0 +1,131 @@
+// api_serve.cuh — the entries around the head: the RMS norm that makes H, the e4m3 quantisation,
+// the 8-bit logits and the sampling. Part of the one translation unit lmh_api.cu.
+#pragma once
+
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Vectors of 8 per thread (1, 2 or 4) and threads per row (a multiple of 32, at most 512).
+void norm_threads(int64_t d, int* vpt, int* threads) {
+  const int64_t nv = d / 8;
+  *vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
+  *threads = static_cast<int>(cdiv(cdiv(nv, *vpt), 32) * 32);
+}
+
+}  // namespace
+
+extern "C" lmh_status lmh_rms_norm(int64_t N, int64_t d, const lmh_bf16* x,
+                                   const lmh_bf16* residual, const lmh_bf16* weight, float eps,
+                                   lmh_bf16* sum, lmh_bf16* y, uint8_t* q, float* scale,
+                                   float* rstd, void* stream) {
+  if (!norm_shape_ok(N, d) || !(eps >= 0.f && eps < 3.0e38f)) return LMH_ERR_INVALID_ARG;
+  if (N > 0 && ((!y && !q) || (q == nullptr) != (scale == nullptr) || !x || !weight))
+    return LMH_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum) ||
+      !aligned16(y) || !aligned16(q) || !aligned4(scale) || !aligned4(rstd))
+    return LMH_ERR_ALIGNMENT;
+  int dev, sms;
+  LMH_TRY(current_device(&dev, &sms));
+  if (N == 0) return LMH_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  NormParams p;
+  p.N = N;
+  p.d = static_cast<int>(d);
+  p.eps = eps;
+  p.x = reinterpret_cast<const uint4*>(x);
+  p.residual = reinterpret_cast<const uint4*>(residual);
+  p.weight = reinterpret_cast<const uint4*>(weight);
+  p.sum = reinterpret_cast<uint4*>(sum);
+  p.y = reinterpret_cast<uint4*>(y);
+  p.q = reinterpret_cast<uint2*>(q);
+  p.scale = scale;
+  p.rstd = rstd;
+  int vpt, threads;
+  norm_threads(d, &vpt, &threads);
+  const int ry = threads <= 32 ? 4 : (threads <= 64 ? 2 : 1);  // rows per block: 128 threads or more
+  const dim3 block(threads, ry);
+  const unsigned grid = static_cast<unsigned>(cdiv(N, ry));
+  ProfScope ps(KID_RMS_NORM, st);
+  if (vpt == 1) rms_norm_kernel<1><<<grid, block, 0, st>>>(p);
+  else if (vpt == 2) rms_norm_kernel<2><<<grid, block, 0, st>>>(p);
+  else rms_norm_kernel<4><<<grid, block, 0, st>>>(p);
+  return last_launch();
+}
+
+extern "C" lmh_status lmh_rms_norm_bwd(int64_t N, int64_t d, const lmh_bf16* sum,
+                                       const lmh_bf16* weight, const float* rstd,
+                                       const lmh_bf16* dy, const lmh_bf16* dsum, lmh_bf16* dx,
+                                       lmh_bf16* dweight, void* workspace,
+                                       size_t workspace_bytes, void* stream) {
+  if (!norm_shape_ok(N, d) || !workspace) return LMH_ERR_INVALID_ARG;
+  if (N > 0 && (!sum || !weight || !rstd || !dy || (!dx && !dweight))) return LMH_ERR_INVALID_ARG;
+  if (!aligned16(sum) || !aligned16(weight) || !aligned16(dy) || !aligned16(dsum) ||
+      !aligned16(dx) || !aligned16(dweight) || !aligned4(rstd) ||
+      (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+    return LMH_ERR_ALIGNMENT;
+  const int slices = norm_slices(N);
+  if (workspace_bytes < norm_bwd_bytes(N, d))
+    return LMH_ERR_WORKSPACE_TOO_SMALL;
+  int dev, sms;
+  LMH_TRY(current_device(&dev, &sms));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Ws ws{static_cast<uint8_t*>(workspace), static_cast<WsHeader*>(workspace)};
+  if (N == 0) {
+    if (dweight && cudaMemsetAsync(dweight, 0, static_cast<size_t>(d) * 2, st) != cudaSuccess)
+      return LMH_ERR_CUDA;
+    return clear_header(ws, st);
+  }
+  NormBwdParams p;
+  p.N = N;
+  p.d = static_cast<int>(d);
+  p.slices = slices;
+  p.sum = reinterpret_cast<const uint4*>(sum);
+  p.weight = reinterpret_cast<const uint4*>(weight);
+  p.rstd = rstd;
+  p.dy = reinterpret_cast<const uint4*>(dy);
+  p.dsum = reinterpret_cast<const uint4*>(dsum);
+  p.dx = reinterpret_cast<uint4*>(dx);
+  p.part = dweight ? ws.at<float>(sizeof(WsHeader)) : nullptr;
+  p.h = ws.h;
+  int vpt, threads;
+  norm_threads(d, &vpt, &threads);
+  {
+    ProfScope ps(KID_RMS_NORM_BWD, st);
+    const unsigned grid = static_cast<unsigned>(slices);
+    if (vpt == 1) rms_norm_bwd_kernel<1><<<grid, threads, 0, st>>>(p);
+    else if (vpt == 2) rms_norm_bwd_kernel<2><<<grid, threads, 0, st>>>(p);
+    else rms_norm_bwd_kernel<4><<<grid, threads, 0, st>>>(p);
+  }
+  LMH_TRY(last_launch());
+  if (!dweight) return LMH_OK;
+  ProfScope ps(KID_NORM_DWEIGHT, st);
+  norm_dweight_kernel<<<static_cast<unsigned>(d / 32), dim3(32, 16), 0, st>>>(
+      slices, static_cast<int>(d), p.part, reinterpret_cast<__nv_bfloat16*>(dweight));
+  return last_launch();
+}
+
+extern "C" lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_rows,
+                                       const lmh_bf16* x, uint8_t* q, float* scale,
+                                       void* stream) {
+  if (rows < 0 || rows > 0x7fffffffLL || d <= 0 || d % 64 != 0 || d > (1LL << 24) ||
+      (block_rows != 1 && block_rows != kQBlock))
+    return LMH_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !q || !scale)) return LMH_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return LMH_ERR_ALIGNMENT;
+  const int64_t nb = cdiv(d, kQBlock);
+  const int64_t grid = block_rows == 1 ? cdiv(rows * nb, 16) : cdiv(rows, kQBlock) * nb;
+  if (grid > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
+  int dev, sms;
+  LMH_TRY(current_device(&dev, &sms));
+  if (rows == 0) return LMH_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  ProfScope ps(KID_QUANTIZE, st);
+  if (block_rows == 1)
+    quantize_rows_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(
+        rows, static_cast<int>(d), reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(q), scale);
+  else
+    quantize_blocks_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(
+        rows, static_cast<int>(d), reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(q), scale);
+  return last_launch();
+}

@@ -1,6 +1,7 @@
 // lmh_api.cu — the C ABI of include/lmh.h, one translation unit: the shared host code
 // (api_common.cuh: checks, plan, launches), the single-device entries below, the
-// vocabulary-parallel entries (api_vp.cuh) and the allocation-free entry (api_noalloc.cuh).
+// vocabulary-parallel entries (api_vp.cuh), the allocation-free entry (api_noalloc.cuh) and the
+// entries around the head (api_serve.cuh).
 // Nothing here allocates device memory or waits for the device (except lmh_read_errors,
 // whose job is to).
 #include <cuda.h>
@@ -17,6 +18,7 @@
 #include "sparse.cuh"
 #include "vp.cuh"
 #include "peer.cuh"
+#include "norm.cuh"
 
 using namespace lmh;
 
@@ -25,7 +27,8 @@ using namespace lmh;
 // ============================================================================ C ABI
 
 extern "C" size_t lmh_workspace_size(const lmh_shape* shape, int entry) {
-  if (!shape_ok(shape) || entry < LMH_ENTRY_LOSS_FWD || entry > LMH_ENTRY_VP_SUPPORT_BWD) return 0;
+  if (!shape_ok(shape) || entry < LMH_ENTRY_LOSS_FWD || entry > LMH_ENTRY_RMS_NORM_BWD) return 0;
+  if (entry == LMH_ENTRY_RMS_NORM_BWD) return norm_bwd_bytes(shape->N, shape->d);
   if ((entry == LMH_ENTRY_SUPPORT_LOGPROB || entry == LMH_ENTRY_SUPPORT_KL ||
        entry == LMH_ENTRY_VP_SUPPORT_PARTIALS || entry == LMH_ENTRY_VP_SUPPORT_COMBINE ||
        entry == LMH_ENTRY_VP_SUPPORT_BWD) &&
@@ -542,3 +545,4 @@ extern "C" const char* lmh_kernel_name(int kernel_id) {
 }
 
 #include "api_noalloc.cuh"
+#include "api_serve.cuh"

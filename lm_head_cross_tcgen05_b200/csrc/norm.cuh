@@ -1,0 +1,333 @@
+// norm.cuh — the final RMS norm with the residual's addition (bf16 output, or e4m3 with one scale
+// per row and 128 columns), its backward pass, and the e4m3 quantisation of matrices by blocks.
+// All are HBM bound: each row is held in registers between its two uses, so every tensor crosses
+// memory once. Sums are fp32 in a fixed order (a thread's elements in ascending order, then a
+// butterfly over the warp, then the warps in ascending order): no result depends on the device.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "rowops.cuh"
+
+namespace lmh {
+
+constexpr int kNormMaxD = 16384;   // 512 threads x 4 vectors of 8
+constexpr int kQBlock = 128;       // columns per scale
+constexpr float kE4m3Max = 448.f;
+constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
+
+// Bits of |x|: as unsigned numbers they order like the values, with NaN above everything, so an
+// integer maximum propagates a NaN into the block's scale.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Scale of a block whose largest magnitude has these bits: max(amax, 2^-100) / 448. The floor
+// keeps the scale and its reciprocal normal numbers, for a block of zeros too.
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+  const float a = __uint_as_float(amax_bits);
+  return (a < kAmaxFloor ? kAmaxFloor : a) / kE4m3Max;  // NaN stays NaN
+}
+
+// Eight values over the scale, rounded to nearest even e4m3 (saturating; NaN stays NaN). The
+// division is exact to half a step, so a block's largest value always becomes 448.
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float scale) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(y[4 * h], scale), __fdiv_rn(y[4 * h + 1], scale)), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
+        make_float2(__fdiv_rn(y[4 * h + 2], scale), __fdiv_rn(y[4 * h + 3], scale)), __NV_SATFINITE, __NV_E4M3);
+    w[h] = static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack_bf16x2(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                    pack_bf16x2(f[6], f[7]));
+}
+
+// Sum over the blockDim.x threads of this threadIdx.y (whole warps): every thread gets it.
+__device__ __forceinline__ float row_sum(float x, float* sh) {
+  x = warp_sum(x);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return x;
+  float* s = sh + threadIdx.y * 32;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+  __syncthreads();
+  float t = 0.f;
+  for (int w = 0; w < warps; ++w) t += s[w];
+  return t;
+}
+
+struct NormParams {
+  long long N;
+  int d;
+  float eps;
+  const uint4* x;
+  const uint4* residual;  // or null
+  const uint4* weight;
+  uint4* sum;      // or null; may be x or residual
+  uint4* y;        // or null
+  uint2* q;        // or null
+  float* scale;    // [N, ceil(d / 128)], with q
+  float* rstd;     // or null
+};
+
+// One row per threadIdx.y, VPT vectors of 8 per thread at v = threadIdx.x + j * blockDim.x. The
+// sum is rounded to bf16 before the norm: the norm is that of the stream as it is stored, which
+// is what the backward pass and a next layer read. A scale's 16 vectors lie in 16 adjacent lanes
+// (blockDim.x is a multiple of 32), so the block's maximum is four shuffles.
+template <int VPT>
+__global__ void __launch_bounds__(512) rms_norm_kernel(const NormParams p) {
+  __shared__ float sh[4 * 32];
+  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool live = row < p.N;
+  const int nv = p.d >> 3;
+  const long long base = row * nv;
+  uint4 s[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    s[j] = (live && v < nv) ? __ldcs(p.x + base + v) : make_uint4(0, 0, 0, 0);
+  }
+  if (p.residual) {
+    uint4 r[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      r[j] = (live && v < nv) ? __ldcs(p.residual + base + v) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float a[8], b[8];
+      unpack8(s[j], a);
+      unpack8(r[j], b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] += b[e];
+      s[j] = pack8(a);
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    float a[8];
+    unpack8(s[j], a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
+  }
+  ss = row_sum(ss, sh);
+  const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
+  if (live && p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  const int nb = (p.d + kQBlock - 1) / kQBlock;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    const bool in = live && v < nv;
+    float a[8], w[8];
+    unpack8(s[j], a);
+    unpack8(in ? __ldg(p.weight + v) : make_uint4(0, 0, 0, 0), w);
+    if (in && p.sum) p.sum[base + v] = s[j];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = in ? a[e] * rstd * w[e] : 0.f;
+    if (in && p.y) p.y[base + v] = pack8(a);
+    if (p.q) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float sc = block_scale(m);
+      if (in) {
+        p.q[base + v] = to_e4m3x8(a, sc);
+        if ((v & 15) == 0) p.scale[row * nb + (v >> 4)] = sc;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- backward
+// With n = r rstd and c = mean(w dy n):  dx = rstd (w dy - n c) + dsum,  dw = sum_rows dy n.
+// Slice blockIdx.x of the rows, one row at a time; a thread keeps its columns' share of dw in
+// registers over the slice and leaves it in part[slice]. The slices depend on N alone.
+constexpr int kNormSlices = 592;  // four blocks of 512 threads on each of 148 SMs
+
+struct NormBwdParams {
+  long long N;
+  int d, slices;
+  const uint4* sum;
+  const uint4* weight;
+  const float* rstd;
+  const uint4* dy;
+  const uint4* dsum;  // or null
+  uint4* dx;          // or null; may be dy or dsum
+  float* part;        // [slices, d], or null
+  WsHeader* h;
+};
+
+template <int VPT>
+__global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const NormBwdParams p) {
+  __shared__ float sh[2][32];
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.h->err = 0;
+  const int nv = p.d >> 3;
+  const long long r0 = p.N * blockIdx.x / p.slices, r1 = p.N * (blockIdx.x + 1) / p.slices;
+  float acc[VPT][8] = {};
+  uint4 w[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    w[j] = v < nv ? __ldg(p.weight + v) : make_uint4(0, 0, 0, 0);
+  }
+  int flip = 0;
+  for (long long row = r0; row < r1; ++row, flip ^= 1) {
+    const long long base = row * nv;
+    const float rstd = p.rstd[row];
+    uint4 s[VPT], g[VPT], t[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      s[j] = g[j] = t[j] = make_uint4(0, 0, 0, 0);
+      if (v < nv) {
+        s[j] = __ldcs(p.sum + base + v);
+        g[j] = __ldcs(p.dy + base + v);
+        if (p.dsum) t[j] = __ldcs(p.dsum + base + v);
+      }
+    }
+    float c = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      float n[8], dy[8], wf[8];
+      unpack8(s[j], n);
+      unpack8(g[j], dy);
+      unpack8(w[j], wf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float dn = dy[e] * (n[e] * rstd);
+        c = fmaf(wf[e], dn, c);
+        acc[j][e] += dn;
+      }
+    }
+    if (!p.dx) continue;
+    c = row_sum(c, sh[flip]) / static_cast<float>(p.d);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      if (v >= nv) continue;
+      float n[8], dy[8], wf[8], ds[8];
+      unpack8(s[j], n);
+      unpack8(g[j], dy);
+      unpack8(w[j], wf);
+      unpack8(t[j], ds);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        ds[e] = fmaf(rstd, wf[e] * dy[e] - n[e] * rstd * c, ds[e]);
+      p.dx[base + v] = pack8(ds);
+    }
+  }
+  if (!p.part) return;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    if (v >= nv) continue;
+    float4* o = reinterpret_cast<float4*>(p.part + static_cast<long long>(blockIdx.x) * p.d + v * 8);
+    o[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+    o[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+  }
+}
+
+// dweight = bf16(sum over the slices): 32 columns per block, threadIdx.y sums every 16th slice in
+// ascending order, then the 16 sums are added in ascending order.
+__global__ void __launch_bounds__(512) norm_dweight_kernel(int slices, int d,
+                                                           const float* __restrict__ part,
+                                                           __nv_bfloat16* __restrict__ dweight) {
+  __shared__ float sh[16][32];
+  const int c = blockIdx.x * 32 + threadIdx.x;  // d is a multiple of 64
+  float a = 0.f;
+  for (int s = threadIdx.y; s < slices; s += 16) a += part[static_cast<long long>(s) * d + c];
+  sh[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.y != 0) return;
+  a = 0.f;
+  for (int i = 0; i < 16; ++i) a += sh[i][threadIdx.x];
+  dweight[c] = __float2bfloat16_rn(a);
+}
+
+// ---------------------------------------------------------------------------- quantisation
+// One scale per row and 128 columns: 16 adjacent lanes hold a block.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(long long rows, int d,
+                                                            const uint4* __restrict__ x,
+                                                            uint2* __restrict__ q,
+                                                            float* __restrict__ scale) {
+  const int nb = (d + kQBlock - 1) / kQBlock, nv = d >> 3;
+  const long long blk = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
+  const long long row = blk / nb;
+  const int b = static_cast<int>(blk - row * nb);
+  const int v = b * 16 + (threadIdx.x & 15);
+  const bool in = row < rows && v < nv;
+  float a[8];
+  unpack8(in ? __ldcs(x + row * nv + v) : make_uint4(0, 0, 0, 0), a);
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!in) return;
+  const float sc = block_scale(m);
+  q[row * nv + v] = to_e4m3x8(a, sc);
+  if ((threadIdx.x & 15) == 0) scale[row * nb + b] = sc;
+}
+
+// One scale per 128 x 128 block, one block of threads each: 16 lanes per row, 8 rows a thread.
+__global__ void __launch_bounds__(256) quantize_blocks_kernel(long long rows, int d,
+                                                              const uint4* __restrict__ x,
+                                                              uint2* __restrict__ q,
+                                                              float* __restrict__ scale) {
+  __shared__ uint32_t sh[8];
+  const int nb = (d + kQBlock - 1) / kQBlock, nv = d >> 3;
+  const long long rb = blockIdx.x / nb;
+  const int b = static_cast<int>(blockIdx.x - rb * nb);
+  const int v = b * 16 + (threadIdx.x & 15);
+  const long long r0 = rb * kQBlock + (threadIdx.x >> 4);
+  uint4 t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const long long r = r0 + 16 * i;
+    t[i] = (r < rows && v < nv) ? __ldcs(x + r * nv + v) : make_uint4(0, 0, 0, 0);
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float a[8];
+    unpack8(t[i], a);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = max(m, sh[w]);
+  const float sc = block_scale(m);
+  if (threadIdx.x == 0) scale[rb * nb + b] = sc;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const long long r = r0 + 16 * i;
+    if (r < rows && v < nv) {
+      float a[8];
+      unpack8(t[i], a);
+      q[r * nv + v] = to_e4m3x8(a, sc);
+    }
+  }
+}
+
+}  // namespace lmh

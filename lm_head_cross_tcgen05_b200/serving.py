@@ -1,0 +1,159 @@
+"""The entries around the head: the RMS norm that makes its input (with its backward pass) and the
+8-bit quantisation of both operands.
+
+As in the package's root, ``lmh_*`` mirror the C ABI on tensors that the caller allocated, and the
+lower-case helpers allocate the outputs. All tensors of a call are on one CUDA device, which need
+not be the current one; the work runs on that device's current stream, or on ``stream``, on which
+a helper then allocates its outputs too. Nothing synchronises the host.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import (ENTRY_RMS_NORM_BWD, _bf, _f32, _ok, _p, _u8, lmh_workspace_size, make_shape)
+from ._abi import lib
+
+__all__ = ["lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8", "rms_norm", "rms_norm_bwd",
+           "quantize_fp8"]
+
+_e4m3 = torch.float8_e4m3fn
+QBLOCK = 128  # columns (and, for a weight, rows) per scale
+
+
+def _blocks(n: int) -> int:
+    return -(-int(n) // QBLOCK)
+
+
+def _shaped(**named) -> None:
+    """Each named (tensor, shape): the tensor, when given, has exactly that shape."""
+    for what, (t, shape) in named.items():
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _matrix(t, what: str):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be a matrix, got {t.dim()} dimensions")
+    return t.shape
+
+
+def _call(name: str, tensors, stream, *args) -> None:
+    """lib().name(*args, stream) with the tensors' device current."""
+    dev = None
+    for t in tensors:
+        if t is not None:
+            if dev is not None and t.device != dev:
+                raise ValueError(f"{name}: tensors on {dev} and {t.device}")
+            dev = t.device
+    if stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    elif hasattr(stream, "cuda_stream"):
+        if stream.device != dev:
+            raise ValueError(f"{name}: a stream of {stream.device} for tensors on {dev}")
+        raw = stream.cuda_stream
+    else:
+        raw = int(stream)
+    f = getattr(lib(), name)
+    if dev.index == torch.cuda.current_device():
+        st = f(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, raw)
+    _ok(name, st)
+
+
+def _allocating(stream, device):
+    """Outputs of a helper belong to the stream that writes them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def lmh_rms_norm(x, weight, residual=None, *, eps, sum=None, y=None, q=None, scale=None,
+                 rstd=None, stream=None) -> None:
+    N, d = _matrix(x, "x")
+    _shaped(weight=(weight, (d,)), residual=(residual, (N, d)), sum=(sum, (N, d)), y=(y, (N, d)),
+            q=(q, (N, d)), scale=(scale, (N, _blocks(d))), rstd=(rstd, (N,)))
+    _call("lmh_rms_norm", (x, weight, residual, sum, y, q, scale, rstd), stream, N, d,
+          _p(x, _bf, "x"), _p(residual, _bf, "residual"), _p(weight, _bf, "weight"), float(eps),
+          _p(sum, _bf, "sum"), _p(y, _bf, "y"), _p(q, _e4m3, "q"), _p(scale, _f32, "scale"),
+          _p(rstd, _f32, "rstd"))
+
+
+def lmh_rms_norm_bwd(sum, weight, rstd, dy, dsum=None, dx=None, dweight=None, *, workspace,
+                     stream=None) -> None:
+    N, d = _matrix(sum, "sum")
+    _shaped(weight=(weight, (d,)), rstd=(rstd, (N,)), dy=(dy, (N, d)), dsum=(dsum, (N, d)),
+            dx=(dx, (N, d)), dweight=(dweight, (d,)))
+    _call("lmh_rms_norm_bwd", (sum, weight, rstd, dy, dsum, dx, dweight, workspace), stream, N, d,
+          _p(sum, _bf, "sum"), _p(weight, _bf, "weight"), _p(rstd, _f32, "rstd"),
+          _p(dy, _bf, "dy"), _p(dsum, _bf, "dsum"), _p(dx, _bf, "dx"),
+          _p(dweight, _bf, "dweight"), _p(workspace, _u8, "workspace"), workspace.numel())
+
+
+def lmh_quantize_fp8(x, q, scale, block_rows: int, *, stream=None) -> None:
+    rows, d = _matrix(x, "x")
+    if block_rows not in (1, QBLOCK):
+        raise ValueError(f"block_rows must be 1 or {QBLOCK}, got {block_rows}")
+    _shaped(q=(q, (rows, d)), scale=(scale, (-(-rows // block_rows), _blocks(d))))
+    _call("lmh_quantize_fp8", (x, q, scale), stream, rows, d, int(block_rows), _p(x, _bf, "x"),
+          _p(q, _e4m3, "q"), _p(scale, _f32, "scale"))
+
+
+def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, fp8: bool = False,
+             keep_sum: bool = True, stream=None) -> dict:
+    """The RMS norm of x + residual over rows of d: ``y`` (bf16) with ``rstd`` for the backward
+    pass, or with fp8=True ``q`` (e4m3) and ``scale`` [N, ceil(d / 128)]. ``sum``: the stream
+    x + residual as bf16 (x itself without a residual; None with keep_sum=False)."""
+    N, d = _matrix(x, "x")
+    dev = x.device
+    out = {}
+    with _allocating(stream, dev):
+        if fp8:
+            out["q"] = torch.empty(N, d, dtype=_e4m3, device=dev)
+            out["scale"] = torch.empty(N, _blocks(d), dtype=_f32, device=dev)
+        else:
+            out["y"] = torch.empty(N, d, dtype=_bf, device=dev)
+            out["rstd"] = torch.empty(N, dtype=_f32, device=dev)
+        new = keep_sum and residual is not None
+        out["sum"] = torch.empty(N, d, dtype=_bf, device=dev) if new else None
+    lmh_rms_norm(x, weight, residual, eps=eps, stream=stream, **out)
+    if keep_sum and residual is None:
+        out["sum"] = x
+    return out
+
+
+def rms_norm_bwd(sum, weight, rstd, dy, dsum=None, *, want_dx: bool = True,
+                 want_dweight: bool = True, ws=None, stream=None) -> dict:
+    """Gradients of rms_norm from its ``sum`` and ``rstd``: ``dx`` (of x and of residual alike;
+    dsum is the gradient that reaches the sum itself) and ``dweight``, both bf16."""
+    N, d = _matrix(sum, "sum")
+    dev = sum.device
+    with _allocating(stream, dev):
+        out = dict(dx=torch.empty(N, d, dtype=_bf, device=dev) if want_dx else None,
+                   dweight=torch.empty(d, dtype=_bf, device=dev) if want_dweight else None)
+        if ws is None:
+            n = lmh_workspace_size(make_shape(N, d, 1), ENTRY_RMS_NORM_BWD)
+            if n == 0:
+                raise ValueError("invalid shape for this entry")
+            ws = torch.empty(n, dtype=_u8, device=dev)
+    lmh_rms_norm_bwd(sum, weight, rstd, dy, dsum, out["dx"], out["dweight"], workspace=ws,
+                     stream=stream)
+    return out
+
+
+def quantize_fp8(x, block_rows: int = QBLOCK, *, stream=None):
+    """(q, scale): x [rows, d] bf16 as e4m3 with one fp32 scale per block of block_rows x 128
+    (128 for a weight, laid out once; 1 for hidden states)."""
+    rows, d = _matrix(x, "x")
+    if block_rows not in (1, QBLOCK):
+        raise ValueError(f"block_rows must be 1 or {QBLOCK}, got {block_rows}")
+    with _allocating(stream, x.device):
+        q = torch.empty(rows, d, dtype=_e4m3, device=x.device)
+        scale = torch.empty(-(-rows // block_rows), _blocks(d), dtype=_f32, device=x.device)
+    lmh_quantize_fp8(x, q, scale, block_rows, stream=stream)
+    return q, scale

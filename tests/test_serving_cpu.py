@@ -1,0 +1,72 @@
+"""Refusals of the entries around the head, found on the host before any CUDA call (CPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import lm_head_cross_tcgen05_b200 as L
+from lm_head_cross_tcgen05_b200._abi import lib
+
+INVALID, SHORT, ALIGN = 1, 3, 4
+P = 4096  # a pointer that no refused call follows
+
+
+def norm(N=1, d=64, x=P, residual=None, weight=P, eps=1e-6, sum=None, y=P, q=None, scale=None, rstd=None):
+    return lib().lmh_rms_norm(N, d, x, residual, weight, eps, sum, y, q, scale, rstd, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(d=0), INVALID), (dict(d=96), INVALID), (dict(d=16448), INVALID), (dict(N=-1), INVALID), (dict(N=2 ** 31), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(eps=float("inf")), INVALID),
+    (dict(y=None), INVALID), (dict(q=P), INVALID), (dict(scale=P), INVALID), (dict(x=None), INVALID), (dict(weight=None), INVALID),
+    (dict(x=P + 2), ALIGN), (dict(residual=P + 8), ALIGN), (dict(y=P + 2), ALIGN), (dict(q=P + 8, scale=P), ALIGN),
+    (dict(q=P, scale=P + 2), ALIGN), (dict(rstd=P + 1), ALIGN), (dict(sum=P + 4), ALIGN), (dict(weight=P + 2), ALIGN)])
+def test_norm_refuses(kw, status):
+    assert norm(**kw) == status
+
+
+def norm_bwd(N=1, d=64, sum=P, weight=P, rstd=P, dy=P, dsum=None, dx=P, dweight=P, ws=P, n=1 << 20):
+    return lib().lmh_rms_norm_bwd(N, d, sum, weight, rstd, dy, dsum, dx, dweight, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(d=65), INVALID), (dict(N=-1), INVALID), (dict(dx=None, dweight=None), INVALID), (dict(ws=None), INVALID),
+    (dict(sum=None), INVALID), (dict(dy=None), INVALID), (dict(rstd=None), INVALID), (dict(weight=None), INVALID),
+    (dict(dsum=P + 2), ALIGN), (dict(ws=P + 16), ALIGN), (dict(rstd=P + 2), ALIGN), (dict(n=511), SHORT),
+    (dict(N=10 ** 6, d=16384, n=592 * 16384 * 4), SHORT)])
+def test_norm_bwd_refuses(kw, status):
+    assert norm_bwd(**kw) == status
+
+
+def test_norm_bwd_workspace():
+    def ws(N, d):
+        return L.lmh_workspace_size(L.make_shape(N, d, 1), L.ENTRY_RMS_NORM_BWD)
+    assert ws(1, 64) == 512 and ws(0, 64) == 256
+    assert ws(592, 4096) == ws(10 ** 6, 4096) == 256 + 592 * 4096 * 4
+    assert ws(1, 16448) == 0 and ws(2 ** 31, 64) == 0
+
+
+@pytest.mark.parametrize("args,status", [
+    ((1, 96, 1, P, P, P), INVALID), ((-1, 64, 1, P, P, P), INVALID), ((1, 64, 64, P, P, P), INVALID), ((1, 64, 0, P, P, P), INVALID),
+    ((1, 64, 1, None, P, P), INVALID), ((1, 64, 1, P, None, P), INVALID), ((1, 64, 1, P, P, None), INVALID),
+    ((2 ** 31 - 1, 2 ** 24, 1, P, P, P), INVALID), ((1, 64, 1, P + 8, P, P), ALIGN), ((1, 64, 1, P, P + 8, P), ALIGN),
+    ((1, 64, 1, P, P, P + 2), ALIGN)])
+def test_quantize_refuses(args, status):
+    assert lib().lmh_quantize_fp8(*args, None) == status
+
+
+def test_python_refuses():
+    b = torch.bfloat16
+    x, w = torch.zeros(2, 64, dtype=b), torch.zeros(64, dtype=b)
+    with pytest.raises(ValueError, match="matrix"):
+        L.rms_norm(x[0], w)
+    with pytest.raises(ValueError, match="weight must have shape"):
+        L.rms_norm(x, w[:32])
+    with pytest.raises(ValueError, match="residual must have shape"):
+        L.rms_norm(x, w, x[:1])
+    with pytest.raises(ValueError, match="CUDA"):
+        L.rms_norm(x, w)
+    with pytest.raises(ValueError, match="block_rows"):
+        L.quantize_fp8(x, 64)
+    with pytest.raises(ValueError, match="rstd must have shape"):
+        L.rms_norm_bwd(x, w, torch.zeros(3), x)
