@@ -96,12 +96,17 @@ typedef enum lmh_status {
 #define LMH_ENTRY_VP_SUPPORT_COMBINE 10
 #define LMH_ENTRY_VP_SUPPORT_BWD 11
 #define LMH_ENTRY_RMS_NORM_BWD 12 /* reads N and d of the shape */
+#define LMH_ENTRY_FP8_LOGITS 13   /* reads N, d and V */
 
 /* objectives of lmh_loss_bwd */
 #define LMH_BWD_CE 0              /* L = sum_i g_i loss_i                                */
 #define LMH_BWD_LOGPROB 1         /* L = sum_i g_i logprob_i                             */
 #define LMH_BWD_SUPPORT_LOGPROB 2 /* L = sum_ik g_ik lp_ik                               */
 #define LMH_BWD_SUPPORT_KL 3      /* L = sum_i g_i KL_i                                  */
+
+/* element types of logits */
+#define LMH_DTYPE_F32 0
+#define LMH_DTYPE_BF16 1
 
 #define LMH_MAX_K 1024 /* largest candidate count per row of the support entries */
 
@@ -560,6 +565,19 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *
  * lmh_quantize_fp8 — x [rows, d] bf16 as an 8-bit matrix q, scale with blocks of block_rows x 128
  * (block_rows 1 or 128). No workspace.
+ *
+ * lmh_fp8_logits — the logits of 8-bit hidden states and an 8-bit weight,
+ *   z_nv = sum_b h_scale[n, b] w_scale[v / 128, b] sum_{k in block b} H8[n, k] W8[v, k],
+ * b over blocks of 128 columns: each block's products are summed on the tensor cores, times its
+ * scale added in fp32 in ascending b, and the logit rounded once to its type. The value of a
+ * logit depends on N (few or many rows are summed by different kernels) but not on the device.
+ *   H8 [N, d] and h_scale [N, ceil(d / 128)] as lmh_rms_norm or lmh_quantize_fp8 (block_rows 1)
+ *   gives them; W8 [V, d] and w_scale [ceil(V / 128), ceil(d / 128)] as lmh_quantize_fp8
+ *   (block_rows 128) does, once per weight. logits [N, V] out, row-major and contiguous, of type
+ *   dtype (LMH_DTYPE_F32 or LMH_DTYPE_BF16), aligned to its element. shape: N < 2^31, d, V; the
+ *   temperature is not applied. These are the only logits this library stores: they are for the
+ *   rows that a token is drawn from or that are looked at, not for a training batch.
+ *   Workspace: lmh_workspace_size(shape, LMH_ENTRY_FP8_LOGITS).
  */
 LMH_API lmh_status lmh_rms_norm(int64_t N, int64_t d, const lmh_bf16* x,
                                 const lmh_bf16* residual, const lmh_bf16* weight, float eps,
@@ -572,6 +590,10 @@ LMH_API lmh_status lmh_rms_norm_bwd(int64_t N, int64_t d, const lmh_bf16* sum,
                                     void* stream);
 LMH_API lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_rows,
                                     const lmh_bf16* x, uint8_t* q, float* scale, void* stream);
+LMH_API lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
+                                  const float* h_scale, const uint8_t* W8, const float* w_scale,
+                                  void* logits, int32_t dtype, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * lmh_read_errors — synchronises `stream`, then copies the device error word of the last

@@ -24,7 +24,8 @@ F_DW_ACC_STORE = 0x20
 ENTRY_LOSS_FWD, ENTRY_LOSS_BWD, ENTRY_LOGPROB, ENTRY_SUPPORT_LOGPROB, ENTRY_SUPPORT_KL = range(5)
 ENTRY_VP_PARTIALS, ENTRY_VP_COMBINE, ENTRY_VP_BWD, ENTRY_LOSS_FWD_BWD = 5, 6, 7, 8
 ENTRY_VP_SUPPORT_PARTIALS, ENTRY_VP_SUPPORT_COMBINE, ENTRY_VP_SUPPORT_BWD = 9, 10, 11
-ENTRY_RMS_NORM_BWD = 12
+ENTRY_RMS_NORM_BWD, ENTRY_FP8_LOGITS = 12, 13
+DTYPE_F32, DTYPE_BF16 = 0, 1
 BWD_CE, BWD_LOGPROB, BWD_SUPPORT_LOGPROB, BWD_SUPPORT_KL = range(4)
 MAX_K = 1024
 
@@ -75,6 +76,8 @@ _SIGS = {
     "lmh_rms_norm": (c_int, [c_int64, c_int64] + [_P] * 3 + [ctypes.c_float] + [_P] * 6),
     "lmh_rms_norm_bwd": (c_int, [c_int64, c_int64] + [_P] * 8 + [c_size_t, _P]),
     "lmh_quantize_fp8": (c_int, [c_int64, c_int64, ctypes.c_int32] + [_P] * 4),
+    "lmh_fp8_logits": (c_int, [ctypes.POINTER(lmh_shape)] + [_P] * 5
+                       + [ctypes.c_int32, _P, c_size_t, _P]),
     "lmh_read_errors": (c_int, [_P, ctypes.POINTER(c_uint32), _P]),
     "lmh_logprob_noalloc": (c_int, [ctypes.POINTER(lmh_shape)] + [_P] * 6),
     "lmh_peer_barrier": (c_int, [_P, _P, ctypes.c_int32, ctypes.c_int32, c_uint32, c_uint32, _P]),

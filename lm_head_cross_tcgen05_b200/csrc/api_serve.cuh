@@ -129,3 +129,108 @@ extern "C" lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_ro
         rows, static_cast<int>(d), reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(q), scale);
   return last_launch();
 }
+
+namespace {
+
+// 8-bit [outer, inner] matrix; box {128, box_outer}, 128-byte swizzle, zero fill out of bounds.
+bool tmap_8bit(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint32_t box_outer) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner};
+  cuuint32_t box[2] = {kFpK, box_outer};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Shared memory above the default has to be asked for once per kernel and device.
+template <class K>
+lmh_status allow_smem(K kernel, int bytes, int dev, std::atomic<uint64_t>* done) {
+  const uint64_t bit = 1ull << dev;
+  if (done->load() & bit) return LMH_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return LMH_ERR_CUDA;
+  done->fetch_or(bit);
+  return LMH_OK;
+}
+
+template <int TN, class Out>
+lmh_status launch_few(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t d, int dev, int sms,
+                      cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  LMH_TRY(allow_smem(fp8_few_kernel<TN, Out>, FpFew<TN>::SMEM, dev, &done));
+  CUtensorMap tw, th;
+  if (!tmap_8bit(&tw, W8, d, p.V, kFpM) || !tmap_8bit(&th, H8, d, p.N, TN)) return LMH_ERR_CUDA;
+  p.vtiles = static_cast<int>(cdiv(p.V, kFpM));
+  p.ntiles = static_cast<int>(cdiv(p.N, TN));
+  const int64_t tiles = static_cast<int64_t>(p.vtiles) * p.ntiles;
+  if (tiles > 0x7fff0000LL) return LMH_ERR_INVALID_ARG;
+  ProfScope ps(KID_FP8_LOGITS, st);
+  fp8_few_kernel<TN, Out><<<static_cast<unsigned>(tiles < sms ? tiles : sms), FpFew<TN>::THREADS,
+                            FpFew<TN>::SMEM, st>>>(tw, th, p);
+  return last_launch();
+}
+
+template <class Out>
+lmh_status launch_many(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t d, int dev, int sms,
+                       cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  LMH_TRY(allow_smem(fp8_many_kernel<Out>, FpMany::SMEM, dev, &done));
+  CUtensorMap tw, th;
+  if (!tmap_8bit(&tw, W8, d, p.V, FpMany::TV) || !tmap_8bit(&th, H8, d, p.N, kFpM))
+    return LMH_ERR_CUDA;
+  p.vtiles = static_cast<int>(cdiv(p.V, FpMany::TV));
+  p.ntiles = static_cast<int>(cdiv(p.N, kFpM));
+  const int64_t tiles = static_cast<int64_t>(p.vtiles) * p.ntiles;
+  if (tiles > 0x7fff0000LL) return LMH_ERR_INVALID_ARG;
+  ProfScope ps(KID_FP8_LOGITS, st);
+  fp8_many_kernel<Out><<<static_cast<unsigned>(tiles < sms ? tiles : sms), FpMany::THREADS,
+                         FpMany::SMEM, st>>>(tw, th, p);
+  return last_launch();
+}
+
+template <class Out>
+lmh_status launch_fp8(const FpParams& p, const uint8_t* H8, const uint8_t* W8, int64_t d, int dev,
+                      int sms, cudaStream_t st) {
+  if (p.N <= 16) return launch_few<16, Out>(p, H8, W8, d, dev, sms, st);
+  if (p.N <= 32) return launch_few<32, Out>(p, H8, W8, d, dev, sms, st);
+  if (p.N <= 64) return launch_few<64, Out>(p, H8, W8, d, dev, sms, st);
+  return launch_many<Out>(p, H8, W8, d, dev, sms, st);
+}
+
+}  // namespace
+
+extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
+                                     const float* h_scale, const uint8_t* W8,
+                                     const float* w_scale, void* logits, int32_t dtype,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (!shape_ok(shape) || shape->N > 0x7fffffffLL ||
+      (dtype != LMH_DTYPE_F32 && dtype != LMH_DTYPE_BF16) || !workspace)
+    return LMH_ERR_INVALID_ARG;
+  if (shape->N > 0 && (!H8 || !h_scale || !W8 || !w_scale || !logits)) return LMH_ERR_INVALID_ARG;
+  const uintptr_t esize = dtype == LMH_DTYPE_F32 ? 4 : 2;
+  if (!aligned16(H8) || !aligned16(W8) || !aligned4(h_scale) || !aligned4(w_scale) ||
+      (reinterpret_cast<uintptr_t>(logits) & (esize - 1)) != 0 ||
+      (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+    return LMH_ERR_ALIGNMENT;
+  if (workspace_bytes < lmh_workspace_size(shape, LMH_ENTRY_FP8_LOGITS))
+    return LMH_ERR_WORKSPACE_TOO_SMALL;
+  int dev, sms;
+  LMH_TRY(current_device(&dev, &sms));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Ws ws{static_cast<uint8_t*>(workspace), static_cast<WsHeader*>(workspace)};
+  LMH_TRY(clear_header(ws, st));
+  if (shape->N == 0) return LMH_OK;
+  FpParams p{};
+  p.N = shape->N;
+  p.V = shape->V;
+  p.nb = static_cast<int>(cdiv(shape->d, kFpK));
+  p.hs = h_scale;
+  p.ws = w_scale;
+  p.out = logits;
+  p.err = &ws.h->err;
+  return dtype == LMH_DTYPE_F32 ? launch_fp8<float>(p, H8, W8, shape->d, dev, sms, st)
+                                : launch_fp8<__nv_bfloat16>(p, H8, W8, shape->d, dev, sms, st);
+}

@@ -1,0 +1,401 @@
+// fp8.cuh — the 8-bit logits product on the tensor cores:
+//   z[n, v] = sum_b hs[n, b] ws[v / 128, b] sum_{k in block b} H8[n, k] W8[v, k]
+// with b over blocks of 128 columns. The scales are general fp32 numbers, so they cannot ride on
+// the MMA: each block of 128 columns (four tcgen05.mma kind::f8f6f4 steps of K = 32) goes into a
+// fresh TMEM accumulator, which the epilogue warps read and add, times its scale, into fp32
+// registers while the next block's MMAs fill another one. That also bounds what the tensor core
+// itself accumulates to 128 terms.
+//
+// Two kernels, by which operand takes the accumulator's 128 lanes:
+//  * few tokens (decode): W8 is the A operand (128 vocabulary rows, one scale of ws each) and H8
+//    the B operand (TN = 16, 32 or 64 tokens), so the tensor core wastes no rows on a few tokens,
+//    and an epilogue warp writes 32 adjacent logits of one token with each store.
+//  * many tokens: H8 is A (128 tokens) and W8 is B (256 vocabulary rows), so a thread's scales
+//    are one hs and two ws per block, held in registers, and its accumulator row is one token's.
+//
+// Roles (per CTA): warp 0 lane 0 loads the operands with TMA; warp 1 lane 0 issues the MMAs; the
+// other warps scale and add. Every wait is bounded; no warp waits for another except on those
+// mbarriers and at the end.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "sm100.cuh"
+
+namespace lmh {
+
+constexpr int kFpK = 128;  // columns per scale block and per stage
+constexpr int kFpM = 128;  // accumulator lanes
+
+template <int TN>
+struct FpFew {
+  static constexpr int THREADS = 192;
+  static constexpr int NBUF = 4;  // TMEM accumulators
+  static constexpr int TMEM = TN * NBUF;
+  static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TN * kFpK, STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = TN == 64 ? 8 : 10;
+  static constexpr int SMEM = STAGES * STAGE + 1024;
+};
+
+// kind::f8f6f4: e4m3 A and B (format 0), K-major both, fp32 accumulator.
+__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+struct FpParams {
+  long long N, V;
+  int nb;              // scale blocks per row
+  int vtiles, ntiles;  // tiles over the vocabulary and the tokens
+  const float* hs;     // [N, nb]
+  const float* ws;     // [ceil(V / 128), nb]
+  void* out;           // [N, V] fp32 or bf16
+  uint32_t* err;
+};
+
+__device__ __forceinline__ void put_logit(float* out, long long i, float x) { out[i] = x; }
+__device__ __forceinline__ void put_logit(__nv_bfloat16* out, long long i, float x) {
+  out[i] = __float2bfloat16_rn(x);
+}
+
+// The producer's last act: the loads still in flight land before the CTA may exit. `issued`
+// stages were filled in ring order.
+template <int STAGES>
+__device__ __forceinline__ void wait_loads(const uint64_t* full_bar, uint32_t issued, uint32_t* err) {
+  const uint32_t first = issued > STAGES ? issued - STAGES : 0;
+  for (uint32_t i = first; i < issued; ++i)
+    mbar_wait(smem_u32(&full_bar[i % STAGES]), (i / STAGES) & 1u, err);
+}
+
+template <int TN, class Out>
+__global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
+    fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH,
+                   const FpParams p) {
+  using C = FpFew<TN>;
+  constexpr int STAGES = C::STAGES, NBUF = C::NBUF;
+  extern __shared__ uint8_t dsmem[];
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[NBUF],
+      tempty_bar[NBUF], drain_bar;
+  __shared__ __align__(16) float sc[4][2][TN];  // per epilogue warp: the tokens' scales, two blocks
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+
+  const uint32_t smem_base = (smem_u32(dsmem) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = p.vtiles * p.ntiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(smem_u32(&tfull_bar[b]), 1);
+      mbar_init(smem_u32(&tempty_bar[b]), 4);
+    }
+    mbar_init(smem_u32(&drain_bar), 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), C::TMEM);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmW);
+      tma_prefetch_desc(&tmH);
+      uint32_t kbg = 0;
+      for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
+        const int v0 = (t / p.ntiles) * kFpM, n0 = (t % p.ntiles) * TN;
+        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+          const uint32_t s = kbg % STAGES;
+          if (!mbar_wait(smem_u32(&empty_bar[s]), ((kbg / STAGES) & 1u) ^ 1u, p.err)) {
+            abort_flag = 1;
+            break;
+          }
+          const uint32_t bar = smem_u32(&full_bar[s]), dst = smem_base + s * C::STAGE;
+          mbar_arrive_expect_tx(bar, C::STAGE);
+          tma_load_2d(dst, &tmW, bar, kb * kFpK, v0);
+          tma_load_2d(dst + C::A_BYTES, &tmH, bar, kb * kFpK, n0);
+        }
+      }
+      wait_loads<STAGES>(full_bar, kbg, p.err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc_e4m3(kFpM, TN);
+      uint32_t kbg = 0;
+      for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
+        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+          const uint32_t s = kbg % STAGES, b = kbg % NBUF;
+          if (!mbar_wait(smem_u32(&tempty_bar[b]), ((kbg / NBUF) & 1u) ^ 1u, p.err) ||
+              !mbar_wait(smem_u32(&full_bar[s]), (kbg / STAGES) & 1u, p.err)) {
+            abort_flag = 1;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = smem_base + s * C::STAGE, h = a + C::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < kFpK / 32; ++k)
+            mma_e4m3(tmem_base + b * TN, make_sw128_desc(a + k * 32, 16, 1024),
+                     make_sw128_desc(h + k * 32, 16, 1024), idesc, k != 0);
+          mma_commit(smem_u32(&empty_bar[s]));
+          mma_commit(smem_u32(&tfull_bar[b]));
+        }
+      }
+      // No MMA may still be writing TMEM when the columns are released.
+      mma_commit(smem_u32(&drain_bar));
+      mbar_wait(smem_u32(&drain_bar), 0, p.err);
+    }
+  } else {
+    constexpr int PL = (TN + 31) / 32;  // token scales per lane
+    constexpr int G = TN >= 32 ? 32 : 16;
+    const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31
+    uint32_t kbg = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const int vt = t / p.ntiles;
+      const long long n0 = static_cast<long long>(t % p.ntiles) * TN;
+      const float* ws = p.ws + static_cast<long long>(vt) * p.nb;
+      float acc[TN] = {};
+      float next[PL];
+#pragma unroll
+      for (int j = 0; j < PL; ++j) {
+        const long long n = n0 + lane + 32 * j;
+        next[j] = n < p.N ? __ldg(p.hs + n * p.nb) * __ldg(ws) : 0.f;
+      }
+      bool ok = true;
+      for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+        const uint32_t b = kbg % NBUF;
+        float* mine = sc[q][kbg & 1];  // read two blocks ago: a __syncwarp lies between
+#pragma unroll
+        for (int j = 0; j < PL; ++j) {
+          const long long n = n0 + lane + 32 * j;
+          if (lane + 32 * j < TN) mine[lane + 32 * j] = next[j];
+          if (n < p.N && kb + 1 < p.nb) next[j] = __ldg(p.hs + n * p.nb + kb + 1) * __ldg(ws + kb + 1);
+        }
+        ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TN;
+        const float4* s4 = reinterpret_cast<const float4*>(mine);
+#pragma unroll
+        for (int g = 0; g < TN; g += G) {
+          float v[G];
+          if constexpr (G == 32) tmem_ld32(taddr + g, v);
+          else tmem_ld16(taddr + g, v);
+#pragma unroll
+          for (int i = 0; i < G; i += 4) {
+            const float4 f = s4[(g + i) / 4];
+            acc[g + i] = fmaf(v[i], f.x, acc[g + i]);
+            acc[g + i + 1] = fmaf(v[i + 1], f.y, acc[g + i + 1]);
+            acc[g + i + 2] = fmaf(v[i + 2], f.z, acc[g + i + 2]);
+            acc[g + i + 3] = fmaf(v[i + 3], f.w, acc[g + i + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
+      }
+      if (!ok) {
+        abort_flag = 1;
+        break;
+      }
+      const long long v = static_cast<long long>(vt) * kFpM + q * 32 + lane;
+      if (v < p.V) {
+        Out* out = static_cast<Out*>(p.out);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+          if (n0 + i < p.N) put_logit(out, (n0 + i) * p.V + v, acc[i]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, C::TMEM);
+}
+
+// ---------------------------------------------------------------------------- many tokens
+struct FpMany {
+  static constexpr int TV = 256;          // vocabulary rows per tile
+  static constexpr int THREADS = 320;     // 8 epilogue warps: each half of the columns
+  static constexpr int NBUF = 2, TMEM = 512;
+  static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TV * kFpK, STAGE = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 4;
+  static constexpr int TRANS = 8 * 32 * 33 * 4;  // per warp: a 32 x 32 block, padded
+  static constexpr int SMEM = STAGES * STAGE + TRANS + 1024;
+};
+
+template <class Out>
+__global__ void __launch_bounds__(FpMany::THREADS, 1)
+    fp8_many_kernel(const __grid_constant__ CUtensorMap tmW,
+                    const __grid_constant__ CUtensorMap tmH, const FpParams p) {
+  using C = FpMany;
+  constexpr int STAGES = C::STAGES, NBUF = C::NBUF, TV = C::TV;
+  extern __shared__ uint8_t dsmem[];
+  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[NBUF],
+      tempty_bar[NBUF], drain_bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+
+  const uint32_t smem_base = (smem_u32(dsmem) + 1023u) & ~1023u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tiles = p.vtiles * p.ntiles;  // tokens fastest: a wave shares few tiles of W8
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(smem_u32(&tfull_bar[b]), 1);
+      mbar_init(smem_u32(&tempty_bar[b]), 8);
+    }
+    mbar_init(smem_u32(&drain_bar), 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(&tmem_slot), C::TMEM);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmW);
+      tma_prefetch_desc(&tmH);
+      uint32_t kbg = 0;
+      for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
+        const int v0 = (t / p.ntiles) * TV, n0 = (t % p.ntiles) * kFpM;
+        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+          const uint32_t s = kbg % STAGES;
+          if (!mbar_wait(smem_u32(&empty_bar[s]), ((kbg / STAGES) & 1u) ^ 1u, p.err)) {
+            abort_flag = 1;
+            break;
+          }
+          const uint32_t bar = smem_u32(&full_bar[s]), dst = smem_base + s * C::STAGE;
+          mbar_arrive_expect_tx(bar, C::STAGE);
+          tma_load_2d(dst, &tmH, bar, kb * kFpK, n0);
+          tma_load_2d(dst + C::A_BYTES, &tmW, bar, kb * kFpK, v0);
+        }
+      }
+      wait_loads<STAGES>(full_bar, kbg, p.err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = make_idesc_e4m3(kFpM, TV);
+      uint32_t kbg = 0;
+      for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
+        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+          const uint32_t s = kbg % STAGES, b = kbg % NBUF;
+          if (!mbar_wait(smem_u32(&tempty_bar[b]), ((kbg / NBUF) & 1u) ^ 1u, p.err) ||
+              !mbar_wait(smem_u32(&full_bar[s]), (kbg / STAGES) & 1u, p.err)) {
+            abort_flag = 1;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t h = smem_base + s * C::STAGE, w = h + C::A_BYTES;
+#pragma unroll
+          for (int k = 0; k < kFpK / 32; ++k)
+            mma_e4m3(tmem_base + b * TV, make_sw128_desc(h + k * 32, 16, 1024),
+                     make_sw128_desc(w + k * 32, 16, 1024), idesc, k != 0);
+          mma_commit(smem_u32(&empty_bar[s]));
+          mma_commit(smem_u32(&tfull_bar[b]));
+        }
+      }
+      mma_commit(smem_u32(&drain_bar));
+      mbar_wait(smem_u32(&drain_bar), 0, p.err);
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes 32 q .., columns 128 half ..
+    float* tr = reinterpret_cast<float*>(dsmem + (smem_base - smem_u32(dsmem)) + STAGES * C::STAGE) +
+                (warp - 2) * 32 * 33;
+    Out* out = static_cast<Out*>(p.out);
+    uint32_t kbg = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const long long v0 = static_cast<long long>(t / p.ntiles) * TV + half * 128;
+      const long long r0 = static_cast<long long>(t % p.ntiles) * kFpM + q * 32;  // warp's tokens
+      const bool row_ok = r0 + lane < p.N, col_ok = v0 < p.V;
+      const float* hs = p.hs + (row_ok ? r0 + lane : 0) * p.nb;
+      const float* ws = p.ws + (col_ok ? v0 / kFpK : 0) * p.nb;
+      float acc[128] = {};
+      float next = __ldg(hs) * __ldg(ws);
+      bool ok = true;
+      for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+        const uint32_t b = kbg % NBUF;
+        const float f = next;
+        if (kb + 1 < p.nb) next = __ldg(hs + kb + 1) * __ldg(ws + kb + 1);
+        ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr =
+            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TV + half * 128;
+#pragma unroll
+        for (int g = 0; g < 128; g += 32) {
+          float v[32];
+          tmem_ld32(taddr + g, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[g + i] = fmaf(v[i], f, acc[g + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
+      }
+      if (!ok) {
+        abort_flag = 1;
+        break;
+      }
+      // a lane holds one token's columns: turn 32 x 32 blocks so that a store's 32 lanes are
+      // adjacent columns of one token, whatever V's alignment
+#pragma unroll
+      for (int g = 0; g < 128; g += 32) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) tr[lane * 33 + i] = acc[g + i];
+        __syncwarp();
+        const long long v = v0 + g + lane;
+        if (v < p.V) {
+#pragma unroll 8
+          for (int i = 0; i < 32; ++i)
+            if (r0 + i < p.N) put_logit(out, (r0 + i) * p.V + v, tr[i * 33 + lane]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, C::TMEM);
+}
+
+}  // namespace lmh

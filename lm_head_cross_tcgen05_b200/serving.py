@@ -9,17 +9,21 @@ a helper then allocates its outputs too. Nothing synchronises the host.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 
 import torch
 
-from . import (ENTRY_RMS_NORM_BWD, _bf, _f32, _ok, _p, _u8, lmh_workspace_size, make_shape)
+from . import (DTYPE_BF16, DTYPE_F32, ENTRY_FP8_LOGITS, ENTRY_RMS_NORM_BWD, _bf, _f32, _ok, _p, _u8, lmh_workspace_size, make_shape)
 from ._abi import lib
 
-__all__ = ["lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8", "rms_norm", "rms_norm_bwd",
-           "quantize_fp8"]
+__all__ = ["lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8", "lmh_fp8_logits", "rms_norm",
+           "rms_norm_bwd", "quantize_fp8", "fp8_logits"]
 
 _e4m3 = torch.float8_e4m3fn
 QBLOCK = 128  # columns (and, for a weight, rows) per scale
+
+
+_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 
 
 def _blocks(n: int) -> int:
@@ -104,6 +108,22 @@ def lmh_quantize_fp8(x, q, scale, block_rows: int, *, stream=None) -> None:
           _p(q, _e4m3, "q"), _p(scale, _f32, "scale"))
 
 
+def _logits_dtype(t) -> int:
+    if t not in _DTYPES:
+        raise ValueError(f"logits must be torch.float32 or torch.bfloat16, got {t}")
+    return _DTYPES[t]
+
+
+def lmh_fp8_logits(shape, H8, h_scale, W8, w_scale, logits, *, workspace, stream=None) -> None:
+    N, d, V = shape.N, shape.d, shape.V
+    _shaped(H8=(H8, (N, d)), h_scale=(h_scale, (N, _blocks(d))), W8=(W8, (V, d)),
+            w_scale=(w_scale, (_blocks(V), _blocks(d))), logits=(logits, (N, V)))
+    _call("lmh_fp8_logits", (H8, h_scale, W8, w_scale, logits, workspace), stream,
+          ctypes.byref(shape), _p(H8, _e4m3, "H8"), _p(h_scale, _f32, "h_scale"),
+          _p(W8, _e4m3, "W8"), _p(w_scale, _f32, "w_scale"), _p(logits, None, "logits"),
+          _logits_dtype(logits.dtype), _p(workspace, _u8, "workspace"), workspace.numel())
+
+
 def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, fp8: bool = False,
              keep_sum: bool = True, stream=None) -> dict:
     """The RMS norm of x + residual over rows of d: ``y`` (bf16) with ``rstd`` for the backward
@@ -157,3 +177,22 @@ def quantize_fp8(x, block_rows: int = QBLOCK, *, stream=None):
         scale = torch.empty(-(-rows // block_rows), _blocks(d), dtype=_f32, device=x.device)
     lmh_quantize_fp8(x, q, scale, block_rows, stream=stream)
     return q, scale
+
+
+def fp8_logits(H8, h_scale, W8, w_scale, *, dtype=torch.float32, ws=None, stream=None) -> dict:
+    """``logits`` [N, V] (float32 or bfloat16) of 8-bit hidden states [N, d] (scales per row and
+    128 columns) and an 8-bit head weight [V, d] (scales per 128 x 128 block)."""
+    N, d = _matrix(H8, "H8")
+    V = _matrix(W8, "W8")[0]
+    _logits_dtype(dtype)
+    shape, dev = make_shape(N, d, V), H8.device
+    with _allocating(stream, dev):
+        out = dict(logits=torch.empty(N, V, dtype=dtype, device=dev))
+        if ws is None:
+            n = lmh_workspace_size(shape, ENTRY_FP8_LOGITS)
+            if n == 0:
+                raise ValueError("invalid shape for this entry")
+            ws = torch.empty(n, dtype=_u8, device=dev)
+    lmh_fp8_logits(shape, H8, h_scale, W8, w_scale, out["logits"], workspace=ws, stream=stream)
+    out["workspace"] = ws
+    return out

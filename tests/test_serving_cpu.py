@@ -70,3 +70,29 @@ def test_python_refuses():
         L.quantize_fp8(x, 64)
     with pytest.raises(ValueError, match="rstd must have shape"):
         L.rms_norm_bwd(x, w, torch.zeros(3), x)
+
+
+def logits(N=1, V=100, d=64, H8=P, hs=P, W8=P, ws=P, out=P, dtype=0, work=P, n=1 << 20):
+    shape = L.make_shape(N, d, V)
+    return lib().lmh_fp8_logits(ctypes.byref(shape), H8, hs, W8, ws, out, dtype, work, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(d=32), INVALID), (dict(V=0), INVALID), (dict(N=-1), INVALID), (dict(N=2 ** 31), INVALID), (dict(dtype=2), INVALID),
+    (dict(dtype=-1), INVALID), (dict(H8=None), INVALID), (dict(hs=None), INVALID), (dict(W8=None), INVALID), (dict(ws=None), INVALID),
+    (dict(out=None), INVALID), (dict(work=None), INVALID), (dict(H8=P + 8), ALIGN), (dict(W8=P + 8), ALIGN), (dict(hs=P + 2), ALIGN),
+    (dict(out=P + 2), ALIGN), (dict(out=P + 1, dtype=1), ALIGN), (dict(work=P + 128), ALIGN), (dict(n=255), SHORT)])
+def test_logits_refuses(kw, status):
+    assert logits(**kw) == status
+
+
+def test_logits_python_refuses():
+    e4 = torch.float8_e4m3fn
+    H, W = torch.zeros(2, 192).to(e4), torch.zeros(130, 192).to(e4)
+    hs, ws = torch.ones(2, 2), torch.ones(2, 2)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.lmh_fp8_logits(L.make_shape(2, 192, 130), H, hs, W, ws, torch.zeros(2, 130), workspace=torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="w_scale must have shape"):
+        L.lmh_fp8_logits(L.make_shape(2, 192, 130), H, hs, W, torch.ones(2, 1), torch.zeros(2, 130), workspace=torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="logits must be"):
+        L.fp8_logits(H, hs, W, ws, dtype=torch.float16)
