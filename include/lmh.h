@@ -73,6 +73,7 @@ typedef enum lmh_status {
 #define LMH_DEVERR_TIMEOUT 0x2u     /* a bounded wait inside a kernel gave up     */
 #define LMH_DEVERR_NONFINITE 0x4u   /* a row's log-sum-exp came out inf or NaN    */
 #define LMH_DEVERR_TEMPERATURE 0x8u /* a per-row temperature was not finite and > 0 (used 1) */
+#define LMH_DEVERR_SAMPLING 0x10u   /* a row's top_p or min_p was NaN, or its u not in [0, 1) */
 
 /* shape->flags */
 #define LMH_F_MEAN 0x1u         /* fused CE gradient is of the mean over valid rows    */
@@ -97,6 +98,7 @@ typedef enum lmh_status {
 #define LMH_ENTRY_VP_SUPPORT_BWD 11
 #define LMH_ENTRY_RMS_NORM_BWD 12 /* reads N and d of the shape */
 #define LMH_ENTRY_FP8_LOGITS 13   /* reads N, d and V */
+#define LMH_ENTRY_SAMPLE 14       /* reads N and V; d any valid value */
 
 /* objectives of lmh_loss_bwd */
 #define LMH_BWD_CE 0              /* L = sum_i g_i loss_i                                */
@@ -578,7 +580,39 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *   temperature is not applied. These are the only logits this library stores: they are for the
  *   rows that a token is drawn from or that are looked at, not for a training batch.
  *   Workspace: lmh_workspace_size(shape, LMH_ENTRY_FP8_LOGITS).
+ *
+ * lmh_sample — one token per row of logits. With tau_i the shape's temperature (scalar times per
+ * row, as everywhere in this library: a scalar of 0 or 1 is none, and greedy choice is top_k = 1)
+ * and the candidates ordered by logit, the largest first, equal ones by id, the lowest first:
+ *   1. top-k keeps the first k candidates (k <= 0 or k >= V: all);
+ *   2. top-p keeps the shortest prefix of these whose softmax weight reaches top_p times the
+ *      weight of all of them (top_p >= 1: all; top_p <= 0: the first);
+ *   3. min-p keeps those whose probability is at least min_p times the largest one, that is
+ *      (z - zmax) / tau_i >= log(min_p) (min_p <= 0: all; min_p > 1 counts as 1);
+ *   4. of what is kept, in the order of the ids, the token is the first whose running softmax
+ *      weight exceeds u_i times the total.
+ * Weights are computed in fp64 and added as whole numbers of 2^-F of the largest, F = min(50,
+ * 62 - ceil(log2 V)), so the token does not depend on any order of addition, on N, on the other
+ * rows or on the device. A token below 2^-F of the most likely one's probability is never drawn.
+ *   logits [N, V] of type dtype, row-major and contiguous, aligned to their element; -inf marks a
+ *   token that cannot be drawn. u [N] fp32 in [0, 1). tokens [N] int32 out. logprob [N] fp32 out,
+ *   nullable: z_token / tau_i - log sum_v exp(z_v / tau_i) over the whole row before the filters,
+ *   the quantity that lmh_logprob gives for that token as a label.
+ *   A row whose log-sum-exp is not finite (no logit above -inf, a NaN, a +inf) gets token -1 (an
+ *   ignored label) and logprob 0, and sets LMH_DEVERR_NONFINITE. A NaN top_p or min_p of a row is
+ *   off, a u below 0 or NaN counts as 0, one of 1 or more draws the last kept id; each sets
+ *   LMH_DEVERR_SAMPLING. A NaN scalar is refused.
+ *   shape: N < 2^28, V, the temperature. Workspace: lmh_workspace_size(shape, LMH_ENTRY_SAMPLE).
  */
+typedef struct lmh_sampling {
+  int32_t top_k;
+  float top_p;
+  float min_p;
+  const int32_t* row_top_k; /* device [N], or NULL; each row value is used instead of the scalar */
+  const float* row_top_p;   /* device [N], or NULL */
+  const float* row_min_p;   /* device [N], or NULL */
+} lmh_sampling;
+
 LMH_API lmh_status lmh_rms_norm(int64_t N, int64_t d, const lmh_bf16* x,
                                 const lmh_bf16* residual, const lmh_bf16* weight, float eps,
                                 lmh_bf16* sum, lmh_bf16* y, uint8_t* q, float* scale,
@@ -594,6 +628,10 @@ LMH_API lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
                                   const float* h_scale, const uint8_t* W8, const float* w_scale,
                                   void* logits, int32_t dtype, void* workspace,
                                   size_t workspace_bytes, void* stream);
+LMH_API lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt,
+                              const void* logits, int32_t dtype, const float* u,
+                              int32_t* tokens, float* logprob, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 /*
  * lmh_read_errors — synchronises `stream`, then copies the device error word of the last

@@ -21,7 +21,8 @@ from ._abi import (BWD_CE, BWD_LOGPROB, BWD_SUPPORT_KL, BWD_SUPPORT_LOGPROB, DEV
                    DEVERR_NONFINITE, DEVERR_TEMPERATURE, DEVERR_TIMEOUT, ENTRY_LOGPROB, ENTRY_LOSS_BWD,
                    ENTRY_LOSS_FWD, ENTRY_SUPPORT_KL, ENTRY_SUPPORT_LOGPROB, ENTRY_VP_BWD,
                    ENTRY_LOSS_FWD_BWD, ENTRY_VP_COMBINE, ENTRY_VP_PARTIALS,
-                   DTYPE_BF16, DTYPE_F32, ENTRY_FP8_LOGITS, ENTRY_RMS_NORM_BWD,
+                   DEVERR_SAMPLING, DTYPE_BF16, DTYPE_F32, ENTRY_FP8_LOGITS, ENTRY_RMS_NORM_BWD,
+                   ENTRY_SAMPLE, lmh_sampling,
                    ENTRY_VP_SUPPORT_BWD, ENTRY_VP_SUPPORT_COMBINE, ENTRY_VP_SUPPORT_PARTIALS,
                    F_DW_ACC_GIVEN, F_DW_ACC_STORE,
                    F_GRAD_SCALAR, lmh_vp_dest,
@@ -48,6 +49,8 @@ __all__ = [
     "ENTRY_RMS_NORM_BWD", "lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8",
     "rms_norm", "rms_norm_bwd", "quantize_fp8",
     "ENTRY_FP8_LOGITS", "DTYPE_F32", "DTYPE_BF16", "lmh_fp8_logits", "fp8_logits",
+    "ENTRY_SAMPLE", "DEVERR_SAMPLING", "lmh_sampling", "make_sampling", "lmh_sample", "sample",
+    "next_tokens",
 ]
 
 lib()  # load now: a missing library is an import error, never a silent fallback
@@ -620,4 +623,5 @@ def support_kl(H, W, ids, ref_logp, *, chunk_rows: int = 0, temperature=None,
 
 
 from .serving import (fp8_logits, lmh_fp8_logits, lmh_quantize_fp8,  # noqa: E402
-                      lmh_rms_norm, lmh_rms_norm_bwd, quantize_fp8, rms_norm, rms_norm_bwd)
+                      lmh_rms_norm, lmh_rms_norm_bwd, lmh_sample, make_sampling, next_tokens,
+                      quantize_fp8, rms_norm, rms_norm_bwd, sample)

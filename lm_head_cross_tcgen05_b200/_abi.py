@@ -19,12 +19,13 @@ STATUS_NAMES = {0: "LMH_OK", 1: "LMH_ERR_INVALID_ARG", 2: "LMH_ERR_UNSUPPORTED_D
 
 IGNORE_INDEX = -100
 DEVERR_LABEL_RANGE, DEVERR_TIMEOUT, DEVERR_NONFINITE, DEVERR_TEMPERATURE = 0x1, 0x2, 0x4, 0x8
+DEVERR_SAMPLING = 0x10
 F_MEAN, F_FUSED_BWD, F_DW_ACC_GIVEN, F_SUPPORT_RENORM, F_GRAD_SCALAR = 0x1, 0x2, 0x4, 0x8, 0x10
 F_DW_ACC_STORE = 0x20
 ENTRY_LOSS_FWD, ENTRY_LOSS_BWD, ENTRY_LOGPROB, ENTRY_SUPPORT_LOGPROB, ENTRY_SUPPORT_KL = range(5)
 ENTRY_VP_PARTIALS, ENTRY_VP_COMBINE, ENTRY_VP_BWD, ENTRY_LOSS_FWD_BWD = 5, 6, 7, 8
 ENTRY_VP_SUPPORT_PARTIALS, ENTRY_VP_SUPPORT_COMBINE, ENTRY_VP_SUPPORT_BWD = 9, 10, 11
-ENTRY_RMS_NORM_BWD, ENTRY_FP8_LOGITS = 12, 13
+ENTRY_RMS_NORM_BWD, ENTRY_FP8_LOGITS, ENTRY_SAMPLE = 12, 13, 14
 DTYPE_F32, DTYPE_BF16 = 0, 1
 BWD_CE, BWD_LOGPROB, BWD_SUPPORT_LOGPROB, BWD_SUPPORT_KL = range(4)
 MAX_K = 1024
@@ -38,6 +39,11 @@ class lmh_shape(ctypes.Structure):
 
 class lmh_vp_dest(ctypes.Structure):
     _fields_ = [("recv", c_void_p), ("R", ctypes.c_int32), ("rank", ctypes.c_int32)]
+
+
+class lmh_sampling(ctypes.Structure):
+    _fields_ = [("top_k", ctypes.c_int32), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float),
+                ("row_top_k", c_void_p), ("row_top_p", c_void_p), ("row_min_p", c_void_p)]
 
 
 _P = c_void_p
@@ -78,6 +84,8 @@ _SIGS = {
     "lmh_quantize_fp8": (c_int, [c_int64, c_int64, ctypes.c_int32] + [_P] * 4),
     "lmh_fp8_logits": (c_int, [ctypes.POINTER(lmh_shape)] + [_P] * 5
                        + [ctypes.c_int32, _P, c_size_t, _P]),
+    "lmh_sample": (c_int, [ctypes.POINTER(lmh_shape), ctypes.POINTER(lmh_sampling), _P,
+                           ctypes.c_int32] + [_P] * 4 + [c_size_t, _P]),
     "lmh_read_errors": (c_int, [_P, ctypes.POINTER(c_uint32), _P]),
     "lmh_logprob_noalloc": (c_int, [ctypes.POINTER(lmh_shape)] + [_P] * 6),
     "lmh_peer_barrier": (c_int, [_P, _P, ctypes.c_int32, ctypes.c_int32, c_uint32, c_uint32, _P]),

@@ -211,7 +211,7 @@ enum KernelId {
   KID_SUPPORT_DH, KID_SUPPORT_DW, KID_SPLIT_SUM, KID_VP_LABELS, KID_VP_FINALIZE,
   KID_VP_COMBINE, KID_VP_REDUCE, KID_VP_SCALE, KID_FIX_CANDS, KID_SCALE, KID_COUNT_VALID,
   KID_REDUCE_RANKS, KID_ZERO_SLOTS, KID_PEER_BARRIER, KID_RMS_NORM, KID_RMS_NORM_BWD,
-  KID_NORM_DWEIGHT, KID_QUANTIZE, KID_FP8_LOGITS, KID_COUNT
+  KID_NORM_DWEIGHT, KID_QUANTIZE, KID_FP8_LOGITS, KID_SAMPLE, KID_COUNT
 };
 const char* const kKernelNames[KID_COUNT] = {
     "count_labels", "prep_cands", "gemm_logits_stats", "gemm_logits_stats_store",
@@ -220,7 +220,7 @@ const char* const kKernelNames[KID_COUNT] = {
     "support_grad_dh", "support_dw", "split_sum", "vp_local_labels", "vp_finalize",
     "vp_combine", "vp_reduce_rows", "vp_scale", "fix_cands", "scale_bf16", "count_valid",
     "reduce_ranks", "zero_slots", "peer_barrier", "rms_norm", "rms_norm_bwd", "norm_dweight",
-    "quantize_fp8", "fp8_logits"};
+    "quantize_fp8", "fp8_logits", "sample"};
 
 struct ProfRec {
   int id;

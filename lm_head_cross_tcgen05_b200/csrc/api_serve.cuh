@@ -234,3 +234,102 @@ extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
   return dtype == LMH_DTYPE_F32 ? launch_fp8<float>(p, H8, W8, shape->d, dev, sms, st)
                                 : launch_fp8<__nv_bfloat16>(p, H8, W8, shape->d, dev, sms, st);
 }
+
+namespace {
+
+// How a row of V logits is split: CTAs per row (1, 2, 4 or 8), logits per CTA, whether they are
+// kept in shared memory. The result does not depend on it. A chunk of up to 84 KB leaves room for
+// two CTAs per SM, so that one row's loads run under another's arithmetic; a few rows are spread
+// over more SMs, down to 4096 logits per CTA.
+struct SampPlan {
+  int C, L;
+  bool resident;
+  int smem;
+};
+SampPlan sample_plan(int64_t N, int64_t V, int esize, int sms) {
+  constexpr int64_t kTwo = 84 * 1024;
+  const int64_t most = kMaxDynSmem - static_cast<int64_t>(sizeof(SampShared)) - 16;
+  int C = 1;
+  while (C < kSampMaxC && (cdiv(V, C) * esize > kTwo || (N * C * 2 <= sms && V / (2 * C) >= 4096))) C *= 2;
+  SampPlan p;
+  p.C = C;
+  p.L = static_cast<int>(cdiv(cdiv(V, C), 8) * 8);
+  p.resident = static_cast<int64_t>(p.L) * esize <= most;
+  p.smem = static_cast<int>(sizeof(SampShared) + (p.resident ? static_cast<int64_t>(p.L) * esize : 0));
+  return p;
+}
+
+template <class T>
+lmh_status launch_sample(const SampParams& p, const SampPlan& plan, int dev, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  LMH_TRY(allow_smem(sample_kernel<T>, kMaxDynSmem, dev, &done));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.N * plan.C));
+  cfg.blockDim = dim3(kSampThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(plan.C);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  ProfScope ps(KID_SAMPLE, st);
+  if (cudaLaunchKernelEx(&cfg, sample_kernel<T>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return LMH_ERR_CUDA;
+  }
+  return last_launch();
+}
+
+}  // namespace
+
+extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt,
+                                 const void* logits, int32_t dtype, const float* u,
+                                 int32_t* tokens, float* logprob, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  if (!shape_ok(shape) || !opt || shape->N > 0xfffffffLL ||
+      (dtype != LMH_DTYPE_F32 && dtype != LMH_DTYPE_BF16) || !workspace)
+    return LMH_ERR_INVALID_ARG;
+  if (!opt->row_top_p && opt->top_p != opt->top_p) return LMH_ERR_INVALID_ARG;
+  if (!opt->row_min_p && opt->min_p != opt->min_p) return LMH_ERR_INVALID_ARG;
+  if (shape->N > 0 && (!logits || !u || !tokens)) return LMH_ERR_INVALID_ARG;
+  const uintptr_t esize = dtype == LMH_DTYPE_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(logits) & (esize - 1)) != 0 || !aligned4(u) || !aligned4(tokens) ||
+      !aligned4(logprob) || !aligned4(opt->row_top_k) || !aligned4(opt->row_top_p) ||
+      !aligned4(opt->row_min_p) || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
+    return LMH_ERR_ALIGNMENT;
+  if (workspace_bytes < lmh_workspace_size(shape, LMH_ENTRY_SAMPLE)) return LMH_ERR_WORKSPACE_TOO_SMALL;
+  int dev, sms;
+  LMH_TRY(current_device(&dev, &sms));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const Ws ws{static_cast<uint8_t*>(workspace), static_cast<WsHeader*>(workspace)};
+  LMH_TRY(clear_header(ws, st));
+  if (shape->N == 0) return LMH_OK;
+  const SampPlan plan = sample_plan(shape->N, shape->V, static_cast<int>(esize), sms);
+  SampParams p{};
+  p.N = shape->N;
+  p.V = static_cast<int>(shape->V);
+  p.L = plan.L;
+  p.C = plan.C;
+  int bits = 0;  // V <= 2^bits weights of up to 2^F stay below 2^62
+  while ((1LL << bits) < shape->V) ++bits;
+  p.F = 62 - bits < 50 ? 62 - bits : 50;
+  p.resident = plan.resident ? 1 : 0;
+  p.logits = logits;
+  p.u = u;
+  p.tau = shape->temperature > 0.f ? shape->temperature : 1.f;
+  p.row_tau = shape->row_temperature;
+  p.top_k = opt->top_k;
+  p.top_p = opt->top_p;
+  p.min_p = opt->min_p;
+  p.row_top_k = opt->row_top_k;
+  p.row_top_p = opt->row_top_p;
+  p.row_min_p = opt->row_min_p;
+  p.tokens = tokens;
+  p.logprob = logprob;
+  p.err = &ws.h->err;
+  return dtype == LMH_DTYPE_F32 ? launch_sample<float>(p, plan, dev, st)
+                                : launch_sample<__nv_bfloat16>(p, plan, dev, st);
+}

@@ -1,5 +1,6 @@
 """The entries around the head: the RMS norm that makes its input (with its backward pass) and the
-8-bit quantisation of both operands.
+8-bit quantisation of both operands, the 8-bit logits, and the token drawn from logits;
+``next_tokens`` is a decode step's end made of them.
 
 As in the package's root, ``lmh_*`` mirror the C ABI on tensors that the caller allocated, and the
 lower-case helpers allocate the outputs. All tensors of a call are on one CUDA device, which need
@@ -13,11 +14,13 @@ import ctypes
 
 import torch
 
-from . import (DTYPE_BF16, DTYPE_F32, ENTRY_FP8_LOGITS, ENTRY_RMS_NORM_BWD, _bf, _f32, _ok, _p, _u8, lmh_workspace_size, make_shape)
+from . import (DTYPE_BF16, DTYPE_F32, ENTRY_FP8_LOGITS, ENTRY_RMS_NORM_BWD, ENTRY_SAMPLE, _bf, _f32,
+               _i32, _ok, _p, _u8, lmh_sampling, lmh_workspace_size, make_shape)
 from ._abi import lib
 
-__all__ = ["lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8", "lmh_fp8_logits", "rms_norm",
-           "rms_norm_bwd", "quantize_fp8", "fp8_logits"]
+__all__ = ["lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8", "lmh_fp8_logits", "lmh_sample",
+           "make_sampling", "rms_norm", "rms_norm_bwd", "quantize_fp8", "fp8_logits", "sample",
+           "next_tokens"]
 
 _e4m3 = torch.float8_e4m3fn
 QBLOCK = 128  # columns (and, for a weight, rows) per scale
@@ -124,6 +127,34 @@ def lmh_fp8_logits(shape, H8, h_scale, W8, w_scale, logits, *, workspace, stream
           _logits_dtype(logits.dtype), _p(workspace, _u8, "workspace"), workspace.numel())
 
 
+def make_sampling(N: int, top_k=None, top_p=None, min_p=None) -> lmh_sampling:
+    """Each of top_k, top_p and min_p: None (off), a number for every row, or a CUDA tensor [N]
+    (int32 for top_k, float32 for the others; kept alive by the caller for the call)."""
+    def rows(v, dtype, what):
+        if not isinstance(v, torch.Tensor):
+            return None
+        _shaped(**{what: (v, (N,))})
+        return _p(v, dtype, what)
+
+    def scalar(v, off):
+        return off if v is None or isinstance(v, torch.Tensor) else v
+    k = min(max(int(scalar(top_k, 0)), 0), 2 ** 31 - 1)
+    return lmh_sampling(k, float(scalar(top_p, 1.0)), float(scalar(min_p, 0.0)),
+                        rows(top_k, _i32, "top_k"), rows(top_p, _f32, "top_p"),
+                        rows(min_p, _f32, "min_p"))
+
+
+def lmh_sample(shape, opt, logits, u, tokens, logprob=None, *, workspace, stream=None,
+               row_tensors=()) -> None:
+    """row_tensors: the tensors that shape and opt point to, checked to be on the same device."""
+    N, V = shape.N, shape.V
+    _shaped(logits=(logits, (N, V)), u=(u, (N,)), tokens=(tokens, (N,)), logprob=(logprob, (N,)))
+    _call("lmh_sample", (logits, u, tokens, logprob, workspace, *row_tensors), stream,
+          ctypes.byref(shape), ctypes.byref(opt), _p(logits, None, "logits"),
+          _logits_dtype(logits.dtype), _p(u, _f32, "u"), _p(tokens, _i32, "tokens"),
+          _p(logprob, _f32, "logprob"), _p(workspace, _u8, "workspace"), workspace.numel())
+
+
 def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, fp8: bool = False,
              keep_sum: bool = True, stream=None) -> dict:
     """The RMS norm of x + residual over rows of d: ``y`` (bf16) with ``rstd`` for the backward
@@ -195,4 +226,43 @@ def fp8_logits(H8, h_scale, W8, w_scale, *, dtype=torch.float32, ws=None, stream
             ws = torch.empty(n, dtype=_u8, device=dev)
     lmh_fp8_logits(shape, H8, h_scale, W8, w_scale, out["logits"], workspace=ws, stream=stream)
     out["workspace"] = ws
+    return out
+
+
+def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, ws=None,
+           stream=None) -> dict:
+    """One token per row of logits [N, V] (float32 or bfloat16; -inf: cannot be drawn) at the
+    uniform numbers u [N] (float32 in [0, 1)): temperature, then top-k, then top-p, then min-p,
+    each None, a number or a CUDA tensor [N]. ``tokens`` int32 and ``logprob`` float32, the
+    token's log-probability at that temperature before the filters; -1 and 0 for a row with no
+    logit above -inf or with a NaN or +inf."""
+    N, V = _matrix(logits, "logits")
+    _logits_dtype(logits.dtype)
+    shape, dev = make_shape(N, 64, V, temperature=temperature), logits.device
+    opt = make_sampling(N, top_k, top_p, min_p)
+    with _allocating(stream, dev):
+        out = dict(tokens=torch.empty(N, dtype=_i32, device=dev),
+                   logprob=torch.empty(N, dtype=_f32, device=dev))
+        if ws is None:
+            n = lmh_workspace_size(shape, ENTRY_SAMPLE)
+            if n == 0:
+                raise ValueError("invalid shape for this entry")
+            ws = torch.empty(n, dtype=_u8, device=dev)
+    rows = [t for t in (temperature, top_k, top_p, min_p) if isinstance(t, torch.Tensor)]
+    lmh_sample(shape, opt, logits, u, out["tokens"], out["logprob"], workspace=ws, stream=stream,
+               row_tensors=rows)
+    out["workspace"] = ws
+    return out
+
+
+def next_tokens(x, norm_weight, W8, w_scale, u, residual=None, *, eps: float = 1e-6,
+                temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> dict:
+    """The end of a decode step: the final RMS norm of x + residual into 8 bits, the 8-bit logits
+    of the head (W8, w_scale from ``quantize_fp8``) and one token per row. The parameters are
+    those of ``rms_norm`` and ``sample``; returns ``tokens``, ``logprob`` and ``logits``."""
+    n = rms_norm(x, norm_weight, residual, eps=eps, fp8=True, keep_sum=False, stream=stream)
+    z = fp8_logits(n["q"], n["scale"], W8, w_scale, stream=stream)
+    out = sample(z["logits"], u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p,
+                 stream=stream)
+    out["logits"] = z["logits"]
     return out

@@ -1,0 +1,270 @@
+"""Sampling against the fp64 oracle: tokens have to be equal. The kernel's weights are off by less
+than 2^-40 of the row's largest, so with random u a token differs from the oracle's with a
+probability of at most V * 2^-39 per row (each token's interval moves by less than that), below 1e-6
+for every row here. The log-prob is the fp64 value rounded to fp32, and its sum of weights is off
+by less than V * 2^-F < 2^-25: it may be off by 2^-24 of itself plus 2^-24."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import lm_head_cross_tcgen05_b200 as L
+from oracle import serving_oracle as S
+
+pytestmark = pytest.mark.gpu
+
+f32 = torch.float32
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def logits(N, V, seed, scale=3.0, dtype=f32, digits=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.randn(N, V, device="cuda", generator=g) * scale
+    if digits is not None:
+        z = (z * 10 ** digits).round() / 10 ** digits
+    return z.to(dtype), torch.rand(N, device="cuda", generator=g)
+
+
+def check(z, u, tau=None, k=None, p=None, m=None, flags=0):
+    o = L.sample(z, u, temperature=tau, top_k=k, top_p=p, min_p=m)
+    assert L.lmh_read_errors(o["workspace"]) == flags
+    N = z.shape[0]
+
+    def row(v, i, off, t):
+        if v is None:
+            return off
+        return float(v[i]) if isinstance(v, torch.Tensor) else float(torch.tensor(v, dtype=t))
+    zz, uu, got, lp = f64(z), f64(u), o["tokens"].tolist(), f64(o["logprob"])
+    for i in range(N):
+        want, wlp = S.sample(zz[i], uu[i], row(tau, i, 1.0, f32) or 1.0, int(row(k, i, 0, torch.int64)), row(p, i, 1.0, f32), row(m, i, 0.0, f32))
+        assert got[i] == want, (i, got[i], want)
+        assert abs(lp[i] - wlp) <= 2.0 ** -24 * (abs(wlp) + 1)
+    return o
+
+
+FILTERS = [dict(), dict(k=1), dict(k=50), dict(p=0.9), dict(p=0.3), dict(m=0.05), dict(k=40, p=0.8), dict(k=2000, p=0.95, m=0.001),
+           dict(tau=0.6), dict(tau=1.7, k=100, p=0.99), dict(tau=0.05, p=0.5, m=0.1), dict(p=0.0), dict(k=-3, p=1.5, m=-1.0), dict(m=2.0)]
+
+
+@pytest.mark.parametrize("kw", FILTERS)
+@pytest.mark.parametrize("V", [1, 2, 31, 513, 5000, 32000, 100003])
+def test_scalars(V, kw):
+    check(*logits(6 if V < 100000 else 3, V, seed=V), **kw)
+
+
+@pytest.mark.parametrize("kw", FILTERS)
+@pytest.mark.parametrize("dtype,digits", [(torch.bfloat16, None), (f32, 1)])
+def test_equal_logits_at_the_borders(dtype, digits, kw):
+    check(*logits(8, 9001, seed=7, dtype=dtype, digits=digits), **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(k=1), dict(k=700), dict(k=30000), dict(p=0.5), dict(p=0.9, k=20000), dict(m=1.0), dict(p=0.001)])
+@pytest.mark.parametrize("V", [3000, 65536, 150001])
+def test_all_logits_equal(V, kw):
+    z, u = logits(3, V, seed=8)
+    check(torch.full_like(z, -1.25), u, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(k=3000), dict(p=0.7), dict(k=9000, p=0.9), dict(k=5)])
+def test_crowded_buckets(kw):
+    """One linear bucket holds most of the row: it is split by the bits of the keys."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    z = 5 + 1e-5 * torch.randn(4, 40000, device="cuda", generator=g)
+    z[1] = (z[1] - 5) * 1e-30  # around zero, both signs
+    z[2, ::2] = 5
+    z[3] = torch.where(z[3] > 5, 0.0, -0.0)  # equal zeros of both signs
+    z[0, 17] = 9
+    check(z, torch.rand(4, device="cuda", generator=g), **kw)
+
+
+def test_one_bucket_of_ties_and_neighbours():
+    z, u = logits(2, 30000, seed=10, scale=1e-6)
+    z[:, 5000:] = z[:, 5000:].round(decimals=6)
+    for kw in (dict(k=2), dict(k=4999), dict(k=15000), dict(p=0.4)):
+        check(z, u, **kw)
+
+
+@pytest.mark.parametrize("dtype", [f32, torch.bfloat16])
+def test_per_row_parameters(dtype):
+    N, V = 64, 20011
+    z, u = logits(N, V, seed=11, dtype=dtype)
+    g = torch.Generator(device="cuda").manual_seed(12)
+
+    def pick(v, t):
+        return torch.tensor(v, device="cuda", dtype=t)[torch.randint(len(v), (N,), device="cuda", generator=g)]
+    check(z, u, tau=pick([0.3, 0.8, 1.0, 2.5], f32), k=pick([0, 1, 7, 50, 900, V, V + 5, -1], torch.int32),
+          p=pick([0.0, 0.2, 0.9, 0.999, 1.0], f32), m=pick([0.0, 0.01, 0.3, 1.0], f32))
+
+
+def test_scalar_times_row_temperature():
+    z, u = logits(5, 777, seed=13)
+    row = torch.tensor([0.5, 1.0, 2.0, 0.7, 3.0], device="cuda")
+    shape = L.make_shape(5, 64, 777, temperature=row)
+    shape.temperature = 0.5
+    tok, lp = torch.empty(5, dtype=torch.int32, device="cuda"), torch.empty(5, device="cuda")
+    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    L.lmh_sample(shape, L.make_sampling(5, top_k=9), z, u, tok, lp, workspace=ws)
+    ref = L.sample(z, u, temperature=row * 0.5, top_k=9)
+    assert torch.equal(tok, ref["tokens"]) and torch.equal(lp, ref["logprob"])
+
+
+@pytest.mark.parametrize("dtype", [f32, torch.bfloat16])
+def test_masked_rows(dtype):
+    N, V = 12, 6007
+    z, u = logits(N, V, seed=14, dtype=dtype)
+    low = torch.finfo(dtype).min
+    z[0, 1:] = -torch.inf          # one left
+    z[1] = -torch.inf              # none left
+    z[2, :5000] = low              # the type's lowest value
+    z[3] = low                     # all at the lowest value
+    z[4, 7] = float("nan")
+    z[5, 6000] = torch.inf
+    z[6, 100:] = -torch.inf
+    z[7, :] = low
+    z[7, 33] = -low                # the whole range of the type
+    z[8] = -torch.inf
+    z[8, -1] = low
+    z[9, 3] = -low
+    for kw in (dict(), dict(k=50), dict(p=0.9), dict(k=20, p=0.5, m=0.1), dict(tau=0.01, p=0.99), dict(tau=1e30, p=0.5), dict(m=0.5)):
+        o = check(z, u, flags=L.DEVERR_NONFINITE, **kw)
+        assert o["tokens"][[1, 4, 5]].tolist() == [-1] * 3 and torch.all(o["logprob"][[1, 4, 5]] == 0)
+
+
+def test_extreme_temperatures():
+    z, u = logits(4, 3000, seed=15)
+    for tau in (1e-38, 1e-20, 1e-3, 1e3, 1e20, 1e38):
+        for kw in (dict(), dict(k=10), dict(p=0.5), dict(m=0.2)):
+            check(z, u, tau=tau, **kw)
+
+
+def test_parameters_out_of_range_are_flagged():
+    z, u = logits(8, 500, seed=16)
+    nan = float("nan")
+    u[0], u[1], u[2], u[3] = 1.0, -0.5, nan, float("inf")
+    p = torch.tensor([0.9] * 6 + [nan, 0.9], device="cuda")
+    o = L.sample(z, u, top_p=p)
+    assert L.lmh_read_errors(o["workspace"]) == L.DEVERR_SAMPLING
+    ok_u = u.clone()
+    ok_u[0] = ok_u[3] = 1 - 2.0 ** -24  # no kept token is so unlikely that this is not the last one
+    ok_u[1] = ok_u[2] = 0
+    p[6] = 1.0
+    assert torch.equal(o["tokens"], check(z, ok_u, p=p)["tokens"])
+    tau = torch.tensor([1.0, 0.0, -1.0, nan, float("inf"), 2.0, 1.0, 1.0], device="cuda")
+    o = L.sample(z, ok_u, temperature=tau)
+    assert L.lmh_read_errors(o["workspace"]) == L.DEVERR_TEMPERATURE
+    tau[1:5] = 1
+    assert torch.equal(o["tokens"], check(z, ok_u, tau=tau)["tokens"])
+
+
+@pytest.mark.parametrize("V,dtype", [(262144, f32), (450001, f32), (450001, torch.bfloat16), (1000003, f32)])
+def test_long_rows(V, dtype):
+    """Up to and past what a cluster's shared memory holds."""
+    z, u = logits(2, V, seed=17, dtype=dtype)
+    for kw in (dict(), dict(k=50, p=0.9), dict(p=0.97), dict(k=60000)):
+        check(z, u, **kw)
+
+
+def test_many_rows_and_each_alone():
+    N, V = 700, 4099
+    z, u = logits(N, V, seed=18)
+    o = check(z, u, k=30, p=0.9, tau=0.8)
+    for i in (0, 1, 350, 699):
+        one = L.sample(z[i:i + 1].clone(), u[i:i + 1].clone(), top_k=30, top_p=0.9, temperature=0.8)
+        assert torch.equal(one["tokens"], o["tokens"][i:i + 1]) and torch.equal(one["logprob"], o["logprob"][i:i + 1])
+
+
+def test_offsets_past_32_bits():
+    N, V = 4200, 524288
+    z = torch.zeros(N, V, device="cuda", dtype=torch.bfloat16)
+    zz, u = logits(3, V, seed=19, dtype=torch.bfloat16)
+    z[-3:] = zz
+    uu = torch.zeros(N, device="cuda")
+    uu[-3:] = u
+    o = L.sample(z, uu, top_k=50)
+    ref = check(zz, u, k=50)
+    assert torch.equal(o["tokens"][-3:], ref["tokens"]) and torch.all(o["tokens"][:-3] == 0)
+
+
+def test_u_covers_every_token_by_its_weight():
+    """Equal weights, u on and beside every border."""
+    V = 64
+    u = torch.arange(0, V * 4, device="cuda", dtype=f32) / (V * 4)
+    z = torch.zeros(V * 4, V, device="cuda")
+    z[:, 10:20] = -torch.inf
+    kept = [i for i in range(V) if not 10 <= i < 20]
+    want = [kept[int(x * len(kept))] for x in u.double().tolist()]
+    assert L.sample(z, u)["tokens"].tolist() == want
+
+
+def test_logprob_is_that_of_the_head():
+    """sample()'s log-prob is lmh_logprob's for the same token, up to the logits' own rounding."""
+    N, V, d = 40, 1500, 128
+    g = torch.Generator(device="cuda").manual_seed(20)
+    H, W = torch.randn(N, d, device="cuda", generator=g).bfloat16(), (0.1 * torch.randn(V, d, device="cuda", generator=g)).bfloat16()
+    z = H.double() @ W.double().t()
+    o = L.sample(z.float(), torch.rand(N, device="cuda", generator=g), temperature=0.7, top_p=0.9)
+    lp = L.logprob(H, W, o["tokens"], temperature=0.7)["logprob"]
+    assert float((lp - o["logprob"]).abs().max()) < 2e-3
+
+
+def test_no_rows():
+    o = L.sample(torch.empty(0, 50, device="cuda"), torch.empty(0, device="cuda"))
+    assert o["tokens"].shape == (0,)
+
+
+def test_another_stream_and_two_graphs():
+    z, u = logits(20, 30011, seed=21)
+    kw = dict(top_k=50, top_p=0.9)
+    ref = L.sample(z, u, **kw)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    o = L.sample(z, u, stream=s, **kw)
+    s.synchronize()
+    assert torch.equal(o["tokens"], ref["tokens"])
+    outs, graphs = [], []
+    for kw in (dict(top_k=50), dict(top_p=0.9)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(L.sample(z, u, **kw))
+        graphs.append(g)
+    z2, u2 = logits(20, 30011, seed=22)
+    z.copy_(z2), u.copy_(u2)
+    torch.cuda.synchronize()
+    for g, st in zip(graphs, (s, torch.cuda.Stream())):
+        with torch.cuda.stream(st):
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0]["tokens"], check(z, u, k=50)["tokens"])
+    assert torch.equal(outs[1]["tokens"], check(z, u, p=0.9)["tokens"])
+
+
+def test_decode_step():
+    """norm -> 8-bit logits -> token, with scores for the drawn tokens from the same logits."""
+    N, V, d = 9, 3001, 320
+    g = torch.Generator(device="cuda").manual_seed(23)
+    x, r = torch.randn(N, d, device="cuda", generator=g).bfloat16(), torch.randn(N, d, device="cuda", generator=g).bfloat16()
+    w = torch.rand(d, device="cuda", generator=g).bfloat16()
+    W = (0.1 * torch.randn(V, d, device="cuda", generator=g)).bfloat16()
+    u = torch.rand(N, device="cuda", generator=g)
+    W8, ws = L.quantize_fp8(W)
+    o = L.next_tokens(x, w, W8, ws, u, r, temperature=0.9, top_k=30, top_p=0.95)
+    n = L.rms_norm(x, w, r, fp8=True)
+    z = L.fp8_logits(n["q"], n["scale"], W8, ws)["logits"]
+    assert torch.equal(o["logits"], z)
+    ref = check(z, u, tau=0.9, k=30, p=0.95)
+    assert torch.equal(o["tokens"], ref["tokens"]) and torch.equal(o["logprob"], ref["logprob"])
+    # the 8-bit head is the bf16 head up to the two quantisations
+    y = L.rms_norm(x, w, r)["y"]
+    zb = y.double() @ W.double().t()
+    mags = y.double().abs() @ W.double().abs().t()
+    assert torch.all((z.double() - zb).abs() <= (2 * 2.0 ** -4 + 2.0 ** -7) * mags)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c = L.next_tokens(x, w, W8, ws, u, r, temperature=0.9, top_k=30, top_p=0.95)
+    x.copy_(x.flip(0)), r.copy_(r.flip(0)), u.copy_(u.flip(0))
+    graph.replay()
+    assert torch.equal(c["tokens"], o["tokens"].flip(0))

@@ -96,3 +96,32 @@ def test_logits_python_refuses():
         L.lmh_fp8_logits(L.make_shape(2, 192, 130), H, hs, W, torch.ones(2, 1), torch.zeros(2, 130), workspace=torch.zeros(256, dtype=torch.uint8))
     with pytest.raises(ValueError, match="logits must be"):
         L.fp8_logits(H, hs, W, ws, dtype=torch.float16)
+
+
+def sample(N=1, V=100, logits=P, dtype=0, u=P, tokens=P, logprob=None, work=P, n=1 << 20, tau=None, no_opt=False, **kw):
+    shape = L.make_shape(N, 64, V, temperature=tau)
+    o = L.make_sampling(N, **kw)
+    return lib().lmh_sample(ctypes.byref(shape), None if no_opt else ctypes.byref(o), logits, dtype, u, tokens, logprob, work, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(V=0), INVALID), (dict(V=2 ** 31), INVALID), (dict(N=-1), INVALID), (dict(N=2 ** 28), INVALID), (dict(dtype=3), INVALID),
+    (dict(logits=None), INVALID), (dict(u=None), INVALID), (dict(tokens=None), INVALID), (dict(work=None), INVALID),
+    (dict(top_p=float("nan")), INVALID), (dict(min_p=float("nan")), INVALID), (dict(tau=float("nan")), INVALID), (dict(tau=-1.0), INVALID),
+    (dict(no_opt=True), INVALID), (dict(logits=P + 2), ALIGN), (dict(logits=P + 1, dtype=1), ALIGN), (dict(u=P + 2), ALIGN),
+    (dict(tokens=P + 2), ALIGN), (dict(logprob=P + 2), ALIGN), (dict(work=P + 4), ALIGN), (dict(n=128), SHORT)])
+def test_sample_refuses(kw, status):
+    assert sample(**kw) == status
+
+
+def test_sample_python_refuses():
+    z, u = torch.zeros(2, 10), torch.zeros(2)
+    with pytest.raises(ValueError, match="CUDA"):
+        L.sample(z, u, top_k=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="top_p must have shape"):
+        L.make_sampling(2, top_p=torch.ones(3))
+    with pytest.raises(ValueError, match="logits must be"):
+        L.sample(z.half(), u)
+    with pytest.raises(ValueError, match="u must have shape"):
+        L.lmh_sample(L.make_shape(2, 64, 10), L.make_sampling(2), z, torch.zeros(3), torch.zeros(2, dtype=torch.int32),
+                     workspace=torch.zeros(256, dtype=torch.uint8))
