@@ -11,11 +11,12 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
 from . import (DTYPE_BF16, DTYPE_F32, ENTRY_FP8_LOGITS, ENTRY_RMS_NORM_BWD, ENTRY_SAMPLE, _bf, _f32,
-               _i32, _ok, _p, _u8, lmh_sampling, lmh_workspace_size, make_shape)
+               _i32, _ok, _u8, lmh_sampling, lmh_shape, lmh_workspace_size, make_shape)
 from ._abi import lib
 
 __all__ = ["lmh_rms_norm", "lmh_rms_norm_bwd", "lmh_quantize_fp8", "lmh_fp8_logits", "lmh_sample",
@@ -33,11 +34,25 @@ def _blocks(n: int) -> int:
     return -(-int(n) // QBLOCK)
 
 
-def _shaped(**named) -> None:
-    """Each named (tensor, shape): the tensor, when given, has exactly that shape."""
-    for what, (t, shape) in named.items():
-        if t is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+def _shape_error(what, shape, t):
+    return ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _arg(t, shape, dtype, what: str, dev: int):
+    """The address of t (None stays None) after the checks: exactly this shape and type,
+    contiguous, on device dev. Decode steps are a few microseconds of GPU time, so the checks
+    are kept to what costs little on the host."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise _shape_error(what, shape, t)
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, another tensor of the call on device {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
 def _matrix(t, what: str):
@@ -46,69 +61,83 @@ def _matrix(t, what: str):
     return t.shape
 
 
-def _call(name: str, tensors, stream, *args) -> None:
-    """lib().name(*args, stream) with the tensors' device current."""
-    dev = None
-    for t in tensors:
-        if t is not None:
-            if dev is not None and t.device != dev:
-                raise ValueError(f"{name}: tensors on {dev} and {t.device}")
-            dev = t.device
+_fns = {}
+
+
+def _call(name: str, dev: int, stream, *args) -> None:
+    """The entry with device dev current, on its current stream or on `stream`."""
+    if dev < 0:
+        raise ValueError(f"{name}: its tensors must be CUDA tensors")
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+        raw = torch._C._cuda_getCurrentRawStream(dev)
     elif hasattr(stream, "cuda_stream"):
-        if stream.device != dev:
-            raise ValueError(f"{name}: a stream of {stream.device} for tensors on {dev}")
+        if stream.device_index != dev:
+            raise ValueError(f"{name}: a stream of device {stream.device_index} for tensors on {dev}")
         raw = stream.cuda_stream
     else:
         raw = int(stream)
-    f = getattr(lib(), name)
-    if dev.index == torch.cuda.current_device():
+    f = _fns.get(name)
+    if f is None:
+        f = _fns[name] = getattr(lib(), name)
+    if dev == torch._C._cuda_getDevice():
         st = f(*args, raw)
     else:
         with torch.cuda.device(dev):
             st = f(*args, raw)
-    _ok(name, st)
+    if st != 0:
+        _ok(name, st)
+
+
+_here = contextlib.nullcontext()
 
 
 def _allocating(stream, device):
     """Outputs of a helper belong to the stream that writes them."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _here
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
 
 
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(entry: int, N: int, d: int, V: int) -> int:
+    n = lmh_workspace_size(make_shape(N, d, V), entry)
+    if n == 0:
+        raise ValueError("invalid shape for this entry")
+    return n
+
+
 def lmh_rms_norm(x, weight, residual=None, *, eps, sum=None, y=None, q=None, scale=None,
                  rstd=None, stream=None) -> None:
     N, d = _matrix(x, "x")
-    _shaped(weight=(weight, (d,)), residual=(residual, (N, d)), sum=(sum, (N, d)), y=(y, (N, d)),
-            q=(q, (N, d)), scale=(scale, (N, _blocks(d))), rstd=(rstd, (N,)))
-    _call("lmh_rms_norm", (x, weight, residual, sum, y, q, scale, rstd), stream, N, d,
-          _p(x, _bf, "x"), _p(residual, _bf, "residual"), _p(weight, _bf, "weight"), float(eps),
-          _p(sum, _bf, "sum"), _p(y, _bf, "y"), _p(q, _e4m3, "q"), _p(scale, _f32, "scale"),
-          _p(rstd, _f32, "rstd"))
+    dev, full = x.get_device(), (N, d)
+    _call("lmh_rms_norm", dev, stream, N, d, _arg(x, full, _bf, "x", dev),
+          _arg(residual, full, _bf, "residual", dev), _arg(weight, (d,), _bf, "weight", dev), eps,
+          _arg(sum, full, _bf, "sum", dev), _arg(y, full, _bf, "y", dev),
+          _arg(q, full, _e4m3, "q", dev), _arg(scale, (N, _blocks(d)), _f32, "scale", dev),
+          _arg(rstd, (N,), _f32, "rstd", dev))
 
 
 def lmh_rms_norm_bwd(sum, weight, rstd, dy, dsum=None, dx=None, dweight=None, *, workspace,
                      stream=None) -> None:
     N, d = _matrix(sum, "sum")
-    _shaped(weight=(weight, (d,)), rstd=(rstd, (N,)), dy=(dy, (N, d)), dsum=(dsum, (N, d)),
-            dx=(dx, (N, d)), dweight=(dweight, (d,)))
-    _call("lmh_rms_norm_bwd", (sum, weight, rstd, dy, dsum, dx, dweight, workspace), stream, N, d,
-          _p(sum, _bf, "sum"), _p(weight, _bf, "weight"), _p(rstd, _f32, "rstd"),
-          _p(dy, _bf, "dy"), _p(dsum, _bf, "dsum"), _p(dx, _bf, "dx"),
-          _p(dweight, _bf, "dweight"), _p(workspace, _u8, "workspace"), workspace.numel())
+    dev, full = sum.get_device(), (N, d)
+    _call("lmh_rms_norm_bwd", dev, stream, N, d, _arg(sum, full, _bf, "sum", dev),
+          _arg(weight, (d,), _bf, "weight", dev), _arg(rstd, (N,), _f32, "rstd", dev),
+          _arg(dy, full, _bf, "dy", dev), _arg(dsum, full, _bf, "dsum", dev),
+          _arg(dx, full, _bf, "dx", dev), _arg(dweight, (d,), _bf, "dweight", dev),
+          *_space(workspace, dev))
 
 
 def lmh_quantize_fp8(x, q, scale, block_rows: int, *, stream=None) -> None:
     rows, d = _matrix(x, "x")
     if block_rows not in (1, QBLOCK):
         raise ValueError(f"block_rows must be 1 or {QBLOCK}, got {block_rows}")
-    _shaped(q=(q, (rows, d)), scale=(scale, (-(-rows // block_rows), _blocks(d))))
-    _call("lmh_quantize_fp8", (x, q, scale), stream, rows, d, int(block_rows), _p(x, _bf, "x"),
-          _p(q, _e4m3, "q"), _p(scale, _f32, "scale"))
+    dev, full = x.get_device(), (rows, d)
+    _call("lmh_quantize_fp8", dev, stream, rows, d, int(block_rows), _arg(x, full, _bf, "x", dev),
+          _arg(q, full, _e4m3, "q", dev),
+          _arg(scale, (-(-rows // block_rows), _blocks(d)), _f32, "scale", dev))
 
 
 def _logits_dtype(t) -> int:
@@ -118,41 +147,59 @@ def _logits_dtype(t) -> int:
 
 
 def lmh_fp8_logits(shape, H8, h_scale, W8, w_scale, logits, *, workspace, stream=None) -> None:
-    N, d, V = shape.N, shape.d, shape.V
-    _shaped(H8=(H8, (N, d)), h_scale=(h_scale, (N, _blocks(d))), W8=(W8, (V, d)),
-            w_scale=(w_scale, (_blocks(V), _blocks(d))), logits=(logits, (N, V)))
-    _call("lmh_fp8_logits", (H8, h_scale, W8, w_scale, logits, workspace), stream,
-          ctypes.byref(shape), _p(H8, _e4m3, "H8"), _p(h_scale, _f32, "h_scale"),
-          _p(W8, _e4m3, "W8"), _p(w_scale, _f32, "w_scale"), _p(logits, None, "logits"),
-          _logits_dtype(logits.dtype), _p(workspace, _u8, "workspace"), workspace.numel())
+    N, d, V, dev = shape.N, shape.d, shape.V, H8.get_device()
+    nb, dt = _blocks(d), logits.dtype
+    _call("lmh_fp8_logits", dev, stream, ctypes.byref(shape), _arg(H8, (N, d), _e4m3, "H8", dev),
+          _arg(h_scale, (N, nb), _f32, "h_scale", dev), _arg(W8, (V, d), _e4m3, "W8", dev),
+          _arg(w_scale, (_blocks(V), nb), _f32, "w_scale", dev),
+          _arg(logits, (N, V), dt, "logits", dev), _logits_dtype(dt), *_space(workspace, dev))
+
+
+def _space(workspace, dev: int):
+    """(address, bytes) of a workspace."""
+    return _arg(workspace, (workspace.numel(),), _u8, "workspace", dev), workspace.numel()
 
 
 def make_sampling(N: int, top_k=None, top_p=None, min_p=None) -> lmh_sampling:
     """Each of top_k, top_p and min_p: None (off), a number for every row, or a CUDA tensor [N]
     (int32 for top_k, float32 for the others; kept alive by the caller for the call)."""
-    def rows(v, dtype, what):
-        if not isinstance(v, torch.Tensor):
-            return None
-        _shaped(**{what: (v, (N,))})
-        return _p(v, dtype, what)
+    o = lmh_sampling(0, 1.0, 0.0, None, None, None)
+    if top_k is not None:
+        if isinstance(top_k, torch.Tensor):
+            o.row_top_k = _row_arg(top_k, N, _i32, "top_k")
+        else:
+            o.top_k = min(max(int(top_k), 0), 2 ** 31 - 1)
+    if top_p is not None:
+        if isinstance(top_p, torch.Tensor):
+            o.row_top_p = _row_arg(top_p, N, _f32, "top_p")
+        else:
+            o.top_p = top_p
+    if min_p is not None:
+        if isinstance(min_p, torch.Tensor):
+            o.row_min_p = _row_arg(min_p, N, _f32, "min_p")
+        else:
+            o.min_p = min_p
+    return o
 
-    def scalar(v, off):
-        return off if v is None or isinstance(v, torch.Tensor) else v
-    k = min(max(int(scalar(top_k, 0)), 0), 2 ** 31 - 1)
-    return lmh_sampling(k, float(scalar(top_p, 1.0)), float(scalar(min_p, 0.0)),
-                        rows(top_k, _i32, "top_k"), rows(top_p, _f32, "top_p"),
-                        rows(min_p, _f32, "min_p"))
+
+def _row_arg(t, N: int, dtype, what: str):
+    at = _arg(t, (N,), dtype, what, t.get_device())
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return at
 
 
 def lmh_sample(shape, opt, logits, u, tokens, logprob=None, *, workspace, stream=None,
                row_tensors=()) -> None:
     """row_tensors: the tensors that shape and opt point to, checked to be on the same device."""
-    N, V = shape.N, shape.V
-    _shaped(logits=(logits, (N, V)), u=(u, (N,)), tokens=(tokens, (N,)), logprob=(logprob, (N,)))
-    _call("lmh_sample", (logits, u, tokens, logprob, workspace, *row_tensors), stream,
-          ctypes.byref(shape), ctypes.byref(opt), _p(logits, None, "logits"),
-          _logits_dtype(logits.dtype), _p(u, _f32, "u"), _p(tokens, _i32, "tokens"),
-          _p(logprob, _f32, "logprob"), _p(workspace, _u8, "workspace"), workspace.numel())
+    N, V, dev, dt = shape.N, shape.V, logits.get_device(), logits.dtype
+    for t in row_tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"a row parameter is on {t.device}, the logits on device {dev}")
+    _call("lmh_sample", dev, stream, ctypes.byref(shape), ctypes.byref(opt),
+          _arg(logits, (N, V), dt, "logits", dev), _logits_dtype(dt), _arg(u, (N,), _f32, "u", dev),
+          _arg(tokens, (N,), _i32, "tokens", dev), _arg(logprob, (N,), _f32, "logprob", dev),
+          *_space(workspace, dev))
 
 
 def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, fp8: bool = False,
@@ -188,10 +235,7 @@ def rms_norm_bwd(sum, weight, rstd, dy, dsum=None, *, want_dx: bool = True,
         out = dict(dx=torch.empty(N, d, dtype=_bf, device=dev) if want_dx else None,
                    dweight=torch.empty(d, dtype=_bf, device=dev) if want_dweight else None)
         if ws is None:
-            n = lmh_workspace_size(make_shape(N, d, 1), ENTRY_RMS_NORM_BWD)
-            if n == 0:
-                raise ValueError("invalid shape for this entry")
-            ws = torch.empty(n, dtype=_u8, device=dev)
+            ws = torch.empty(_ws_bytes(ENTRY_RMS_NORM_BWD, N, d, 1), dtype=_u8, device=dev)
     lmh_rms_norm_bwd(sum, weight, rstd, dy, dsum, out["dx"], out["dweight"], workspace=ws,
                      stream=stream)
     return out
@@ -216,14 +260,11 @@ def fp8_logits(H8, h_scale, W8, w_scale, *, dtype=torch.float32, ws=None, stream
     N, d = _matrix(H8, "H8")
     V = _matrix(W8, "W8")[0]
     _logits_dtype(dtype)
-    shape, dev = make_shape(N, d, V), H8.device
+    shape, dev = lmh_shape(N, d, V, 0, 0, 0, 0.0, None), H8.device
     with _allocating(stream, dev):
         out = dict(logits=torch.empty(N, V, dtype=dtype, device=dev))
         if ws is None:
-            n = lmh_workspace_size(shape, ENTRY_FP8_LOGITS)
-            if n == 0:
-                raise ValueError("invalid shape for this entry")
-            ws = torch.empty(n, dtype=_u8, device=dev)
+            ws = torch.empty(_ws_bytes(ENTRY_FP8_LOGITS, N, d, V), dtype=_u8, device=dev)
     lmh_fp8_logits(shape, H8, h_scale, W8, w_scale, out["logits"], workspace=ws, stream=stream)
     out["workspace"] = ws
     return out
@@ -244,10 +285,7 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, w
         out = dict(tokens=torch.empty(N, dtype=_i32, device=dev),
                    logprob=torch.empty(N, dtype=_f32, device=dev))
         if ws is None:
-            n = lmh_workspace_size(shape, ENTRY_SAMPLE)
-            if n == 0:
-                raise ValueError("invalid shape for this entry")
-            ws = torch.empty(n, dtype=_u8, device=dev)
+            ws = torch.empty(_ws_bytes(ENTRY_SAMPLE, N, 64, V), dtype=_u8, device=dev)
     rows = [t for t in (temperature, top_k, top_p, min_p) if isinstance(t, torch.Tensor)]
     lmh_sample(shape, opt, logits, u, out["tokens"], out["logprob"], workspace=ws, stream=stream,
                row_tensors=rows)
