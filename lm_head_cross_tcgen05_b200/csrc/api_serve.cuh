@@ -238,7 +238,7 @@ extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
 namespace {
 
 // How a row of V logits is split: CTAs per row (1, 2, 4 or 8), logits per CTA, whether they are
-// kept in shared memory. The result does not depend on it. A chunk of up to 84 KB leaves room for
+// kept in shared memory. The result does not depend on it. A chunk of up to 80 KB leaves room for
 // two CTAs per SM, so that one row's loads run under another's arithmetic; a few rows are spread
 // over more SMs, down to 4096 logits per CTA.
 struct SampPlan {
@@ -247,15 +247,15 @@ struct SampPlan {
   int smem;
 };
 SampPlan sample_plan(int64_t N, int64_t V, int esize, int sms) {
-  constexpr int64_t kTwo = 84 * 1024;
-  const int64_t most = kMaxDynSmem - static_cast<int64_t>(sizeof(SampShared)) - 16;
+  constexpr int64_t kTwo = 80 * 1024;
+  const int64_t most = kMaxDynSmem - static_cast<int64_t>(sizeof(SampShared)) - 16;  // the row's alignment
   int C = 1;
   while (C < kSampMaxC && (cdiv(V, C) * esize > kTwo || (N * C * 2 <= sms && V / (2 * C) >= 4096))) C *= 2;
   SampPlan p;
   p.C = C;
   p.L = static_cast<int>(cdiv(cdiv(V, C), 8) * 8);
   p.resident = static_cast<int64_t>(p.L) * esize <= most;
-  p.smem = static_cast<int>(sizeof(SampShared) + (p.resident ? static_cast<int64_t>(p.L) * esize : 0));
+  p.smem = static_cast<int>(sizeof(SampShared) + 16 + (p.resident ? static_cast<int64_t>(p.L) * esize : 0));
   return p;
 }
 

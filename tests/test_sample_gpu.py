@@ -1,8 +1,11 @@
 """Sampling against the fp64 oracle: tokens have to be equal. The kernel's weights are off by less
 than 2^-40 of the row's largest, so with random u a token differs from the oracle's with a
 probability of at most V * 2^-39 per row (each token's interval moves by less than that), below 1e-6
-for every row here. The log-prob is the fp64 value rounded to fp32, and its sum of weights is off
-by less than V * 2^-F < 2^-25: it may be off by 2^-24 of itself plus 2^-24."""
+for every row here. The log-prob is rounded to fp32 once (2^-24), and the sum of weights in it is
+formed of fp32 exponentials 2^y, y = log2(e) (z - zmax) / tau: 2^-22 of each for the exponential,
+three roundings of y, 3 * 2^-24 |y| ln2, and 2^-41 for its rounding to a whole number. Relative to
+the sum that is 2^-22 + 3 * 2^-24 E[|z - zmax| / tau] + V * 2^-41, the expectation over the row's
+softmax, as log2(e) ln2 = 1."""
 from __future__ import annotations
 
 import numpy as np
@@ -40,9 +43,16 @@ def check(z, u, tau=None, k=None, p=None, m=None, flags=0):
         return float(v[i]) if isinstance(v, torch.Tensor) else float(torch.tensor(v, dtype=t))
     zz, uu, got, lp = f64(z), f64(u), o["tokens"].tolist(), f64(o["logprob"])
     for i in range(N):
-        want, wlp = S.sample(zz[i], uu[i], row(tau, i, 1.0, f32) or 1.0, int(row(k, i, 0, torch.int64)), row(p, i, 1.0, f32), row(m, i, 0.0, f32))
+        tau_i = row(tau, i, 1.0, f32) or 1.0
+        want, wlp = S.sample(zz[i], uu[i], tau_i, int(row(k, i, 0, torch.int64)), row(p, i, 1.0, f32), row(m, i, 0.0, f32))
         assert got[i] == want, (i, got[i], want)
-        assert abs(lp[i] - wlp) <= 2.0 ** -24 * (abs(wlp) + 1)
+        if want >= 0:
+            t0 = (zz[i] - zz[i].max()) / tau_i
+            e = np.exp(t0)
+            away = -(e[e > 0] * t0[e > 0]).sum() / e.sum()
+            assert abs(lp[i] - wlp) <= 2.0 ** -24 * (abs(wlp) + 1) + 2.0 ** -22 + 3 * 2.0 ** -24 * away + len(t0) * 2.0 ** -41
+        else:
+            assert lp[i] == 0
     return o
 
 
