@@ -171,6 +171,18 @@ size_t norm_bwd_bytes(int64_t N, int64_t d) {
   return norm_shape_ok(N, d) ? align_up(sizeof(WsHeader) + static_cast<size_t>(norm_slices(N)) * d * 4) : 0;
 }
 
+// ------------------------------------------------------------------------ sampling workspace
+struct SampSpace {
+  size_t gmax, gsum, total;
+};
+SampSpace sample_space(int64_t N, int64_t V) {
+  SampSpace s;
+  s.gsum = sizeof(WsHeader);
+  s.gmax = align_up(s.gsum + static_cast<size_t>(N) * cdiv(V, kSum) * 8);
+  s.total = align_up(s.gmax + static_cast<size_t>(N) * cdiv(V, kGroup) * 4);
+  return s;
+}
+
 // ------------------------------------------------------------------------ device state
 struct DevState {
   bool init = false;
@@ -211,7 +223,8 @@ enum KernelId {
   KID_SUPPORT_DH, KID_SUPPORT_DW, KID_SPLIT_SUM, KID_VP_LABELS, KID_VP_FINALIZE,
   KID_VP_COMBINE, KID_VP_REDUCE, KID_VP_SCALE, KID_FIX_CANDS, KID_SCALE, KID_COUNT_VALID,
   KID_REDUCE_RANKS, KID_ZERO_SLOTS, KID_PEER_BARRIER, KID_RMS_NORM, KID_RMS_NORM_BWD,
-  KID_NORM_DWEIGHT, KID_QUANTIZE, KID_FP8_LOGITS, KID_SAMPLE, KID_COUNT
+  KID_NORM_DWEIGHT, KID_QUANTIZE, KID_FP8_LOGITS, KID_SAMPLE_GROUPS, KID_SAMPLE, KID_SAMPLE_ROWS,
+  KID_COUNT
 };
 const char* const kKernelNames[KID_COUNT] = {
     "count_labels", "prep_cands", "gemm_logits_stats", "gemm_logits_stats_store",
@@ -220,7 +233,8 @@ const char* const kKernelNames[KID_COUNT] = {
     "support_grad_dh", "support_dw", "split_sum", "vp_local_labels", "vp_finalize",
     "vp_combine", "vp_reduce_rows", "vp_scale", "fix_cands", "scale_bf16", "count_valid",
     "reduce_ranks", "zero_slots", "peer_barrier", "rms_norm", "rms_norm_bwd", "norm_dweight",
-    "quantize_fp8", "fp8_logits", "sample"};
+    "quantize_fp8", "fp8_logits", "sample_groups", "sample",
+    "sample_rows"};
 
 struct ProfRec {
   int id;

@@ -237,50 +237,80 @@ extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
 
 namespace {
 
-// How a row of V logits is split: CTAs per row (1, 2, 4 or 8), logits per CTA, whether they are
-// kept in shared memory. The result does not depend on it. A chunk of up to 80 KB leaves room for
-// two CTAs per SM, so that one row's loads run under another's arithmetic; a few rows are spread
-// over more SMs, down to 4096 logits per CTA.
+// How the row kernel splits a row: CTAs per row (1, 2, 4 or 8), logits per CTA, whether they are
+// copied to shared memory. No result depends on it. With many rows one CTA each keeps the GPU
+// busy without waiting for others; few rows are spread over as many SMs as there are.
 struct SampPlan {
-  int C, L;
-  bool resident;
-  int smem;
+  int C, L, chunk;  // chunk: bytes of shared memory, 0 if it is not kept
 };
 SampPlan sample_plan(int64_t N, int64_t V, int esize, int sms) {
-  constexpr int64_t kTwo = 80 * 1024;
-  const int64_t most = kMaxDynSmem - static_cast<int64_t>(sizeof(SampShared)) - 16;  // the row's alignment
   int C = 1;
-  while (C < kSampMaxC && (cdiv(V, C) * esize > kTwo || (N * C * 2 <= sms && V / (2 * C) >= 4096))) C *= 2;
+  while (C < kSampMaxC && N * C * 2 <= sms && V / (2 * C) >= 4096) C *= 2;
   SampPlan p;
   p.C = C;
   p.L = static_cast<int>(cdiv(cdiv(V, C), 8) * 8);
-  p.resident = static_cast<int64_t>(p.L) * esize <= most;
-  p.smem = static_cast<int>(sizeof(SampShared) + 16 + (p.resident ? static_cast<int64_t>(p.L) * esize : 0));
+  const int64_t bytes = static_cast<int64_t>(p.L) * esize + 16;  // 16: the row's alignment
+  p.chunk = bytes <= kMaxDynSmem - static_cast<int64_t>(sizeof(RowShared)) ? static_cast<int>(bytes) : 0;
   return p;
 }
 
-template <class T>
-lmh_status launch_sample(const SampParams& p, const SampPlan& plan, int dev, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  LMH_TRY(allow_smem(sample_kernel<T>, kMaxDynSmem, dev, &done));
+// The kernels of one call, each waiting for the one before at its own start, so that its launch
+// overlaps that one's end.
+template <class K>
+lmh_status launch_sample(K kernel, const SampParams& p, int64_t grid, int threads, size_t smem,
+                         int cluster, bool follows, cudaStream_t st) {
+  if (grid > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.N * plan.C));
-  cfg.blockDim = dim3(kSampThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = static_cast<unsigned>(plan.C);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  int n = 0;
+  if (cluster > 0) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = static_cast<unsigned>(cluster);
+    at[n].val.clusterDim.y = 1;
+    at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (follows) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  ProfScope ps(KID_SAMPLE, st);
-  if (cudaLaunchKernelEx(&cfg, sample_kernel<T>, p) != cudaSuccess) {
+  cfg.numAttrs = static_cast<unsigned>(n);
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     cudaGetLastError();
     return LMH_ERR_CUDA;
   }
   return last_launch();
+}
+
+// by_group: a row may be drawn from its groups' records; may_leave: one may be left by that.
+template <class T>
+lmh_status run_sample(SampParams p, bool by_group, bool may_leave, int dev, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  if (by_group) {
+    {
+      ProfScope ps(KID_SAMPLE_GROUPS, st);
+      LMH_TRY(launch_sample(sample_groups_kernel<T>, p, p.N * cdiv(p.g256, kGroupWarps * kGroupPer),
+                            32 * kGroupWarps, 0, 0, false, st));
+    }
+    ProfScope ps(KID_SAMPLE, st);
+    LMH_TRY(launch_sample(sample_list_kernel<T>, p, p.N, kSampThreads, 0, 0, true, st));
+    if (!may_leave) return LMH_OK;
+  }
+  p.all_rows = by_group ? 0 : 1;
+  const SampPlan plan = sample_plan(p.N, p.V, sizeof(T), sms);
+  p.C = plan.C;
+  p.L = plan.L;
+  p.resident = plan.chunk > 0 ? 1 : 0;
+  LMH_TRY(allow_smem(sample_row_kernel<T>, kMaxDynSmem, dev, &done));
+  ProfScope ps(KID_SAMPLE_ROWS, st);
+  return launch_sample(sample_row_kernel<T>, p, p.N * plan.C, kSampThreads, sizeof(RowShared) + plan.chunk, plan.C,
+                       by_group, st);
 }
 
 }  // namespace
@@ -307,16 +337,17 @@ extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt
   const Ws ws{static_cast<uint8_t*>(workspace), static_cast<WsHeader*>(workspace)};
   LMH_TRY(clear_header(ws, st));
   if (shape->N == 0) return LMH_OK;
-  const SampPlan plan = sample_plan(shape->N, shape->V, static_cast<int>(esize), sms);
   SampParams p{};
   p.N = shape->N;
   p.V = static_cast<int>(shape->V);
-  p.L = plan.L;
-  p.C = plan.C;
+  p.g32 = static_cast<int>(cdiv(shape->V, kGroup));
+  p.g256 = static_cast<int>(cdiv(shape->V, kSum));
+  const SampSpace space = sample_space(shape->N, shape->V);
+  p.gmax = ws.at<float>(space.gmax);
+  p.gsum = ws.at<double>(space.gsum);
   int bits = 0;  // V <= 2^bits weights of up to 2^F stay below 2^62
   while ((1LL << bits) < shape->V) ++bits;
   p.F = 62 - bits < 50 ? 62 - bits : 50;
-  p.resident = plan.resident ? 1 : 0;
   p.logits = logits;
   p.u = u;
   p.tau = shape->temperature > 0.f ? shape->temperature : 1.f;
@@ -330,6 +361,13 @@ extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt
   p.tokens = tokens;
   p.logprob = logprob;
   p.err = &ws.h->err;
-  return dtype == LMH_DTYPE_F32 ? launch_sample<float>(p, plan, dev, st)
-                                : launch_sample<__nv_bfloat16>(p, plan, dev, st);
+  // what each row's kernel is, its own parameters say on the device; from the scalars alone the
+  // host sees when no row goes by its groups, and when none of those can be left
+  const bool rows = opt->row_top_k || opt->row_top_p || opt->row_min_p;
+  const int64_t k = opt->top_k > 0 && opt->top_k < shape->V ? opt->top_k : 0;
+  const bool filtered = k > 0 || opt->top_p < 1.f || opt->min_p > 0.f;
+  const bool by_group = rows || k <= kSampListK || shape->V <= kSampList;
+  const bool may_leave = shape->V > kSampList && (rows || filtered);
+  return dtype == LMH_DTYPE_F32 ? run_sample<float>(p, by_group, may_leave, dev, sms, st)
+                                : run_sample<__nv_bfloat16>(p, by_group, may_leave, dev, sms, st);
 }

@@ -31,7 +31,8 @@ using namespace lmh;
 extern "C" size_t lmh_workspace_size(const lmh_shape* shape, int entry) {
   if (!shape_ok(shape) || entry < LMH_ENTRY_LOSS_FWD || entry > LMH_ENTRY_SAMPLE) return 0;
   if (entry == LMH_ENTRY_RMS_NORM_BWD) return norm_bwd_bytes(shape->N, shape->d);
-  if (entry == LMH_ENTRY_FP8_LOGITS || entry == LMH_ENTRY_SAMPLE) return sizeof(WsHeader);
+  if (entry == LMH_ENTRY_FP8_LOGITS) return sizeof(WsHeader);
+  if (entry == LMH_ENTRY_SAMPLE) return sample_space(shape->N, shape->V).total;
   if ((entry == LMH_ENTRY_SUPPORT_LOGPROB || entry == LMH_ENTRY_SUPPORT_KL ||
        entry == LMH_ENTRY_VP_SUPPORT_PARTIALS || entry == LMH_ENTRY_VP_SUPPORT_COMBINE ||
        entry == LMH_ENTRY_VP_SUPPORT_BWD) &&

@@ -1,26 +1,27 @@
 // sample.cuh — one token per row of logits, by inversion of the filtered softmax at a given
-// uniform number. A cluster of 1, 2, 4 or 8 CTAs takes one row: each holds a contiguous chunk of
-// the vocabulary in shared memory (or, where it does not fit, reads it again from global memory),
-// so the row crosses memory once.
+// uniform number. Candidates are ordered by logit, the largest first, equal ones by id; every
+// filter keeps a prefix of that order. Three kernels:
 //
-// All sums are of whole numbers, so no order of addition can change a result: the weight of logit
-// z is w(z) = round(2^F exp((z - zmax) / tau)), computed in fp64, with 2^F as large as V weights
-// can be added in 63 bits (F = 44 for a vocabulary of 152 thousand, at most 50). A token whose
-// probability is below 2^-F of the most likely one's counts as impossible.
+//  * sample_groups_kernel streams the logits once: the maximum of every 32 of a row, and the sum
+//    of exponentials of every 256 relative to their own maximum. This is the pass that is bound
+//    by memory; no thread waits for another beyond its warp.
+//  * sample_list_kernel, one CTA per row, draws the token from those records and a few logits.
+//    Unfiltered, the running sums of the groups lead to the one whose 256 logits decide. With a
+//    short prefix, everything that can be in it is collected and sorted (up to 1024 candidates):
+//    at least k logits lie at or above the k-th largest group maximum, so only groups whose
+//    maximum lies there are read again, 128 bytes for most of k candidates. A top-p prefix
+//    without top-k ends where the candidates' weight reaches a part of the whole sum, which is
+//    known from fp32 exponentials within a bound; if that does not decide it, the row is left.
+//  * sample_row_kernel takes the rows left over (long prefixes), a cluster of 1 to 8 CTAs each. A
+//    prefix that reaches a count or a weight is found by a histogram over 2048 linear buckets of
+//    (zmax - z) / tau, whose threshold bucket's few members go to the first CTA and are sorted
+//    there. A bucket with too many members (equal logits, mostly) is split again by the bits of
+//    its keys until they fit or are all equal; equal ones are counted in vocabulary order.
 //
-// Candidates are ordered by logit, the largest first, equal ones by id. Every filter keeps a
-// prefix of that order. Two ways to the token:
-//  * The list. Where the kept prefix is short, everything that can be in it goes to the first CTA
-//    (up to 1024 candidates), which sorts, filters and draws. What can be in a top-k prefix is
-//    bounded by the maxima of groups of the row's elements: at least k elements lie at or above
-//    the k-th largest group maximum. A top-p prefix without top-k needs the sum of all weights;
-//    here that sum is formed in fp32 (fast_weight) with a bound on its error, and the row goes
-//    the other way if the bound leaves the prefix's end open.
-//  * The whole row. A prefix that reaches a count or a weight is found by a histogram over 2048
-//    linear buckets of (zmax - z) / tau, whose threshold bucket's few members go to the first CTA
-//    and are sorted there. A bucket with too many members (equal logits, mostly) is split again
-//    by the bits of its keys until they fit or are all equal; equal ones are counted in
-//    vocabulary order. What is kept is then (key, id) of the prefix's last candidate.
+// Where a token depends on sums of weights, the weights are whole numbers, so that no order of
+// addition can change it: w(z) = round(2^F exp((z - zmax) / tau)), computed in fp64, with 2^F as
+// large as V weights can be added in 63 bits (F = 44 for a vocabulary of 152 thousand, at most
+// 50). A token whose probability is below 2^-F of the most likely one's counts as impossible.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,9 +35,11 @@ constexpr int kSampThreads = 512, kSampWarps = kSampThreads / 32;
 constexpr int kSampBuckets = 2048;
 constexpr int kSampList = 1024;   // candidates that the first CTA sorts
 constexpr int kSampListK = 512;   // largest top-k that takes the list
-constexpr int kSampGroups = kSampThreads / 4;  // group maxima per CTA
 constexpr int kSampMaxC = 8;
-constexpr int kFastF = 40;        // fast weights are fractions of 2^40
+constexpr int kGroup = 32;        // logits per maximum
+constexpr int kSum = 256;         // logits per sum
+constexpr int kFastF = 40;        // the row kernel's fast weights are fractions of 2^40
+constexpr int kSampPending = -2;  // tokens[row] of a row that the list kernel leaves
 
 struct SampParams {
   long long N;
@@ -55,6 +58,10 @@ struct SampParams {
   int32_t* tokens;      // [N]
   float* logprob;       // [N] or null
   uint32_t* err;
+  int g32, g256;        // groups per row
+  float* gmax;          // [N, g32] largest logit of each 32 (NaN if one is)
+  double* gsum;         // [N, g256] sum of exp((z - max) / tau) over each 256, max their largest
+  int all_rows;         // row kernel: every row, not only those left by the list kernel
 };
 
 typedef unsigned long long u64;
@@ -98,27 +105,38 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-struct SampShared {
+struct SampCommon {
+  double table[64];                        // 2^(j / 64)
+  u64 red[2][kSampWarps];
+  u64 tot_m[kSampMaxC], tot_f[kSampMaxC];  // per CTA, written by each into all: maximum, fast sum
+};
+struct ListShared {
+  double table[64];
+  u64 red[2][kSampWarps];
+  double dred[kSampWarps];
+  u64 list[kSampList];       // candidates, key << 32 | ~id
+  u64 wlist[kSampList];      // their weights, once sorted
+  uint32_t queue[kSampList]; // groups that hold candidates
+  uint4 chist[kSampBuckets / 4];
+  uint32_t list_n, queue_n;
+  int pick[2];
+  u64 base;
+};
+struct alignas(16) RowShared {
+  SampCommon c;
   union {
     u64 whist[kSampBuckets];  // dead once merge() has brought its sums into registers
-    struct {
-      u64 list[kSampList];    // (key << 32 | ~id), on the cluster's first CTA
-      u64 wlist[kSampList];   // their weights, once sorted
-    };
+    u64 list[kSampList];      // as above
   };
   uint32_t chist[kSampBuckets];
-  float gmax[kSampMaxC * kSampGroups];     // every CTA's group maxima
-  double table[64];                        // 2^(j / 64)
-  u64 tot_c[kSampMaxC], tot_w[kSampMaxC];  // per CTA, written by each into all
-  u64 tot_l[kSampMaxC], tot_f[kSampMaxC];  // the same, of locate() and of the fast weights
-  u64 red[2][kSampWarps];
+  u64 tot_c[kSampMaxC], tot_w[kSampMaxC], tot_l[kSampMaxC];  // per CTA, written by each into all
   u64 warp_sum[kSampWarps];
   u64 found[4];                            // bucket, its count, count before, weight before
   u64 cut[2];                              // (key << 32 | ~id) of the last kept, weight kept
-  u64 verdict;
   uint32_t list_n;
-  int pick[4];
 };
+
+static_assert(sizeof(RowShared) % 16 == 0, "the row's copy follows, in 16-byte vectors");
 
 // What a row's threads share about it.
 struct SampRow {
@@ -155,15 +173,14 @@ struct SampRow {
     const double sc = __hiloint2double(__double2hiint(tb) + ((F + (n >> 6)) << 20), __double2loint(tb));
     return static_cast<u64>(__double_as_longlong(fma(e, sc, 4503599627370496.0))) - 0x4330000000000000ull;
   }
-  // 2^40 2^(y / 64) in fp32. Relative error: 2^-22 of ex2.approx, and y / 64 (of magnitude below
-  // F <= 50) is off by three roundings, 50 * 3 * 2^-24 * ln2 < 2^-17; the sum of the two and of the
-  // 2^-41 of the rounding is below kFastErr of a row's sum for V < 2^21.
+  // 2^40 2^(y / 64), from an fp32 exponential
   __device__ __forceinline__ u64 fast_weight(float z) const {
     return __float2ull_rn(fast_exp2(-fmaf(-0.5f, z, half_max) * c32) * 1099511627776.f);
   }
 };
+// Bound on the relative error of a row's sum of fp32 exponentials 2^y: 2^-22 of ex2.approx, three
+// roundings of y (|y| <= 50 where it matters), 50 * 3 * 2^-24 * ln2 < 2^-17, and 13 additions.
 constexpr double kFastErr = 1.0 / 65536;
-constexpr int kFastMaxV = 1 << 21;
 
 __device__ __forceinline__ u64 warp_sum64(u64 x) {
 #pragma unroll
@@ -243,281 +260,485 @@ __device__ __forceinline__ void for_chunk(const T* p, int len, int mis, Fn f) {
   if (i < len) f(as_float(p[i]), i);
 }
 
+// The place of this CTA's chunk of a row.
 template <class T>
-__global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParams p) {
-  constexpr int E = 16 / sizeof(T);
-  extern __shared__ __align__(16) uint8_t dyn[];
-  SampShared& sh = *reinterpret_cast<SampShared*>(dyn);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t rank = cluster_ctarank();
-  const int C = p.C;
-  const long long row = blockIdx.x / C;
-  const int c0 = static_cast<int>(min(static_cast<long long>(rank) * p.L, static_cast<long long>(p.V)));
-  const int len = min(p.L, p.V - c0);
-  const T* gsrc = static_cast<const T*>(p.logits) + row * p.V + c0;
-  const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(gsrc) & 15) / sizeof(T));
-  T* chunk = reinterpret_cast<T*>(dyn + sizeof(SampShared)) + mis;  // aligned as the row is
-  const T* src = p.resident ? chunk : gsrc;
-
-  // before any CTA writes another's shared memory, all have started
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-
-  // ---- the row, its largest logit, whether any is NaN, and the maxima of groups of 4 threads
-  float tmax = -INFINITY;
-  bool bad = false;
-  {
-    const int head = min(len, mis ? E - mis : 0);
-    const int nv = (len - head) / E;
-    auto one = [&](int i) {
-      const T t = gsrc[i];
-      if (p.resident) chunk[i] = t;
-      const float z = as_float(t);
-      bad |= z != z;
-      tmax = fmaxf(tmax, z);
-    };
-    if (tid < head) one(tid);
-    if (head + nv * E + tid < len) one(head + nv * E + tid);
-    const uint4* gv = reinterpret_cast<const uint4*>(gsrc + head);
-    uint4* sv = reinterpret_cast<uint4*>(chunk + head);
-    for (int j0 = tid; j0 < nv; j0 += 4 * kSampThreads) {
-      uint4 w[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (j0 + q * kSampThreads < nv) w[q] = p.resident ? __ldcs(gv + j0 + q * kSampThreads) : gv[j0 + q * kSampThreads];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (j0 + q * kSampThreads < nv) {
-          if (p.resident) sv[j0 + q * kSampThreads] = w[q];
-          const T* e = reinterpret_cast<const T*>(&w[q]);
-#pragma unroll
-          for (int x = 0; x < E; ++x) {
-            const float z = as_float(e[x]);
-            bad |= z != z;
-            tmax = fmaxf(tmax, z);
-          }
-        }
-    }
+struct SampChunk {
+  const T* gsrc;
+  T* chunk;       // its copy in shared memory, aligned as the row is
+  const T* src;   // the copy, or the row itself where it does not fit
+  int c0, len, mis;
+  __device__ __forceinline__ SampChunk(const SampParams& p, long long row, uint32_t rank, uint8_t* room) {
+    c0 = static_cast<int>(min(static_cast<long long>(rank) * p.L, static_cast<long long>(p.V)));
+    len = min(p.L, p.V - c0);
+    gsrc = static_cast<const T*>(p.logits) + row * p.V + c0;
+    mis = static_cast<int>((reinterpret_cast<uintptr_t>(gsrc) & 15) / sizeof(T));
+    chunk = reinterpret_cast<T*>(room) + mis;
+    src = p.resident ? chunk : gsrc;
   }
-  if (tid < 64) sh.table[tid] = exp2(tid / 64.0);
-  if (tid == 0) sh.list_n = 0;
-  float gm = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 1));
-  gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-  const uint32_t kmax = __reduce_max_sync(0xffffffffu, sort_key(gm));
-  bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) sh.red[0][warp] = (static_cast<u64>(bad) << 32) | kmax;
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Copies the chunk to shared memory (where it fits) and returns this thread's largest logit, NaN
+// if it saw one.
+template <class T>
+__device__ __forceinline__ float load_chunk(const SampParams& p, const SampChunk<T>& k) {
+  constexpr int E = 16 / sizeof(T);
+  const int tid = threadIdx.x;
+  float tmax = -INFINITY;
+  const int head = min(k.len, k.mis ? E - k.mis : 0);
+  const int nv = (k.len - head) / E;
+  auto one = [&](int i) {
+    const T t = k.gsrc[i];
+    if (p.resident) k.chunk[i] = t;
+    tmax = max_nan(tmax, as_float(t));
+  };
+  if (tid < head) one(tid);
+  if (head + nv * E + tid < k.len) one(head + nv * E + tid);
+  const uint4* gv = reinterpret_cast<const uint4*>(k.gsrc + head);
+  uint4* sv = reinterpret_cast<uint4*>(k.chunk + head);
+  for (int j0 = tid; j0 < nv; j0 += 4 * kSampThreads) {
+    uint4 w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (j0 + q * kSampThreads < nv) w[q] = p.resident ? __ldcs(gv + j0 + q * kSampThreads) : gv[j0 + q * kSampThreads];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (j0 + q * kSampThreads < nv) {
+        if (p.resident) sv[j0 + q * kSampThreads] = w[q];
+        const T* e = reinterpret_cast<const T*>(&w[q]);
+#pragma unroll
+        for (int x = 0; x < E; ++x) tmax = max_nan(tmax, as_float(e[x]));
+      }
+  }
+  return tmax;
+}
+
+// The row's maximum from the threads' (NaN: one is NaN), in every thread of the cluster. Contains
+// the cluster barrier before which every CTA has started.
+__device__ __forceinline__ float row_max(float tmax, SampCommon& sh, uint32_t rank, int C) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool bad = __any_sync(0xffffffffu, tmax != tmax);
+  const uint32_t kmax = __reduce_max_sync(0xffffffffu, bad ? 0u : sort_key(tmax));
   __syncthreads();
-  if ((lane & 3) == 0)
-    for (int r = 0; r < C; ++r) dsm_st32f(&sh.gmax[rank * kSampGroups + (tid >> 2)], r, gm);
+  if (lane == 0) sh.red[0][warp] = (static_cast<u64>(bad) << 32) | kmax;
+  __syncthreads();
   if (tid < C) {
     u64 m = 0;
     for (int w = 0; w < kSampWarps; ++w) m = max(m, sh.red[0][w]);  // a NaN above every key
-    dsm_st64(&sh.tot_c[rank], tid, m);
+    dsm_st64(&sh.tot_m[rank], tid, m);
   }
-  for (int i = tid; i < kSampBuckets; i += kSampThreads) sh.chist[i] = 0;
   samp_sync();
   u64 m = 0;
-  for (int r = 0; r < C; ++r) m = max(m, sh.tot_c[r]);
-  SampRow R;
-  R.zmax = key_value(static_cast<uint32_t>(m));
-  if ((m >> 32) != 0 || !(fabsf(R.zmax) <= 3.402823466e38f)) {  // no finite log-sum-exp
-    if (rank == 0 && tid == 0) {
-      p.tokens[row] = -1;
-      if (p.logprob) p.logprob[row] = 0.f;
-      atomicOr(p.err, kErrNonFinite);
+  for (int r = 0; r < C; ++r) m = max(m, sh.tot_m[r]);
+  return (m >> 32) != 0 ? NAN : key_value(static_cast<uint32_t>(m));
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// A row's parameters, off where they do nothing.
+struct SampFilter {
+  int k;            // 0: off
+  float top_p;
+  bool use_p, use_m;
+  double tau, ud, low64;  // low64: 64 log2(min_p)
+  uint32_t flag;
+  __device__ __forceinline__ SampFilter(const SampParams& p, long long row) {
+    flag = 0;
+    tau = p.tau;
+    if (p.row_tau) {
+      const float t = p.row_tau[row];
+      if (temperature_ok(t)) tau *= t;
+      else flag |= kErrTemperature;
     }
-    return;  // the same decision in every CTA; none reads another's memory any more
+    k = p.row_top_k ? p.row_top_k[row] : p.top_k;
+    if (k <= 0 || k >= p.V) k = 0;
+    top_p = p.row_top_p ? p.row_top_p[row] : p.top_p;
+    const float min_p = p.row_min_p ? p.row_min_p[row] : p.min_p;
+    const float u = p.u[row];
+    if (top_p != top_p || min_p != min_p || !(u >= 0.f && u < 1.f)) flag |= kErrSampling;
+    use_p = top_p < 1.f;  // NaN: off
+    use_m = min_p > 0.f;
+    low64 = use_m ? 64.0 * log2(fmin(static_cast<double>(min_p), 1.0)) : -HUGE_VAL;
+    ud = u >= 0.f ? static_cast<double>(u) : 0.0;  // NaN: 0
   }
-
-  // ---- parameters
-  uint32_t flag = 0;
-  double tau = p.tau;
-  if (p.row_tau) {
-    const float t = p.row_tau[row];
-    if (temperature_ok(t)) tau *= t;
-    else flag |= kErrTemperature;
-  }
-  int k = p.row_top_k ? p.row_top_k[row] : p.top_k;
-  if (k <= 0 || k >= p.V) k = 0;
-  const float top_p = p.row_top_p ? p.row_top_p[row] : p.top_p;
-  const float min_p = p.row_min_p ? p.row_min_p[row] : p.min_p;
-  const float u = p.u[row];
-  if (top_p != top_p || min_p != min_p || !(u >= 0.f && u < 1.f)) flag |= kErrSampling;
-  const bool use_p = top_p < 1.f;  // NaN: off
-  const bool use_m = min_p > 0.f;
-  const double low64 = use_m ? 64.0 * log2(fmin(static_cast<double>(min_p), 1.0)) : -HUGE_VAL;
-  const double ud = u >= 0.f ? static_cast<double>(u) : 0.0;  // NaN: 0
-  if (flag && rank == 0 && tid == 0) atomicOr(p.err, flag);
-
-  const double c = 1.4426950408889634 / tau;
-  R.zmaxd = R.zmax;
-  R.c64 = 64.0 * c;
-  R.c32 = static_cast<float>(fmin(2.0 * c, 3e38));
-  R.half_max = 0.5f * R.zmax;
-  R.bucket_scale = static_cast<float>(fmin(c * (2.0 * kSampBuckets / p.F), 3e38));
-  R.F = p.F;
-  R.table = sh.table;
-
-  auto log_prob = [&](float z, u64 total, int f) {  // total in units of 2^-f
-    return static_cast<float>((R.y64(z) / 64.0 - (log2(static_cast<double>(total)) - f)) * 0.6931471805599453);
-  };
-  auto draw_at = [&](u64 all) -> u64 {
+  __device__ __forceinline__ u64 draw_at(u64 all) const {
     const u64 r = static_cast<u64>(ud * static_cast<double>(all));
     return r < all ? r : all - 1;
-  };
-  auto p_target = [&](u64 all) -> u64 {
+  }
+  __device__ __forceinline__ u64 p_target(u64 all) const {
     const u64 t = top_p > 0.f ? __double2ull_ru(static_cast<double>(top_p) * static_cast<double>(all)) : 1;
     return t < 1 ? 1 : (t > all ? all : t);
+  }
+  // Whether the row goes by its groups, and whether their sums have to be exact: nothing but the
+  // sums then decides the token.
+  __device__ __forceinline__ bool grouped(int V) const { return V <= kSampList || k <= kSampListK; }
+  __device__ __forceinline__ bool exact() const { return k == 0 && !use_p && !use_m; }
+};
+
+__device__ __forceinline__ SampRow samp_row(const SampParams& p, float zmax, double tau, const double* table) {
+  const double c = 1.4426950408889634 / tau;
+  SampRow R;
+  R.zmaxd = zmax;
+  R.c64 = 64.0 * c;
+  R.c32 = static_cast<float>(fmin(2.0 * c, 3e38));
+  R.half_max = 0.5f * zmax;
+  R.bucket_scale = static_cast<float>(fmin(c * (2.0 * kSampBuckets / p.F), 3e38));
+  R.F = p.F;
+  R.table = table;
+  return R;
+}
+__device__ __forceinline__ bool no_sum(const SampParams& p, long long row, float zmax, bool writer) {
+  if (fabsf(zmax) <= 3.402823466e38f) return false;
+  if (writer) {  // no finite log-sum-exp
+    p.tokens[row] = -1;
+    if (p.logprob) p.logprob[row] = 0.f;
+    atomicOr(p.err, kErrNonFinite);
+  }
+  return true;
+}
+
+// total: the sum of the row's weights, the largest one's being 1
+__device__ __forceinline__ float samp_logprob(const SampRow& R, float z, double total) {
+  return static_cast<float>((R.y64(z) / 64.0 - log2(total)) * 0.6931471805599453);
+}
+
+__device__ __forceinline__ float warp_max_nan(float x) {
+  float r;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// One warp per 256 logits of a row, two such per warp so that 16 loads are under way.
+constexpr int kGroupWarps = 8, kGroupPer = 2;
+template <class T>
+__global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const SampParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_row = (p.g256 + kGroupWarps * kGroupPer - 1) / (kGroupWarps * kGroupPer);
+  const long long row = blockIdx.x / per_row;
+  const int g0 = (static_cast<int>(blockIdx.x - row * per_row) * kGroupWarps + warp) * kGroupPer;
+  if (g0 >= p.g256) return;
+  const SampFilter f(p, row);
+  if (!f.grouped(p.V)) return;
+  const T* src = static_cast<const T*>(p.logits) + row * p.V;
+  float z[kGroupPer][8];
+#pragma unroll
+  for (int q = 0; q < kGroupPer; ++q)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const long long i = static_cast<long long>(g0 + q) * kSum + j * kGroup + lane;
+      z[q][j] = i < p.V ? as_float(src[i]) : -INFINITY;
+    }
+  const double c = 1.4426950408889634 / f.tau;
+  const float c2 = static_cast<float>(fmin(2.0 * c, 3e38));
+#pragma unroll
+  for (int q = 0; q < kGroupPer; ++q) {
+    if (g0 + q >= p.g256) break;
+    float mine = -INFINITY, m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = warp_max_nan(z[q][j]);
+      if (lane == j) mine = x;
+      m = max_nan(m, x);
+    }
+    const int g = (g0 + q) * 8 + lane;
+    if (lane < 8 && g < p.g32) p.gmax[row * p.g32 + g] = mine;
+    double s = 0.0;
+    if (fabsf(m) <= 3.402823466e38f) {  // else no finite logit, or the row has no finite sum
+      if (f.exact()) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s += exp2((static_cast<double>(z[q][j]) - m) * c);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      } else {
+        float e = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) e += fast_exp2(-fmaf(-0.5f, z[q][j], 0.5f * m) * c2);
+        s = warp_sum(e);
+      }
+    }
+    if (lane == 0) p.gsum[row * p.g256 + g0 + q] = s;
+  }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampParams p) {
+  __shared__ ListShared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long row = blockIdx.x;
+  const SampFilter f(p, row);
+  if (!f.grouped(p.V)) {
+    if (tid == 0) p.tokens[row] = kSampPending;
+    return;
+  }
+  if (tid < 64) sh.table[tid] = exp2(tid / 64.0);
+  if (tid < 2) sh.pick[tid] = kSampBuckets - 1;
+  if (tid == 0) sh.list_n = sh.queue_n = 0;
+  for (int i = tid; i < kSampBuckets / 4; i += kSampThreads) sh.chist[i] = make_uint4(0, 0, 0, 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the groups' records
+  const T* src = static_cast<const T*>(p.logits) + row * p.V;
+  const float* gmax = p.gmax + row * p.g32;
+  const double* gsum = p.gsum + row * p.g256;
+
+  float tmax = -INFINITY;
+  for (int g = tid; g < p.g32; g += kSampThreads) tmax = max_nan(tmax, gmax[g]);
+  tmax = warp_max_nan(tmax);
+  if (lane == 0) sh.red[0][warp] = __float_as_uint(tmax);
+  __syncthreads();
+  float zmax = -INFINITY;
+  for (int w = 0; w < kSampWarps; ++w) zmax = max_nan(zmax, __uint_as_float(static_cast<uint32_t>(sh.red[0][w])));
+  if (no_sum(p, row, zmax, tid == 0)) return;
+  if (f.flag && tid == 0) atomicOr(p.err, f.flag);
+  const SampRow R = samp_row(p, zmax, f.tau, sh.table);
+  // the largest logit of 256
+  auto max256 = [&](int g) {
+    float m = -INFINITY;
+    for (int j = g * 8; j < min(g * 8 + 8, p.g32); ++j) m = fmaxf(m, gmax[j]);
+    return m;
   };
 
-  // ---- the list
-  const bool all_listed = p.V <= kSampList;
-  const bool filtered = k > 0 || use_p || use_m;
-  bool fast = false;  // tot_f holds the fast weights' sums
-  if (all_listed || (k > 0 ? k <= kSampListK : (use_p ? p.V < kFastMaxV : use_m))) {
-    // candidates lie in the buckets up to b0
-    int b0 = kSampBuckets - 1;
-    const int want = k > 0 ? k : kSampListK / 2;
-    if (!all_listed && (k > 0 || use_p)) {
-      for (int i = tid; i < C * kSampGroups; i += kSampThreads) {
-        const int b = R.bucket(sh.gmax[i]);
-        if (b < kSampBuckets) atomicAdd(&sh.chist[b], 1u);
+  if (f.exact()) {
+    // whole numbers of 2^-F again; each thread has a run of groups
+    const double up = __hiloint2double((1023 + p.F) << 20, 0);
+    const int run = (p.g256 + kSampThreads - 1) / kSampThreads;
+    const int r0 = min(p.g256, tid * run), r1 = min(p.g256, r0 + run);
+    auto group_weight = [&](int g) -> u64 {
+      const double s = gsum[g];
+      return s > 0.0 ? __double2ull_rn(s * exp2(R.y64(max256(g)) / 64.0) * up) : 0;
+    };
+    u64 s = 0, before, px, total, tx;
+    for (int g = r0; g < r1; ++g) s += group_weight(g);
+    block_scan2(s, 0, &before, &px, &total, &tx, sh.red);
+    const u64 r = f.draw_at(total);
+    if (before <= r && r < before + s) {
+      int g = r0;
+      for (; g < r1 - 1; ++g) {
+        const u64 w = group_weight(g);
+        if (r < before + w) break;
+        before += w;
       }
-      if (tid == 0) sh.pick[0] = kSampBuckets - 1;
-      __syncthreads();
-      uint4 h = *reinterpret_cast<const uint4*>(&sh.chist[tid * 4]);
-      u64 pc, px, tc, tx;
-      block_scan2(h.x + h.y + h.z + h.w, 0, &pc, &px, &tc, &tx, sh.red);
-      const uint32_t hv[4] = {h.x, h.y, h.z, h.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (pc < static_cast<u64>(want) && static_cast<u64>(want) <= pc + hv[j]) sh.pick[0] = tid * 4 + j;
-        pc += hv[j];
-      }
-      __syncthreads();
-      b0 = sh.pick[0];
+      sh.pick[0] = g;
+      sh.base = r - before;
     }
-    if (use_m && !use_p) {
-      const double bm = -low64 / 64.0 * (kSampBuckets / static_cast<double>(p.F)) + 1.0;
-      if (bm < b0) b0 = static_cast<int>(bm);
-    }
-    u64 sum = 0;
-    fast = true;
-    for_chunk(src, len, mis, [&](float z, int i) {
-      const int b = R.bucket(z);
-      if (b <= b0) {
-        const uint32_t at = dsm_add32(&sh.list_n, 0, 1);
-        if (at < kSampList) dsm_st64(&sh.list[at], 0, (static_cast<u64>(sort_key(z)) << 32) | static_cast<uint32_t>(~(c0 + i)));
-      }
-      if (b < kSampBuckets) sum += R.fast_weight(z);
-    });
-    sum = warp_sum64(sum);
     __syncthreads();
-    if (lane == 0) sh.red[0][warp] = sum;
-    __syncthreads();
-    if (tid < C) {
-      u64 t = 0;
-      for (int w = 0; w < kSampWarps; ++w) t += sh.red[0][w];
-      dsm_st64(&sh.tot_f[rank], tid, t);
+    if (warp != 0) return;
+    // within the group, 8 adjacent logits a lane; its weights' sum is its rounded sum up to their
+    // own roundings, so a remainder past the last goes to the last that can be drawn
+    const long long i0 = static_cast<long long>(sh.pick[0]) * kSum + lane * 8;
+    const u64 rest = sh.base;
+    u64 w[8], sum = 0;
+    int last = -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      w[j] = i0 + j < p.V ? R.weight(as_float(src[i0 + j])) : 0;
+      sum += w[j];
+      if (w[j] > 0) last = j;
     }
-    samp_sync();
-    if (rank == 0) {
-      const int n = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(kSampList)));
-      bool ok = sh.list_n <= kSampList;
-      u64 fsum = 0;
-      for (int r = 0; r < C; ++r) fsum += sh.tot_f[r];
-      if (ok) {  // uniform over the block
-        int P = 2;
-        while (P < n) P <<= 1;
-        for (int i = n + tid; i < P; i += kSampThreads) sh.list[i] = 0;
-        __syncthreads();
-        bitonic_desc(sh.list, P);
-        // this thread's two candidates, and the weight before them
-        u64 w[2] = {0, 0}, pw, px, tw, tx;
-        bool in_m[2] = {false, false};
-        const int nk = k > 0 ? min(n, k) : n;
+    const u64 incl = warp_scan64(sum, lane);
+    u64 at = incl - sum;
+    int hit = -1;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (tid * 2 + j < nk) {
-            const float z = key_value(static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32));
-            w[j] = R.weight(z);
-            in_m[j] = R.y64(z) >= low64;
-            sh.wlist[tid * 2 + j] = w[j];
-          }
-        block_scan2(w[0] + w[1], static_cast<u64>(in_m[0]) + in_m[1], &pw, &px, &tw, &tx, sh.red);
-        // kept: nk by count, tx by min-p, and by top-p the first whose running weight reaches the
-        // target; without top-k and with more candidates than the list's, the target is only
-        // known to lie in [t0, t1]
-        u64 t0 = tw, t1 = tw;
-        if (use_p) {
-          if (k > 0 || all_listed) {
-            t0 = t1 = p_target(tw);
-          } else {
-            const double s = static_cast<double>(top_p > 0.f ? top_p : 0.f) * static_cast<double>(fsum) *
-                             __hiloint2double((1023 + p.F - kFastF) << 20, 0);
-            t0 = max(static_cast<u64>(s * (1.0 - kFastErr)), 1ull);
-            t1 = static_cast<u64>(s * (1.0 + kFastErr)) + 2;
-            if (top_p <= 0.f) t1 = 1;
-          }
-        }
-        if (tid < 2) sh.pick[tid] = -1;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (pw < t0 && t0 <= pw + w[j]) sh.pick[0] = tid * 2 + j;
-          if (pw < t1 && t1 <= pw + w[j]) sh.pick[1] = tid * 2 + j;
-          pw += w[j];
-        }
-        __syncthreads();
-        int nkeep = min(nk, static_cast<int>(tx));
-        if (use_p) {
-          ok = sh.pick[0] >= 0 && sh.pick[0] == sh.pick[1];
-          nkeep = min(nkeep, sh.pick[0] + 1);
-        }
-        if (ok) {
-          // in the order of the ids
-          u64 x[2] = {0, 0};
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (tid * 2 + j < nkeep) x[j] = (sh.list[tid * 2 + j] << 32) | static_cast<uint32_t>(tid * 2 + j);
-          __syncthreads();
-          P = 2;
-          while (P < nkeep) P <<= 1;
-          if (tid * 2 < P) {
-            sh.list[tid * 2] = x[0];
-            sh.list[tid * 2 + 1] = x[1];
-          }
-          __syncthreads();
-          bitonic_desc(sh.list, P);
-          w[0] = tid * 2 < nkeep ? sh.wlist[static_cast<uint32_t>(sh.list[tid * 2])] : 0;
-          w[1] = tid * 2 + 1 < nkeep ? sh.wlist[static_cast<uint32_t>(sh.list[tid * 2 + 1])] : 0;
-          block_scan2(w[0] + w[1], 0, &pw, &px, &tx, &px, sh.red);
-          const u64 r = draw_at(tx);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (pw <= r && r < pw + w[j]) {
-              const int id = static_cast<int>(~static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32));
-              p.tokens[row] = id;
-              if (p.logprob) {
-                const float z = as_float(static_cast<const T*>(p.logits)[row * p.V + id]);
-                p.logprob[row] = log_prob(z, fsum, kFastF);
-              }
-            }
-            pw += w[j];
-          }
-        }
-      }
-      __syncthreads();
-      if (tid == 0) sh.list_n = 0;
-      if (tid < C) dsm_st64(&sh.verdict, tid, ok ? 1 : 0);
+    for (int j = 0; j < 8; ++j) {
+      if (hit < 0 && at <= rest && rest < at + w[j]) hit = j;
+      at += w[j];
     }
-    samp_sync();
-    if (sh.verdict) return;  // in every CTA alike; none reads another's memory any more
+    const uint32_t found = __ballot_sync(0xffffffffu, hit >= 0);
+    const uint32_t can = __ballot_sync(0xffffffffu, last >= 0);
+    const int owner = found ? __ffs(found) - 1 : (can ? 31 - __clz(can) : 0);
+    if (lane == owner) {
+      const long long id = i0 + (found ? hit : max(last, 0));
+      p.tokens[row] = static_cast<int>(id);
+      if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), static_cast<double>(total) / up);
+    }
+    return;
   }
 
-  // ---- the whole row
+  // ---- the row's sum, in a fixed order
+  double part = 0.0;
+  for (int g = tid; g < p.g256; g += kSampThreads) {
+    const double s = gsum[g];
+    if (s > 0.0) part += s * exp2(R.y64(max256(g)) / 64.0);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+  if (lane == 0) sh.dred[warp] = part;
+
+  // ---- candidates lie in the buckets up to b0
+  const bool all_listed = p.V <= kSampList;
+  int b0 = kSampBuckets - 1;
+  if (!all_listed && (f.k > 0 || f.use_p)) {
+    const u64 want = f.k > 0 ? f.k : kSampListK / 2;
+    uint32_t* hist = reinterpret_cast<uint32_t*>(sh.chist);
+    for (int g = tid; g < p.g32; g += kSampThreads) {
+      const int b = R.bucket(gmax[g]);
+      if (b < kSampBuckets) atomicAdd(&hist[b], 1u);
+    }
+    __syncthreads();
+    const uint4 h = sh.chist[tid];
+    const uint32_t hv[4] = {h.x, h.y, h.z, h.w};
+    u64 pc, px, tc, tx;
+    block_scan2(h.x + h.y + h.z + h.w, 0, &pc, &px, &tc, &tx, sh.red);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (pc < want && want <= pc + hv[j]) sh.pick[0] = tid * 4 + j;
+      pc += hv[j];
+    }
+    __syncthreads();
+    b0 = sh.pick[0];
+  }
+  if (f.use_m && !f.use_p) {
+    const double bm = -f.low64 / 64.0 * (kSampBuckets / static_cast<double>(p.F)) + 1.0;
+    if (bm < b0) b0 = static_cast<int>(bm);
+  }
+  for (int g = tid; g < p.g32; g += kSampThreads)
+    if (R.bucket(gmax[g]) <= b0) {
+      const uint32_t at = atomicAdd(&sh.queue_n, 1u);
+      if (at < kSampList) sh.queue[at] = g;
+    }
+  __syncthreads();
+  double total = 0.0;
+  for (int w = 0; w < kSampWarps; ++w) total += sh.dred[w];
+  // every queued group holds a candidate: more of them than the list holds leave the row
+  const int groups = static_cast<int>(min(sh.queue_n, static_cast<uint32_t>(kSampList)));
+  if (sh.queue_n <= kSampList) {
+    for (int q0 = warp; q0 < groups; q0 += 4 * kSampWarps) {
+      float z[4];
+      int id[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = q0 + j * kSampWarps;
+        id[j] = q < groups ? static_cast<int>(sh.queue[q]) * kGroup + lane : -1;
+        const bool in = id[j] >= 0 && id[j] < p.V;
+        z[j] = in ? as_float(src[id[j]]) : 0.f;
+        if (!in) id[j] = -1;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool hit = id[j] >= 0 && R.bucket(z[j]) <= b0;
+        const uint32_t mask = __ballot_sync(0xffffffffu, hit);
+        uint32_t at = 0;
+        if (mask && lane == 0) at = atomicAdd(&sh.list_n, __popc(mask));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1));
+        if (hit && at < kSampList) sh.list[at] = (static_cast<u64>(sort_key(z[j])) << 32) | static_cast<uint32_t>(~id[j]);
+      }
+    }
+  }
+  __syncthreads();
+  const int n = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(kSampList)));
+  bool ok = sh.queue_n <= kSampList && sh.list_n <= kSampList;  // alike in all threads, as every `ok` below
+  if (ok) {
+    int P = 2;
+    while (P < n) P <<= 1;
+    for (int i = n + tid; i < P; i += kSampThreads) sh.list[i] = 0;
+    if (tid < 2) sh.pick[tid] = -1;
+    __syncthreads();
+    bitonic_desc(sh.list, P);
+    // this thread's two candidates, and the weight before them
+    u64 w[2] = {0, 0}, pw, px, tw, tx;
+    bool in_m[2] = {false, false};
+    const int nk = f.k > 0 ? min(n, f.k) : n;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (tid * 2 + j < nk) {
+        const float z = key_value(static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32));
+        w[j] = R.weight(z);
+        in_m[j] = R.y64(z) >= f.low64;
+        sh.wlist[tid * 2 + j] = w[j];
+      }
+    block_scan2(w[0] + w[1], static_cast<u64>(in_m[0]) + in_m[1], &pw, &px, &tw, &tx, sh.red);
+    // kept: nk by count, tx by min-p, and by top-p up to the first whose running weight reaches
+    // the target; without top-k and with candidates outside the list, the target is only known
+    // to lie in [t0, t1]
+    int nkeep = min(nk, static_cast<int>(tx));
+    if (f.use_p) {
+      u64 t0, t1;
+      if (f.k > 0 || all_listed) {
+        t0 = t1 = f.p_target(tw);
+      } else if (!(f.top_p > 0.f)) {
+        t0 = t1 = 1;
+      } else {
+        const double s = static_cast<double>(f.top_p) * total * __hiloint2double((1023 + p.F) << 20, 0);
+        t0 = max(static_cast<u64>(s * (1.0 - kFastErr)), 1ull);
+        t1 = static_cast<u64>(s * (1.0 + kFastErr)) + 2;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (pw < t0 && t0 <= pw + w[j]) sh.pick[0] = tid * 2 + j;
+        if (pw < t1 && t1 <= pw + w[j]) sh.pick[1] = tid * 2 + j;
+        pw += w[j];
+      }
+      __syncthreads();
+      ok = sh.pick[0] >= 0 && sh.pick[0] == sh.pick[1];
+      nkeep = min(nkeep, sh.pick[0] + 1);
+    }
+    if (ok) {
+      // in the order of the ids
+      u64 x[2] = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (tid * 2 + j < nkeep) x[j] = (sh.list[tid * 2 + j] << 32) | static_cast<uint32_t>(tid * 2 + j);
+      __syncthreads();
+      P = 2;
+      while (P < nkeep) P <<= 1;
+      if (tid * 2 < P) {
+        sh.list[tid * 2] = x[0];
+        sh.list[tid * 2 + 1] = x[1];
+      }
+      __syncthreads();
+      bitonic_desc(sh.list, P);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) w[j] = tid * 2 + j < nkeep ? sh.wlist[static_cast<uint32_t>(sh.list[tid * 2 + j])] : 0;
+      block_scan2(w[0] + w[1], 0, &pw, &px, &tw, &tx, sh.red);
+      const u64 r = f.draw_at(tw);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (pw <= r && r < pw + w[j]) {
+          const int id = static_cast<int>(~static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32));
+          p.tokens[row] = id;
+          if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), total);
+        }
+        pw += w[j];
+      }
+      return;
+    }
+  }
+  if (tid == 0) p.tokens[row] = kSampPending;
+}
+
+// One row per cluster; it needs no other row's turn, so rows that are not pending cost an exit.
+template <class T>
+__global__ void __launch_bounds__(kSampThreads, 1) sample_row_kernel(const SampParams p) {
+  extern __shared__ __align__(16) uint8_t dyn[];
+  RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
+  const uint32_t rank = cluster_ctarank();
+  const long long row = blockIdx.x / p.C;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list kernel's tokens
+  if (!p.all_rows && p.tokens[row] != kSampPending) return;  // in every CTA alike
+  if (threadIdx.x < 64) sh.c.table[threadIdx.x] = exp2(threadIdx.x / 64.0);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = p.C;
+  const SampFilter f(p, row);
+  cluster_arrive();
+  const SampChunk<T> ch(p, row, rank, dyn + sizeof(RowShared));
+  const int len = ch.len;
+  const float tmax = load_chunk(p, ch);
+  if (tid == 0) sh.list_n = 0;
+  cluster_wait();
+  const float zmax = row_max(tmax, sh.c, rank, C);
+  if (no_sum(p, row, zmax, rank == 0 && tid == 0)) return;
+  if (f.flag && rank == 0 && tid == 0) atomicOr(p.err, f.flag);
+  const SampRow R = samp_row(p, zmax, f.tau, sh.c.table);
   for (int i = tid; i < kSampBuckets; i += kSampThreads) {
     sh.whist[i] = 0;
     sh.chist[i] = 0;
@@ -546,7 +767,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
       }
     }
     u64 xc, xw;
-    block_scan2(sc, sw, bc, bw, &xc, &xw, sh.red);
+    block_scan2(sc, sw, bc, bw, &xc, &xw, sh.c.red);
     if (tid < C) {
       dsm_st64(&sh.tot_c[rank], tid, xc);
       dsm_st64(&sh.tot_w[rank], tid, xw);
@@ -581,14 +802,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
     }
     samp_sync();
   };
-  // The id at which the running sum, in vocabulary order, of f(z, id) passes r (which the sum
+  // The id at which the running sum, in vocabulary order, of fn(z, id) passes r (which the sum
   // over the row does); -1 where another warp holds it. Each warp has a contiguous segment.
   const int seg = ((len + kSampThreads - 1) / kSampThreads) * 32;
-  auto locate = [&](auto f, auto target) -> int {
+  auto locate = [&](auto fn, auto target) -> int {
     u64 s = 0;
     const int s0 = min(len, warp * seg), s1 = min(len, s0 + seg);
 #pragma unroll 4
-    for (int i = s0 + lane; i < s1; i += 32) s += f(as_float(src[i]), c0 + i);
+    for (int i = s0 + lane; i < s1; i += 32) s += fn(as_float(ch.src[i]), ch.c0 + i);
     s = warp_sum64(s);
     if (lane == 0) sh.warp_sum[warp] = s;
     __syncthreads();
@@ -608,16 +829,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
     const int run = (s1 - s0 + 31) / 32;
     const int r0 = min(s1, s0 + lane * run), r1 = min(s1, r0 + run);
     u64 x = 0;
-    for (int i = r0; i < r1; ++i) x += f(as_float(src[i]), c0 + i);
+    for (int i = r0; i < r1; ++i) x += fn(as_float(ch.src[i]), ch.c0 + i);
     const u64 incl = warp_scan64(x, lane);
     const int owner = __ffs(__ballot_sync(0xffffffffu, r < base + incl)) - 1;
     base += __shfl_sync(0xffffffffu, incl - x, owner);
     const int e1 = __shfl_sync(0xffffffffu, r1, owner);
     for (int i0 = __shfl_sync(0xffffffffu, r0, owner); i0 < e1; i0 += 32) {
       const int i = i0 + lane;
-      const u64 y = warp_scan64(i < e1 ? f(as_float(src[i]), c0 + i) : 0, lane);
+      const u64 y = warp_scan64(i < e1 ? fn(as_float(ch.src[i]), ch.c0 + i) : 0, lane);
       const uint32_t hit = __ballot_sync(0xffffffffu, r < base + y);
-      if (hit) return c0 + i0 + __ffs(hit) - 1;
+      if (hit) return ch.c0 + i0 + __ffs(hit) - 1;
       base += __shfl_sync(0xffffffffu, y, 31);
     }
     return -1;
@@ -633,7 +854,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
       // the members' smallest and largest key
       uint32_t lo = 0xffffffffu, hi = 0;
       for (int i = tid; i < len; i += kSampThreads) {
-        const float z = as_float(src[i]);
+        const float z = as_float(ch.src[i]);
         const uint32_t key = sort_key(z);
         if (key >= klo && key <= khi && R.bucket(z) == bucket0) {
           lo = min(lo, key);
@@ -644,8 +865,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
       hi = __reduce_max_sync(0xffffffffu, hi);
       __syncthreads();
       if (lane == 0) {
-        sh.red[0][warp] = lo;
-        sh.red[1][warp] = hi;
+        sh.c.red[0][warp] = lo;
+        sh.c.red[1][warp] = hi;
       }
       for (int i = tid; i < kSampBuckets; i += kSampThreads) {
         sh.whist[i] = 0;
@@ -655,8 +876,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
       if (tid < C) {
         u64 a = 0xffffffffu, b = 0;
         for (int w = 0; w < kSampWarps; ++w) {
-          a = min(a, sh.red[0][w]);
-          b = max(b, sh.red[1][w]);
+          a = min(a, sh.c.red[0][w]);
+          b = max(b, sh.c.red[1][w]);
         }
         dsm_st64(&sh.tot_c[rank], tid, a);
         dsm_st64(&sh.tot_w[rank], tid, b);
@@ -682,11 +903,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
       }
       const int shift = max(0, 32 - __clz(khi - klo) - 11);
       for (int i = tid; i < len; i += kSampThreads) {
-        const float z = as_float(src[i]);
+        const float z = as_float(ch.src[i]);
         const uint32_t key = sort_key(z);
         if (key >= klo && key <= khi && R.bucket(z) == bucket0) {
           atomicAdd(&sh.chist[(khi - key) >> shift], 1u);
-          if (use_p) atomicAdd(&sh.whist[(khi - key) >> shift], R.weight(z));
+          if (f.use_p) atomicAdd(&sh.whist[(khi - key) >> shift], R.weight(z));
         }
       }
       u64 c2[4], w2[4], b2c, b2w, t2c, t2w;
@@ -712,11 +933,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
     }
     // the members go to the first CTA and are sorted
     for (int i = tid; i < len; i += kSampThreads) {
-      const float z = as_float(src[i]);
+      const float z = as_float(ch.src[i]);
       const uint32_t key = sort_key(z);
       if (key >= klo && key <= khi && R.bucket(z) == bucket0) {
         const uint32_t at = dsm_add32(&sh.list_n, 0, 1);
-        if (at < kSampList) dsm_st64(&sh.list[at], 0, (static_cast<u64>(key) << 32) | static_cast<uint32_t>(~(c0 + i)));
+        if (at < kSampList) dsm_st64(&sh.list[at], 0, (static_cast<u64>(key) << 32) | static_cast<uint32_t>(~(ch.c0 + i)));
       }
     }
     samp_sync();
@@ -734,7 +955,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
           w[j] = R.weight(key_value(static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32)));
           c[j] = 1;
         }
-      block_scan2(c[0] + c[1], w[0] + w[1], &pc, &pw, &tc, &tw, sh.red);
+      block_scan2(c[0] + c[1], w[0] + w[1], &pc, &pw, &tc, &tw, sh.c.red);
       pc += bc;
       pw += bw;
 #pragma unroll
@@ -755,40 +976,38 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
   };
 
   u64 cut = 0;  // nothing is cut: every (key, id) is above
-  if (k > 0 || use_p || (use_m && !fast)) {
+  {
     u64 sum = 0;
-    for_chunk(src, len, mis, [&](float z, int) {
+    for_chunk(ch.src, len, ch.mis, [&](float z, int) {
       const int b = R.bucket(z);
       if (b < kSampBuckets) {
-        if (!fast) sum += R.fast_weight(z);
-        if (k > 0 || use_p) atomicAdd(&sh.chist[b], 1u);
-        if (use_p) atomicAdd(&sh.whist[b], R.weight(z));
+        sum += R.fast_weight(z);
+        if (f.k > 0 || f.use_p) atomicAdd(&sh.chist[b], 1u);
+        if (f.use_p) atomicAdd(&sh.whist[b], R.weight(z));
       }
     });
-    if (!fast) {
-      sum = warp_sum64(sum);
-      __syncthreads();
-      if (lane == 0) sh.red[0][warp] = sum;
-      __syncthreads();
-      if (tid < C) {
-        u64 t = 0;
-        for (int w = 0; w < kSampWarps; ++w) t += sh.red[0][w];
-        dsm_st64(&sh.tot_f[rank], tid, t);
-      }
+    sum = warp_sum64(sum);
+    __syncthreads();
+    if (lane == 0) sh.c.red[0][warp] = sum;
+    __syncthreads();
+    if (tid < C) {
+      u64 t = 0;
+      for (int w = 0; w < kSampWarps; ++w) t += sh.c.red[0][w];
+      dsm_st64(&sh.c.tot_f[rank], tid, t);
     }
   }
-  if (k > 0 || use_p) {
+  if (f.k > 0 || f.use_p) {
     merge(&before_c, &before_w, &all_c, &all_w);
     u64 kept_w = all_w;
-    if (k > 0 && all_c >= static_cast<u64>(k)) {
-      search(false, k, hc, hw, before_c, before_w);
-      finish(false, k);
+    if (f.k > 0 && all_c >= static_cast<u64>(f.k)) {
+      search(false, f.k, hc, hw, before_c, before_w);
+      finish(false, f.k);
       cut = sh.cut[0];
       kept_w = sh.cut[1];
       samp_sync();  // cut and found are read before they are written again
     }
-    if (use_p) {
-      const u64 target = p_target(kept_w);
+    if (f.use_p) {
+      const u64 target = f.p_target(kept_w);
       search(true, target, hc, hw, before_c, before_w);
       finish(true, target);
       cut = max(cut, sh.cut[0]);
@@ -798,22 +1017,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_kernel(const SampParam
   // ---- the token
   const int id = locate(
       [&](float z, int i) -> u64 {
-        if (filtered) {
-          const u64 x = (static_cast<u64>(sort_key(z)) << 32) | static_cast<uint32_t>(~i);
-          if (x < cut || R.y64(z) < low64) return 0;
-        }
-        return R.weight(z);
+        const u64 x = (static_cast<u64>(sort_key(z)) << 32) | static_cast<uint32_t>(~i);
+        return x < cut || R.y64(z) < f.low64 ? 0 : R.weight(z);
       },
-      draw_at);
+      [&](u64 all) { return f.draw_at(all); });
   if (id >= 0 && lane == 0) {
-    u64 exact = 0, rough = 0;
-    for (int r = 0; r < C; ++r) {
-      exact += sh.tot_l[r];
-      rough += sh.tot_f[r];
-    }
+    u64 rough = 0;
+    for (int r = 0; r < C; ++r) rough += sh.c.tot_f[r];
     p.tokens[row] = id;
     if (p.logprob)
-      p.logprob[row] = filtered ? log_prob(as_float(src[id - c0]), rough, kFastF) : log_prob(as_float(src[id - c0]), exact, R.F);
+      p.logprob[row] = samp_logprob(R, as_float(ch.src[id - ch.c0]), static_cast<double>(rough) / __hiloint2double((1023 + kFastF) << 20, 0));
   }
 }
 

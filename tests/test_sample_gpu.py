@@ -116,7 +116,7 @@ def test_scalar_times_row_temperature():
     shape = L.make_shape(5, 64, 777, temperature=row)
     shape.temperature = 0.5
     tok, lp = torch.empty(5, dtype=torch.int32, device="cuda"), torch.empty(5, device="cuda")
-    ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+    ws = L.workspace(shape, L.ENTRY_SAMPLE, "cuda")
     L.lmh_sample(shape, L.make_sampling(5, top_k=9), z, u, tok, lp, workspace=ws)
     ref = L.sample(z, u, temperature=row * 0.5, top_k=9)
     assert torch.equal(tok, ref["tokens"]) and torch.equal(lp, ref["logprob"])
