@@ -173,12 +173,13 @@ size_t norm_bwd_bytes(int64_t N, int64_t d) {
 
 // ------------------------------------------------------------------------ sampling workspace
 struct SampSpace {
-  size_t gmax, gsum, total;
+  size_t gsum, rsum, gmax, total;
 };
 SampSpace sample_space(int64_t N, int64_t V) {
   SampSpace s;
   s.gsum = sizeof(WsHeader);
-  s.gmax = align_up(s.gsum + static_cast<size_t>(N) * cdiv(V, kSum) * 8);
+  s.rsum = align_up(s.gsum + static_cast<size_t>(N) * cdiv(V, kSum) * 8);
+  s.gmax = align_up(s.rsum + static_cast<size_t>(N) * 8);
   s.total = align_up(s.gmax + static_cast<size_t>(N) * cdiv(V, kGroup) * 4);
   return s;
 }

@@ -237,33 +237,23 @@ extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
 
 namespace {
 
-// How the row kernel splits a row: CTAs per row (1, 2, 4 or 8), logits per CTA, whether they are
-// copied to shared memory. No result depends on it. With many rows one CTA each keeps the GPU
-// busy without waiting for others; few rows are spread over as many SMs as there are.
-struct SampPlan {
-  int C, L, chunk;  // chunk: bytes of shared memory, 0 if it is not kept
-};
-SampPlan sample_plan(int64_t N, int64_t V, int esize, int sms) {
+// CTAs per row of the row kernel: 1, 2, 4 or 8. No result depends on it. With many rows one CTA
+// each keeps the GPU busy without waiting for others; few rows are spread over more SMs.
+int sample_cluster(int64_t N, int64_t V, int sms) {
   int C = 1;
   while (C < kSampMaxC && N * C * 2 <= sms && V / (2 * C) >= 4096) C *= 2;
-  SampPlan p;
-  p.C = C;
-  p.L = static_cast<int>(cdiv(cdiv(V, C), 8) * 8);
-  const int64_t bytes = static_cast<int64_t>(p.L) * esize + 16;  // 16: the row's alignment
-  p.chunk = bytes <= kMaxDynSmem - static_cast<int64_t>(sizeof(RowShared)) ? static_cast<int>(bytes) : 0;
-  return p;
+  return C;
 }
 
 // The kernels of one call, each waiting for the one before at its own start, so that its launch
 // overlaps that one's end.
 template <class K>
-lmh_status launch_sample(K kernel, const SampParams& p, int64_t grid, int threads, size_t smem,
-                         int cluster, bool follows, cudaStream_t st) {
+lmh_status launch_sample(K kernel, const SampParams& p, int64_t grid, int threads, int cluster,
+                         bool follows, cudaStream_t st) {
   if (grid > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   int n = 0;
@@ -288,29 +278,22 @@ lmh_status launch_sample(K kernel, const SampParams& p, int64_t grid, int thread
   return last_launch();
 }
 
-// by_group: a row may be drawn from its groups' records; may_leave: one may be left by that.
+// may_leave: a row may be left to the row kernel.
 template <class T>
-lmh_status run_sample(SampParams p, bool by_group, bool may_leave, int dev, int sms, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  if (by_group) {
-    {
-      ProfScope ps(KID_SAMPLE_GROUPS, st);
-      LMH_TRY(launch_sample(sample_groups_kernel<T>, p, p.N * cdiv(p.g256, kGroupWarps * kGroupPer),
-                            32 * kGroupWarps, 0, 0, false, st));
-    }
-    ProfScope ps(KID_SAMPLE, st);
-    LMH_TRY(launch_sample(sample_list_kernel<T>, p, p.N, kSampThreads, 0, 0, true, st));
-    if (!may_leave) return LMH_OK;
+lmh_status run_sample(SampParams p, bool may_leave, int sms, cudaStream_t st) {
+  {
+    ProfScope ps(KID_SAMPLE_GROUPS, st);
+    LMH_TRY(launch_sample(sample_groups_kernel<T>, p, p.N * cdiv(p.g256, kGroupWarps * kGroupPer),
+                          32 * kGroupWarps, 0, false, st));
   }
-  p.all_rows = by_group ? 0 : 1;
-  const SampPlan plan = sample_plan(p.N, p.V, sizeof(T), sms);
-  p.C = plan.C;
-  p.L = plan.L;
-  p.resident = plan.chunk > 0 ? 1 : 0;
-  LMH_TRY(allow_smem(sample_row_kernel<T>, kMaxDynSmem, dev, &done));
+  {
+    ProfScope ps(KID_SAMPLE, st);
+    LMH_TRY(launch_sample(sample_list_kernel<T>, p, p.N, kSampThreads, 0, true, st));
+  }
+  if (!may_leave) return LMH_OK;
+  p.C = sample_cluster(p.N, p.V, sms);
   ProfScope ps(KID_SAMPLE_ROWS, st);
-  return launch_sample(sample_row_kernel<T>, p, p.N * plan.C, kSampThreads, sizeof(RowShared) + plan.chunk, plan.C,
-                       by_group, st);
+  return launch_sample(sample_row_kernel<T>, p, p.N * p.C, kSampThreads, p.C, true, st);
 }
 
 }  // namespace
@@ -345,6 +328,7 @@ extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt
   const SampSpace space = sample_space(shape->N, shape->V);
   p.gmax = ws.at<float>(space.gmax);
   p.gsum = ws.at<double>(space.gsum);
+  p.rsum = ws.at<double>(space.rsum);
   int bits = 0;  // V <= 2^bits weights of up to 2^F stay below 2^62
   while ((1LL << bits) < shape->V) ++bits;
   p.F = 62 - bits < 50 ? 62 - bits : 50;
@@ -361,13 +345,10 @@ extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt
   p.tokens = tokens;
   p.logprob = logprob;
   p.err = &ws.h->err;
-  // what each row's kernel is, its own parameters say on the device; from the scalars alone the
-  // host sees when no row goes by its groups, and when none of those can be left
-  const bool rows = opt->row_top_k || opt->row_top_p || opt->row_min_p;
-  const int64_t k = opt->top_k > 0 && opt->top_k < shape->V ? opt->top_k : 0;
-  const bool filtered = k > 0 || opt->top_p < 1.f || opt->min_p > 0.f;
-  const bool by_group = rows || k <= kSampListK || shape->V <= kSampList;
-  const bool may_leave = shape->V > kSampList && (rows || filtered);
-  return dtype == LMH_DTYPE_F32 ? run_sample<float>(p, by_group, may_leave, dev, sms, st)
-                                : run_sample<__nv_bfloat16>(p, by_group, may_leave, dev, sms, st);
+  // from the scalars alone the host sees when no row can be left to the row kernel
+  const bool filtered = opt->row_top_k || opt->row_top_p || opt->row_min_p ||
+                        (opt->top_k > 0 && opt->top_k < shape->V) || opt->top_p < 1.f || opt->min_p > 0.f;
+  const bool may_leave = shape->V > kSampList && filtered;
+  return dtype == LMH_DTYPE_F32 ? run_sample<float>(p, may_leave, sms, st)
+                                : run_sample<__nv_bfloat16>(p, may_leave, sms, st);
 }

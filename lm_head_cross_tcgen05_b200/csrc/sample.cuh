@@ -15,8 +15,12 @@
 //  * sample_row_kernel takes the rows left over (long prefixes), a cluster of 1 to 8 CTAs each. A
 //    prefix that reaches a count or a weight is found by a histogram over 2048 linear buckets of
 //    (zmax - z) / tau, whose threshold bucket's few members go to the first CTA and are sorted
-//    there. A bucket with too many members (equal logits, mostly) is split again by the bits of
-//    its keys until they fit or are all equal; equal ones are counted in vocabulary order.
+//    there. Adding every weight to its bucket in shared memory would cost more than the rest, so
+//    counts of an eighth of the row first give a window of buckets; the pass over the row adds
+//    what lies above the window in registers and only the window's weights to buckets, and is
+//    repeated with all buckets if the prefix does not end in the window. A bucket with too many
+//    members (equal logits, mostly) is split again by the bits of its keys until they fit or are
+//    all equal; equal ones are counted in vocabulary order.
 //
 // Where a token depends on sums of weights, the weights are whole numbers, so that no order of
 // addition can change it: w(z) = round(2^F exp((z - zmax) / tau)), computed in fp64, with 2^F as
@@ -38,14 +42,14 @@ constexpr int kSampListK = 512;   // largest top-k that takes the list
 constexpr int kSampMaxC = 8;
 constexpr int kGroup = 32;        // logits per maximum
 constexpr int kSum = 256;         // logits per sum
-constexpr int kFastF = 40;        // the row kernel's fast weights are fractions of 2^40
+constexpr int kBatch = 16;        // groups that a warp of the row kernel loads at once
+constexpr int kParts = 64;        // partial sums per warp that locate() keeps
 constexpr int kSampPending = -2;  // tokens[row] of a row that the list kernel leaves
 
 struct SampParams {
   long long N;
-  int V, L, C;          // row length, chunk per CTA, CTAs per row
+  int V, C;             // row length; row kernel: CTAs per row
   int F;                // weights are fractions of 2^F
-  int resident;         // the chunk is copied to shared memory
   const void* logits;   // [N, V]
   const float* u;       // [N]
   float tau;            // scalar temperature (1: none)
@@ -61,7 +65,7 @@ struct SampParams {
   int g32, g256;        // groups per row
   float* gmax;          // [N, g32] largest logit of each 32 (NaN if one is)
   double* gsum;         // [N, g256] sum of exp((z - max) / tau) over each 256, max their largest
-  int all_rows;         // row kernel: every row, not only those left by the list kernel
+  double* rsum;         // [N] sum of exp((z - zmax) / tau), of the rows left by the list kernel
 };
 
 typedef unsigned long long u64;
@@ -75,17 +79,15 @@ __device__ __forceinline__ void samp_sync() {
 __device__ __forceinline__ void dsm_st64(const void* p, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_to_rank(smem_u32(p), rank)), "l"(v) : "memory");
 }
-__device__ __forceinline__ void dsm_st32f(const void* p, uint32_t rank, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_u32(p), rank)), "f"(v) : "memory");
-}
 __device__ __forceinline__ u64 dsm_ld64(const void* p, uint32_t rank) {
   u64 v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t dsm_ld32(const void* p, uint32_t rank) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
+__device__ __forceinline__ uint4 dsm_ld128(const void* p, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
   return v;
 }
 __device__ __forceinline__ uint32_t dsm_add32(const void* p, uint32_t rank, uint32_t x) {
@@ -105,11 +107,6 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-struct SampCommon {
-  double table[64];                        // 2^(j / 64)
-  u64 red[2][kSampWarps];
-  u64 tot_m[kSampMaxC], tot_f[kSampMaxC];  // per CTA, written by each into all: maximum, fast sum
-};
 struct ListShared {
   double table[64];
   u64 red[2][kSampWarps];
@@ -122,27 +119,42 @@ struct ListShared {
   int pick[2];
   u64 base;
 };
-struct alignas(16) RowShared {
-  SampCommon c;
-  union {
-    u64 whist[kSampBuckets];  // dead once merge() has brought its sums into registers
-    u64 list[kSampList];      // as above
-  };
-  uint32_t chist[kSampBuckets];
-  u64 tot_c[kSampMaxC], tot_w[kSampMaxC], tot_l[kSampMaxC];  // per CTA, written by each into all
-  u64 warp_sum[kSampWarps];
-  u64 found[4];                            // bucket, its count, count before, weight before
-  u64 cut[2];                              // (key << 32 | ~id) of the last kept, weight kept
+struct RowShared {
+  double table[64];
+  u64 red[2][kSampWarps];
+  u64 whist[kSampBuckets];
+  uint4 chist[kSampBuckets / 4];
+  u64 list[kSampList];                       // members of a bucket, on the cluster's first CTA
+  u64 part[kSampWarps][kParts];              // locate(): partial sums of each warp's segment
+  u64 tot_a[kSampMaxC], tot_b[kSampMaxC];    // per CTA, written by each into all
+  u64 tot_l[kSampMaxC];                      // the same, of locate()
+  u64 found[4];                              // bin, its members, count before, weight before
+  u64 cut;                                   // (key << 32 | ~id) of the last kept
   uint32_t list_n;
+  int hit, window[2];
 };
 
-static_assert(sizeof(RowShared) % 16 == 0, "the row's copy follows, in 16-byte vectors");
+// 2^up 2^(y / 64) as e * sc: with n the whole number next to y and g = (y - n) ln2 / 64, the
+// table's 2^(n / 64) times the Taylor polynomial of e^g, |g| <= ln2 / 128, whose first left-out
+// term is below 4e-17. |y| < 2^31 and a normal result.
+__device__ __forceinline__ void exp2_64(double y, int up, const double* table, double* e, double* sc) {
+  const double m = y + 6755399441055744.0;  // 1.5 * 2^52: the low bits hold n
+  const int n = __double2loint(m);
+  const double f = y - (m - 6755399441055744.0);
+  constexpr double a = 0.6931471805599453 / 64;
+  double x = fma(f, a * a * a * a * a / 120, a * a * a * a / 24);
+  x = fma(f, x, a * a * a / 6);
+  x = fma(f, x, a * a / 2);
+  x = fma(f, x, a);
+  *e = fma(f, x, 1.0);
+  const double tb = table[n & 63];
+  *sc = __hiloint2double(__double2hiint(tb) + ((up + (n >> 6)) << 20), __double2loint(tb));
+}
 
 // What a row's threads share about it.
 struct SampRow {
   double zmaxd, c64;             // zmax; 64 log2(e) / tau
   float half_max, bucket_scale;  // zmax / 2, 2 * 2048 / F * log2(e) / tau
-  float zmax, c32;               // 2 log2(e) / tau
   int F;
   const double* table;
 
@@ -153,33 +165,19 @@ struct SampRow {
   }
   // 64 log2 of the probability over the largest one's
   __device__ __forceinline__ double y64(float z) const { return (static_cast<double>(z) - zmaxd) * c64; }
-  // 2^F 2^(y / 64): with n the whole number next to y and g = (y - n) ln2 / 64, the table's
-  // 2^(n / 64) times the Taylor polynomial of e^g, |g| <= ln2 / 128, whose first left-out term
-  // is below 4e-17. Whole numbers are taken from the low bits of sums with 2^52, which costs an
-  // addition where a conversion of 64-bit types runs at a fraction of that rate.
+  // 2^F 2^(y / 64) as a whole number, read from the low bits of a sum with 2^52: an addition
+  // where a conversion of 64-bit types runs at a fraction of that rate
   __device__ __forceinline__ u64 weight(float z) const {
     const double y = y64(z);
     if (y < -64.0 * (F + 1)) return 0;
-    const double m = y + 6755399441055744.0;  // 1.5 * 2^52
-    const int n = __double2loint(m);
-    const double f = y - (m - 6755399441055744.0);
-    constexpr double a = 0.6931471805599453 / 64;
-    double e = fma(f, a * a * a * a * a / 120, a * a * a * a / 24);
-    e = fma(f, e, a * a * a / 6);
-    e = fma(f, e, a * a / 2);
-    e = fma(f, e, a);
-    e = fma(f, e, 1.0);
-    const double tb = table[n & 63];
-    const double sc = __hiloint2double(__double2hiint(tb) + ((F + (n >> 6)) << 20), __double2loint(tb));
+    double e, sc;
+    exp2_64(y, F, table, &e, &sc);
     return static_cast<u64>(__double_as_longlong(fma(e, sc, 4503599627370496.0))) - 0x4330000000000000ull;
   }
-  // 2^40 2^(y / 64), from an fp32 exponential
-  __device__ __forceinline__ u64 fast_weight(float z) const {
-    return __float2ull_rn(fast_exp2(-fmaf(-0.5f, z, half_max) * c32) * 1099511627776.f);
-  }
 };
-// Bound on the relative error of a row's sum of fp32 exponentials 2^y: 2^-22 of ex2.approx, three
-// roundings of y (|y| <= 50 where it matters), 50 * 3 * 2^-24 * ln2 < 2^-17, and 13 additions.
+// Bound on the relative error of a row's sum of fp32 exponentials 2^y: 2^-22 of ex2.approx, four
+// roundings of y (|y| <= 50 where it matters), 50 * 4 * 2^-24 * ln2 < 2^-16.8, and 13 additions
+// (2^-24 each).
 constexpr double kFastErr = 1.0 / 65536;
 
 __device__ __forceinline__ u64 warp_sum64(u64 x) {
@@ -240,102 +238,10 @@ __device__ __forceinline__ void bitonic_desc(u64* a, int P) {
   __syncthreads();
 }
 
-// f(z, i) over the chunk, 16 bytes a load where the row's alignment allows. `mis`: elements by
-// which p lies past a 16-byte boundary.
-template <class T, class Fn>
-__device__ __forceinline__ void for_chunk(const T* p, int len, int mis, Fn f) {
-  constexpr int E = 16 / sizeof(T);
-  const int head = min(len, mis ? E - mis : 0);
-  const int nv = (len - head) / E;
-  if (static_cast<int>(threadIdx.x) < head) f(as_float(p[threadIdx.x]), static_cast<int>(threadIdx.x));
-  const uint4* v = reinterpret_cast<const uint4*>(p + head);
-#pragma unroll 2
-  for (int j = threadIdx.x; j < nv; j += kSampThreads) {
-    const uint4 w = v[j];
-    const T* e = reinterpret_cast<const T*>(&w);
-#pragma unroll
-    for (int q = 0; q < E; ++q) f(as_float(e[q]), head + j * E + q);
-  }
-  const int i = head + nv * E + threadIdx.x;
-  if (i < len) f(as_float(p[i]), i);
-}
-
-// The place of this CTA's chunk of a row.
-template <class T>
-struct SampChunk {
-  const T* gsrc;
-  T* chunk;       // its copy in shared memory, aligned as the row is
-  const T* src;   // the copy, or the row itself where it does not fit
-  int c0, len, mis;
-  __device__ __forceinline__ SampChunk(const SampParams& p, long long row, uint32_t rank, uint8_t* room) {
-    c0 = static_cast<int>(min(static_cast<long long>(rank) * p.L, static_cast<long long>(p.V)));
-    len = min(p.L, p.V - c0);
-    gsrc = static_cast<const T*>(p.logits) + row * p.V + c0;
-    mis = static_cast<int>((reinterpret_cast<uintptr_t>(gsrc) & 15) / sizeof(T));
-    chunk = reinterpret_cast<T*>(room) + mis;
-    src = p.resident ? chunk : gsrc;
-  }
-};
-
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
-}
-
-// Copies the chunk to shared memory (where it fits) and returns this thread's largest logit, NaN
-// if it saw one.
-template <class T>
-__device__ __forceinline__ float load_chunk(const SampParams& p, const SampChunk<T>& k) {
-  constexpr int E = 16 / sizeof(T);
-  const int tid = threadIdx.x;
-  float tmax = -INFINITY;
-  const int head = min(k.len, k.mis ? E - k.mis : 0);
-  const int nv = (k.len - head) / E;
-  auto one = [&](int i) {
-    const T t = k.gsrc[i];
-    if (p.resident) k.chunk[i] = t;
-    tmax = max_nan(tmax, as_float(t));
-  };
-  if (tid < head) one(tid);
-  if (head + nv * E + tid < k.len) one(head + nv * E + tid);
-  const uint4* gv = reinterpret_cast<const uint4*>(k.gsrc + head);
-  uint4* sv = reinterpret_cast<uint4*>(k.chunk + head);
-  for (int j0 = tid; j0 < nv; j0 += 4 * kSampThreads) {
-    uint4 w[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (j0 + q * kSampThreads < nv) w[q] = p.resident ? __ldcs(gv + j0 + q * kSampThreads) : gv[j0 + q * kSampThreads];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (j0 + q * kSampThreads < nv) {
-        if (p.resident) sv[j0 + q * kSampThreads] = w[q];
-        const T* e = reinterpret_cast<const T*>(&w[q]);
-#pragma unroll
-        for (int x = 0; x < E; ++x) tmax = max_nan(tmax, as_float(e[x]));
-      }
-  }
-  return tmax;
-}
-
-// The row's maximum from the threads' (NaN: one is NaN), in every thread of the cluster. Contains
-// the cluster barrier before which every CTA has started.
-__device__ __forceinline__ float row_max(float tmax, SampCommon& sh, uint32_t rank, int C) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool bad = __any_sync(0xffffffffu, tmax != tmax);
-  const uint32_t kmax = __reduce_max_sync(0xffffffffu, bad ? 0u : sort_key(tmax));
-  __syncthreads();
-  if (lane == 0) sh.red[0][warp] = (static_cast<u64>(bad) << 32) | kmax;
-  __syncthreads();
-  if (tid < C) {
-    u64 m = 0;
-    for (int w = 0; w < kSampWarps; ++w) m = max(m, sh.red[0][w]);  // a NaN above every key
-    dsm_st64(&sh.tot_m[rank], tid, m);
-  }
-  samp_sync();
-  u64 m = 0;
-  for (int r = 0; r < C; ++r) m = max(m, sh.tot_m[r]);
-  return (m >> 32) != 0 ? NAN : key_value(static_cast<uint32_t>(m));
 }
 
 __device__ __forceinline__ void cluster_arrive() {
@@ -381,18 +287,23 @@ struct SampFilter {
     const u64 t = top_p > 0.f ? __double2ull_ru(static_cast<double>(top_p) * static_cast<double>(all)) : 1;
     return t < 1 ? 1 : (t > all ? all : t);
   }
-  // Whether the row goes by its groups, and whether their sums have to be exact: nothing but the
-  // sums then decides the token.
-  __device__ __forceinline__ bool grouped(int V) const { return V <= kSampList || k <= kSampListK; }
+  // Whether the list kernel may draw the row: nothing is filtered, or the prefix may be short.
+  __device__ __forceinline__ bool listed(int V) const { return V <= kSampList || k <= kSampListK; }
   __device__ __forceinline__ bool exact() const { return k == 0 && !use_p && !use_m; }
 };
+// SampFilter::exact() of a row: its groups' sums alone decide the token, so they are fp64.
+__device__ __forceinline__ bool samp_exact(const SampParams& p, long long row) {
+  const int k = p.row_top_k ? p.row_top_k[row] : p.top_k;
+  const float top_p = p.row_top_p ? p.row_top_p[row] : p.top_p;
+  const float min_p = p.row_min_p ? p.row_min_p[row] : p.min_p;
+  return (k <= 0 || k >= p.V) && !(top_p < 1.f) && !(min_p > 0.f);
+}
 
 __device__ __forceinline__ SampRow samp_row(const SampParams& p, float zmax, double tau, const double* table) {
   const double c = 1.4426950408889634 / tau;
   SampRow R;
   R.zmaxd = zmax;
   R.c64 = 64.0 * c;
-  R.c32 = static_cast<float>(fmin(2.0 * c, 3e38));
   R.half_max = 0.5f * zmax;
   R.bucket_scale = static_cast<float>(fmin(c * (2.0 * kSampBuckets / p.F), 3e38));
   R.F = p.F;
@@ -420,17 +331,15 @@ __device__ __forceinline__ float warp_max_nan(float x) {
   return r;
 }
 
-// One warp per 256 logits of a row, two such per warp so that 16 loads are under way.
+// One warp per 256 logits of a row at a time, two such under way.
 constexpr int kGroupWarps = 8, kGroupPer = 2;
 template <class T>
 __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const SampParams p) {
+  __shared__ double table[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_row = (p.g256 + kGroupWarps * kGroupPer - 1) / (kGroupWarps * kGroupPer);
   const long long row = blockIdx.x / per_row;
   const int g0 = (static_cast<int>(blockIdx.x - row * per_row) * kGroupWarps + warp) * kGroupPer;
-  if (g0 >= p.g256) return;
-  const SampFilter f(p, row);
-  if (!f.grouped(p.V)) return;
   const T* src = static_cast<const T*>(p.logits) + row * p.V;
   float z[kGroupPer][8];
 #pragma unroll
@@ -440,8 +349,18 @@ __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const S
       const long long i = static_cast<long long>(g0 + q) * kSum + j * kGroup + lane;
       z[q][j] = i < p.V ? as_float(src[i]) : -INFINITY;
     }
-  const double c = 1.4426950408889634 / f.tau;
-  const float c2 = static_cast<float>(fmin(2.0 * c, 3e38));
+  float tau = 1.f;
+  if (p.row_tau) {
+    tau = p.row_tau[row];
+    if (!temperature_ok(tau)) tau = 1.f;
+  }
+  const bool exact = samp_exact(p, row);  // of the whole block
+  if (exact) {
+    if (threadIdx.x < 64) table[threadIdx.x] = exp2(threadIdx.x / 64.0);
+    __syncthreads();
+  }
+  const double c64 = exact ? 64.0 * 1.4426950408889634 / (static_cast<double>(tau) * p.tau) : 0.0;
+  const float c2 = fminf(2.8853900817779268f / p.tau / tau, 3e38f);  // 2 log2(e) / tau
 #pragma unroll
   for (int q = 0; q < kGroupPer; ++q) {
     if (g0 + q >= p.g256) break;
@@ -456,15 +375,23 @@ __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const S
     if (lane < 8 && g < p.g32) p.gmax[row * p.g32 + g] = mine;
     double s = 0.0;
     if (fabsf(m) <= 3.402823466e38f) {  // else no finite logit, or the row has no finite sum
-      if (f.exact()) {
+      if (exact) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s += exp2((static_cast<double>(z[q][j]) - m) * c);
+        for (int j = 0; j < 8; ++j) {
+          const double y = (static_cast<double>(z[q][j]) - m) * c64;
+          double e = 0.0, sc = 0.0;
+          if (y > -64.0 * 100) exp2_64(y, 0, table, &e, &sc);  // less cannot be drawn
+          s = fma(e, sc, s);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       } else {
         float e = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) e += fast_exp2(-fmaf(-0.5f, z[q][j], 0.5f * m) * c2);
+        for (int j = 0; j < 8; ++j) {
+          const float x = fmaf(-0.5f, z[q][j], 0.5f * m);
+          e += x < INFINITY ? fast_exp2(-x * c2) : 0.f;  // c2 may be 0
+        }
         s = warp_sum(e);
       }
     }
@@ -478,10 +405,6 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long row = blockIdx.x;
   const SampFilter f(p, row);
-  if (!f.grouped(p.V)) {
-    if (tid == 0) p.tokens[row] = kSampPending;
-    return;
-  }
   if (tid < 64) sh.table[tid] = exp2(tid / 64.0);
   if (tid < 2) sh.pick[tid] = kSampBuckets - 1;
   if (tid == 0) sh.list_n = sh.queue_n = 0;
@@ -573,6 +496,16 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
   if (lane == 0) sh.dred[warp] = part;
+  if (!f.listed(p.V)) {
+    __syncthreads();
+    if (tid == 0) {
+      double total = 0.0;
+      for (int w = 0; w < kSampWarps; ++w) total += sh.dred[w];
+      p.rsum[row] = total;
+      p.tokens[row] = kSampPending;
+    }
+    return;
+  }
 
   // ---- candidates lie in the buckets up to b0
   const bool all_listed = p.V <= kSampList;
@@ -713,109 +646,154 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       return;
     }
   }
-  if (tid == 0) p.tokens[row] = kSampPending;
+  if (tid == 0) {
+    p.rsum[row] = total;
+    p.tokens[row] = kSampPending;
+  }
 }
 
-// One row per cluster; it needs no other row's turn, so rows that are not pending cost an exit.
+// One row per cluster; rows that are not pending cost an exit.
 template <class T>
-__global__ void __launch_bounds__(kSampThreads, 1) sample_row_kernel(const SampParams p) {
-  extern __shared__ __align__(16) uint8_t dyn[];
-  RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
-  const uint32_t rank = cluster_ctarank();
-  const long long row = blockIdx.x / p.C;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list kernel's tokens
-  if (!p.all_rows && p.tokens[row] != kSampPending) return;  // in every CTA alike
-  if (threadIdx.x < 64) sh.c.table[threadIdx.x] = exp2(threadIdx.x / 64.0);
+__global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampParams p) {
+  __shared__ RowShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_ctarank();
   const int C = p.C;
+  const long long row = blockIdx.x / C;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list kernel's tokens
+  if (p.tokens[row] != kSampPending) return;          // in every CTA alike
+  cluster_arrive();  // before any CTA writes another's shared memory, all have started
   const SampFilter f(p, row);
-  cluster_arrive();
-  const SampChunk<T> ch(p, row, rank, dyn + sizeof(RowShared));
-  const int len = ch.len;
-  const float tmax = load_chunk(p, ch);
+  const T* src = static_cast<const T*>(p.logits) + row * p.V;
+  const float* gmax = p.gmax + row * p.g32;
+  uint32_t* chist = reinterpret_cast<uint32_t*>(sh.chist);
+  if (tid < 64) sh.table[tid] = exp2(tid / 64.0);
   if (tid == 0) sh.list_n = 0;
-  cluster_wait();
-  const float zmax = row_max(tmax, sh.c, rank, C);
-  if (no_sum(p, row, zmax, rank == 0 && tid == 0)) return;
-  if (f.flag && rank == 0 && tid == 0) atomicOr(p.err, f.flag);
-  const SampRow R = samp_row(p, zmax, f.tau, sh.c.table);
-  for (int i = tid; i < kSampBuckets; i += kSampThreads) {
-    sh.whist[i] = 0;
-    sh.chist[i] = 0;
-  }
+  float zmax = -INFINITY;
+  for (int g = tid; g < p.g32; g += kSampThreads) zmax = fmaxf(zmax, gmax[g]);  // finite: the list kernel saw it
+  zmax = warp_max_nan(zmax);
+  if (lane == 0) sh.red[0][warp] = __float_as_uint(zmax);
   __syncthreads();
+  for (int w = 0; w < kSampWarps; ++w) zmax = fmaxf(zmax, __uint_as_float(static_cast<uint32_t>(sh.red[0][w])));
+  const SampRow R = samp_row(p, zmax, f.tau, sh.table);
+  cluster_wait();
 
-  // Merges the CTAs' histograms: this thread's buckets of this CTA's slice (up to 4), what lies
-  // before them over the whole cluster, and the cluster's totals.
-  const int slice = kSampBuckets / C;
-  u64 hc[4], hw[4], before_c, before_w, all_c, all_w;
-  auto merge = [&](u64* bc, u64* bw, u64* tc, u64* tw) {
-    samp_sync();  // every CTA's histogram is complete
-    u64 sc = 0, sw = 0;
+  // groups [s0, s1) are this warp's: contiguous, in the order of the CTAs and their warps
+  const int per_cta = (p.g32 + C - 1) / C;
+  const int cta0 = min(p.g32, static_cast<int>(rank) * per_cta), cta1 = min(p.g32, cta0 + per_cta);
+  const int per_warp = ((cta1 - cta0 + kSampWarps - 1) / kSampWarps + kBatch - 1) / kBatch * kBatch;
+  const int s0 = min(cta1, cta0 + warp * per_warp), s1 = min(cta1, s0 + per_warp);
+  // fn(z, id) for every logit of the batch's groups whose maximum passes `pred` (-inf past the
+  // row's end)
+  auto batch = [&](int b, auto pred, auto fn) {
+    const bool mine = lane < kBatch && b + lane < s1;
+    const uint32_t mask = __ballot_sync(0xffffffffu, mine && pred(mine ? gmax[b + lane] : 0.f));
+    if (!mask) return;
+    float z[kBatch];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      hc[j] = hw[j] = 0;
-      const int per = (slice + kSampThreads - 1) / kSampThreads;
-      const int b = tid * per + j;
-      if (j < per && b < slice) {
-        for (int r = 0; r < C; ++r) {
-          hc[j] += dsm_ld32(&sh.chist[rank * slice + b], r);
-          hw[j] += dsm_ld64(&sh.whist[rank * slice + b], r);
-        }
-        sc += hc[j];
-        sw += hw[j];
-      }
+    for (int j = 0; j < kBatch; ++j) {
+      const long long i = static_cast<long long>(b + j) * kGroup + lane;
+      z[j] = ((mask >> j) & 1) && i < p.V ? as_float(src[i]) : -INFINITY;
     }
-    u64 xc, xw;
-    block_scan2(sc, sw, bc, bw, &xc, &xw, sh.c.red);
-    if (tid < C) {
-      dsm_st64(&sh.tot_c[rank], tid, xc);
-      dsm_st64(&sh.tot_w[rank], tid, xw);
-    }
-    samp_sync();
-    *tc = *tw = 0;
-    for (int r = 0; r < C; ++r) {
-      if (r == static_cast<int>(rank)) {
-        *bc += *tc;
-        *bw += *tw;
-      }
-      *tc += sh.tot_c[r];
-      *tw += sh.tot_w[r];
-    }
-  };
-  // The bucket in which the running count (by_w false) or weight reaches `target` (which the
-  // totals reach): sh.found = bucket, members, count before, weight before; in every CTA.
-  auto search = [&](bool by_w, u64 target, const u64* c, const u64* w, u64 bc, u64 bw) {
-    const int per = (slice + kSampThreads - 1) / kSampThreads;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const u64 lo = by_w ? bw : bc, hi = lo + (by_w ? w[j] : c[j]);
-      if (lo < target && target <= hi)
-        for (int r = 0; r < C; ++r) {
-          dsm_st64(&sh.found[0], r, static_cast<u64>(rank * slice + tid * per + j));
-          dsm_st64(&sh.found[1], r, c[j]);
-          dsm_st64(&sh.found[2], r, bc);
-          dsm_st64(&sh.found[3], r, bw);
-        }
-      bc += c[j];
-      bw += w[j];
-    }
-    samp_sync();
+    for (int j = 0; j < kBatch; ++j)
+      if ((mask >> j) & 1) fn(z[j], (b + j) * kGroup + lane);
   };
-  // The id at which the running sum, in vocabulary order, of fn(z, id) passes r (which the sum
-  // over the row does); -1 where another warp holds it. Each warp has a contiguous segment.
-  const int seg = ((len + kSampThreads - 1) / kSampThreads) * 32;
-  auto locate = [&](auto fn, auto target) -> int {
-    u64 s = 0;
-    const int s0 = min(len, warp * seg), s1 = min(len, s0 + seg);
-#pragma unroll 4
-    for (int i = s0 + lane; i < s1; i += 32) s += fn(as_float(ch.src[i]), ch.c0 + i);
-    s = warp_sum64(s);
-    if (lane == 0) sh.warp_sum[warp] = s;
+  auto compose = [](float z, int id) { return (static_cast<u64>(sort_key(z)) << 32) | static_cast<uint32_t>(~id); };
+  // Sums over the row of two values per thread, in every thread of the cluster.
+  auto sum2 = [&](u64 a, u64 b, u64* ta, u64* tb) {
+    a = warp_sum64(a);
+    b = warp_sum64(b);
     __syncthreads();
+    if (lane == 0) {
+      sh.red[0][warp] = a;
+      sh.red[1][warp] = b;
+    }
+    __syncthreads();
+    if (tid < C) {
+      u64 x = 0, y = 0;
+      for (int w = 0; w < kSampWarps; ++w) {
+        x += sh.red[0][w];
+        y += sh.red[1][w];
+      }
+      dsm_st64(&sh.tot_a[rank], tid, x);
+      dsm_st64(&sh.tot_b[rank], tid, y);
+    }
+    samp_sync();
+    *ta = *tb = 0;
+    for (int r = 0; r < C; ++r) {
+      *ta += sh.tot_a[r];
+      *tb += sh.tot_b[r];
+    }
+  };
+  auto zero = [&](bool w) {
+    for (int i = tid; i < kSampBuckets / 4; i += kSampThreads) sh.chist[i] = make_uint4(0, 0, 0, 0);
+    if (w)
+      for (int i = tid; i < kSampBuckets; i += kSampThreads) sh.whist[i] = 0;
+    __syncthreads();
+  };
+  // This thread's four bins of the cluster's histograms. The barrier before it has been passed.
+  auto bins = [&](bool w, u64 (&hc)[4], u64 (&hw)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) hc[j] = hw[j] = 0;
+    for (int r = 0; r < C; ++r) {
+      const uint4 h = dsm_ld128(&sh.chist[tid], r);
+      hc[0] += h.x;
+      hc[1] += h.y;
+      hc[2] += h.z;
+      hc[3] += h.w;
+      if (w)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) hw[j] += dsm_ld64(&sh.whist[tid * 4 + j], r);
+    }
+  };
+  // The bin in which the running count or weight, from (bc, bw), reaches the target: sh.found in
+  // every CTA, which each works out for itself; false if none does.
+  auto search = [&](bool by_w, u64 target, u64 bc, u64 bw) -> bool {
+    u64 hc[4], hw[4], pc, pw, tc, tw;
+    bins(by_w, hc, hw);
+    if (tid == 0) sh.hit = 0;
+    block_scan2(hc[0] + hc[1] + hc[2] + hc[3], hw[0] + hw[1] + hw[2] + hw[3], &pc, &pw, &tc, &tw, sh.red);
+    pc += bc;
+    pw += bw;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u64 lo = by_w ? pw : pc, hi = lo + (by_w ? hw[j] : hc[j]);
+      if (lo < target && target <= hi) {
+        sh.found[0] = tid * 4 + j;
+        sh.found[1] = hc[j];
+        sh.found[2] = pc;
+        sh.found[3] = pw;
+        sh.hit = 1;
+      }
+      pc += hc[j];
+      pw += hw[j];
+    }
+    samp_sync();  // also: every CTA has read the histograms
+    return sh.hit != 0;
+  };
+  // The id at which the running sum, in vocabulary order, of fn(z, id) passes r = target(sum over
+  // the row), fn being 0 in groups whose maximum fails `pred`; -1 where another warp holds it.
+  auto locate = [&](auto pred, auto fn, auto target) -> int {
+    const int nb = (s1 - s0 + kBatch - 1) / kBatch, span = (nb + kParts - 1) / kParts;  // batches per part
     u64 mine = 0;
-    for (int w = 0; w < kSampWarps; ++w) mine += sh.warp_sum[w];
-    if (tid < C) dsm_st64(&sh.tot_l[rank], tid, mine);
+    for (int q = 0; q < kParts; ++q) {
+      if (q * span >= nb) break;
+      u64 s = 0;
+      for (int b = q * span; b < min(nb, (q + 1) * span); ++b)
+        batch(s0 + b * kBatch, pred, [&](float z, int id) { s += fn(z, id); });
+      s = warp_sum64(s);
+      if (lane == 0) sh.part[warp][q] = s;
+      mine += s;
+    }
+    __syncthreads();
+    if (lane == 0) sh.red[0][warp] = mine;
+    __syncthreads();
+    if (tid < C) {
+      u64 x = 0;
+      for (int w = 0; w < kSampWarps; ++w) x += sh.red[0][w];
+      dsm_st64(&sh.tot_l[rank], tid, x);
+    }
     samp_sync();
     u64 base = 0, all = 0;
     for (int r = 0; r < C; ++r) {
@@ -823,123 +801,178 @@ __global__ void __launch_bounds__(kSampThreads, 1) sample_row_kernel(const SampP
       all += sh.tot_l[r];
     }
     const u64 r = target(all);
-    for (int w = 0; w < warp; ++w) base += sh.warp_sum[w];
-    if (!(base <= r && r < base + s)) return -1;
-    // the lane whose run of the segment holds it, then the place in that run
-    const int run = (s1 - s0 + 31) / 32;
-    const int r0 = min(s1, s0 + lane * run), r1 = min(s1, r0 + run);
-    u64 x = 0;
-    for (int i = r0; i < r1; ++i) x += fn(as_float(ch.src[i]), ch.c0 + i);
-    const u64 incl = warp_scan64(x, lane);
-    const int owner = __ffs(__ballot_sync(0xffffffffu, r < base + incl)) - 1;
-    base += __shfl_sync(0xffffffffu, incl - x, owner);
-    const int e1 = __shfl_sync(0xffffffffu, r1, owner);
-    for (int i0 = __shfl_sync(0xffffffffu, r0, owner); i0 < e1; i0 += 32) {
-      const int i = i0 + lane;
-      const u64 y = warp_scan64(i < e1 ? fn(as_float(ch.src[i]), ch.c0 + i) : 0, lane);
-      const uint32_t hit = __ballot_sync(0xffffffffu, r < base + y);
-      if (hit) return ch.c0 + i0 + __ffs(hit) - 1;
-      base += __shfl_sync(0xffffffffu, y, 31);
+    for (int w = 0; w < warp; ++w) base += sh.red[0][w];
+    if (!(base <= r && r < base + mine)) return -1;
+    int q = 0;
+    for (; q < kParts - 1; ++q) {
+      const u64 s = sh.part[warp][q];
+      if (r < base + s) break;
+      base += s;
     }
-    return -1;
+    int found = -1;
+    for (int b = q * span; b < min(nb, (q + 1) * span) && found < 0; ++b)
+      batch(s0 + b * kBatch, pred, [&](float z, int id) {
+        const u64 x = warp_scan64(fn(z, id), lane);
+        const uint32_t hit = __ballot_sync(0xffffffffu, r < base + x);
+        if (found < 0 && hit) found = __shfl_sync(0xffffffffu, id, __ffs(hit) - 1);
+        base += __shfl_sync(0xffffffffu, x, 31);
+      });
+    return found;
   };
 
-  // Shortest prefix that reaches the target in the bucket sh.found: sh.cut in every CTA.
-  auto finish = [&](bool by_w, u64 target) {
+  // The last candidate of the shortest prefix of those at or above `from` that reaches top-k's
+  // count (by_w false) or top-p's weight; 0 if all of them do not reach it.
+  auto prefix = [&](bool by_w, u64 from) -> u64 {
+    const float from_z = from ? key_value(static_cast<uint32_t>(from >> 32)) : -INFINITY;
+    auto in_range = [&](float m) { return m >= from_z && R.bucket(m) < kSampBuckets; };
+    // a window of buckets from an eighth of the row; all buckets for a short one
+    int lo = 0, hi = kSampBuckets - 1;
+    if (p.g32 > 64 * kBatch) {
+      zero(false);
+      int seen = 0;
+      for (int b = s0 + (warp & 7) * kBatch; b < s1; b += 8 * kBatch) {
+        seen += min(s1 - b, kBatch);
+        batch(b, in_range, [&](float z, int id) {
+          const int k = R.bucket(z);
+          if (k < kSampBuckets && compose(z, id) >= from) atomicAdd(&chist[k], 1u);
+        });
+      }
+      u64 groups, none;
+      sum2(lane == 0 ? seen : 0, 0, &groups, &none);
+      u64 hc[4], hw[4], pc, px, tc, tx;
+      bins(false, hc, hw);
+      if (tid == 0) {
+        sh.window[0] = 0;
+        sh.window[1] = kSampBuckets - 1;
+      }
+      u64 own = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // counts, or counts times the weight of the bucket's middle
+        hw[j] = by_w ? static_cast<u64>(static_cast<double>(hc[j]) * exp2(30.0 - (tid * 4 + j + 0.5) * p.F / kSampBuckets)) : hc[j];
+        own += hw[j];
+      }
+      block_scan2(own, 0, &pc, &px, &tc, &tx, sh.red);
+      const double t = by_w ? static_cast<double>(f.top_p) * static_cast<double>(tc)
+                            : static_cast<double>(f.k) * static_cast<double>(groups) / p.g32;
+      const double t0 = by_w ? 0.94 * t : 0.9 * t - 16.0, t1 = by_w ? t + 0.06 * static_cast<double>(tc) : 1.1 * t + 16.0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const double a = static_cast<double>(pc), b = static_cast<double>(pc + hw[j]);
+        if (a < t0 && t0 <= b) sh.window[0] = tid * 4 + j;
+        if (a < t1 && t1 <= b) sh.window[1] = tid * 4 + j;
+        pc += hw[j];
+      }
+      samp_sync();  // also: every CTA has read the histograms
+      lo = sh.window[0];
+      hi = sh.window[1];
+    }
+    u64 target = f.k;
+    for (int pass = 0; pass < 2; ++pass) {  // the second with all buckets, one of which holds it
+      zero(by_w);
+      u64 above = 0, total = 0;
+      for (int b = s0; b < s1; b += kBatch)
+        batch(b, in_range, [&](float z, int id) {
+          const int k = R.bucket(z);
+          if (k >= kSampBuckets || compose(z, id) < from) return;
+          const u64 w = by_w ? R.weight(z) : 1;
+          total += w;
+          if (k < lo) above += w;
+          else if (k <= hi) {
+            atomicAdd(&chist[k], 1u);
+            if (by_w) atomicAdd(&sh.whist[k], w);
+          }
+        });
+      u64 ta, tt;
+      sum2(above, total, &ta, &tt);
+      if (by_w) target = f.p_target(tt);
+      else if (tt < target) {
+        samp_sync();  // the sums are read before they are written again
+        return 0;
+      }
+      if (search(by_w, target, ta, ta)) break;
+      lo = 0;
+      hi = kSampBuckets - 1;
+    }
     const int bucket0 = static_cast<int>(sh.found[0]);
     u64 members = sh.found[1], bc = sh.found[2], bw = sh.found[3];
     uint32_t klo = 0, khi = 0xffffffffu;
+    auto has = [&](float m) { return R.bucket(m) <= bucket0; };
+    auto member = [&](float z, int id) {
+      const uint32_t key = sort_key(z);
+      return key >= klo && key <= khi && R.bucket(z) == bucket0 && compose(z, id) >= from;
+    };
     // 2048 ranges a level: after three levels a range is one key
     for (int level = 0; level < 4 && members > kSampList; ++level) {
-      // the members' smallest and largest key
-      uint32_t lo = 0xffffffffu, hi = 0;
-      for (int i = tid; i < len; i += kSampThreads) {
-        const float z = as_float(ch.src[i]);
-        const uint32_t key = sort_key(z);
-        if (key >= klo && key <= khi && R.bucket(z) == bucket0) {
-          lo = min(lo, key);
-          hi = max(hi, key);
-        }
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      __syncthreads();
+      uint32_t l = 0xffffffffu, h = 0;  // the members' smallest and largest key
+      for (int b = s0; b < s1; b += kBatch)
+        batch(b, has, [&](float z, int id) {
+          if (member(z, id)) {
+            l = min(l, sort_key(z));
+            h = max(h, sort_key(z));
+          }
+        });
+      l = __reduce_min_sync(0xffffffffu, l);
+      h = __reduce_max_sync(0xffffffffu, h);
+      zero(by_w);  // its barrier also parts the uses of red
       if (lane == 0) {
-        sh.c.red[0][warp] = lo;
-        sh.c.red[1][warp] = hi;
-      }
-      for (int i = tid; i < kSampBuckets; i += kSampThreads) {
-        sh.whist[i] = 0;
-        sh.chist[i] = 0;
+        sh.red[0][warp] = l;
+        sh.red[1][warp] = h;
       }
       __syncthreads();
       if (tid < C) {
-        u64 a = 0xffffffffu, b = 0;
+        u64 x = 0xffffffffu, y = 0;
         for (int w = 0; w < kSampWarps; ++w) {
-          a = min(a, sh.c.red[0][w]);
-          b = max(b, sh.c.red[1][w]);
+          x = min(x, sh.red[0][w]);
+          y = max(y, sh.red[1][w]);
         }
-        dsm_st64(&sh.tot_c[rank], tid, a);
-        dsm_st64(&sh.tot_w[rank], tid, b);
+        dsm_st64(&sh.tot_a[rank], tid, x);
+        dsm_st64(&sh.tot_b[rank], tid, y);
       }
       samp_sync();
       klo = 0xffffffffu;
       khi = 0;
       for (int r = 0; r < C; ++r) {
-        klo = min(klo, static_cast<uint32_t>(sh.tot_c[r]));
-        khi = max(khi, static_cast<uint32_t>(sh.tot_w[r]));
+        klo = min(klo, static_cast<uint32_t>(sh.tot_a[r]));
+        khi = max(khi, static_cast<uint32_t>(sh.tot_b[r]));
       }
       if (klo == khi) {  // equal logits: the first ones in vocabulary order
-        const u64 w = R.weight(key_value(klo));
-        const u64 need = by_w ? (target - bw + w - 1) / w : target - bc;
-        const int id = locate([&](float z, int) -> u64 { return sort_key(z) == klo; }, [&](u64) -> u64 { return need - 1; });
+        u64 need = target - bc;
+        if (by_w) {
+          const u64 w = R.weight(key_value(klo));
+          need = (target - bw + w - 1) / w;
+        }
+        const int id = locate(has, [&](float z, int i) -> u64 { return member(z, i); }, [&](u64) -> u64 { return need - 1; });
         if (id >= 0 && lane == 0)
-          for (int r = 0; r < C; ++r) {
-            dsm_st64(&sh.cut[0], r, (static_cast<u64>(klo) << 32) | static_cast<uint32_t>(~id));
-            dsm_st64(&sh.cut[1], r, bw + need * w);
-          }
+          for (int r = 0; r < C; ++r) dsm_st64(&sh.cut, r, (static_cast<u64>(klo) << 32) | static_cast<uint32_t>(~id));
         samp_sync();
-        return;
+        return sh.cut;
       }
       const int shift = max(0, 32 - __clz(khi - klo) - 11);
-      for (int i = tid; i < len; i += kSampThreads) {
-        const float z = as_float(ch.src[i]);
-        const uint32_t key = sort_key(z);
-        if (key >= klo && key <= khi && R.bucket(z) == bucket0) {
-          atomicAdd(&sh.chist[(khi - key) >> shift], 1u);
-          if (f.use_p) atomicAdd(&sh.whist[(khi - key) >> shift], R.weight(z));
-        }
-      }
-      u64 c2[4], w2[4], b2c, b2w, t2c, t2w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        c2[j] = hc[j];
-        w2[j] = hw[j];
-      }
-      merge(&b2c, &b2w, &t2c, &t2w);
-      search(by_w, target, hc, hw, bc + b2c, bw + b2w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {  // the linear histogram's buckets stay the thread's own
-        hc[j] = c2[j];
-        hw[j] = w2[j];
-      }
+      for (int b = s0; b < s1; b += kBatch)
+        batch(b, has, [&](float z, int id) {
+          if (member(z, id)) {
+            const int k = (khi - sort_key(z)) >> shift;
+            atomicAdd(&chist[k], 1u);
+            if (by_w) atomicAdd(&sh.whist[k], R.weight(z));
+          }
+        });
+      samp_sync();
+      search(by_w, target, bc, bw);
       members = sh.found[1];
       bc = sh.found[2];
       bw = sh.found[3];
       khi -= static_cast<uint32_t>(sh.found[0]) << shift;
       const uint32_t low = khi - ((1u << shift) - 1);
       klo = low > khi ? klo : max(klo, low);
-      samp_sync();  // found is read before a next search writes it
     }
     // the members go to the first CTA and are sorted
-    for (int i = tid; i < len; i += kSampThreads) {
-      const float z = as_float(ch.src[i]);
-      const uint32_t key = sort_key(z);
-      if (key >= klo && key <= khi && R.bucket(z) == bucket0) {
-        const uint32_t at = dsm_add32(&sh.list_n, 0, 1);
-        if (at < kSampList) dsm_st64(&sh.list[at], 0, (static_cast<u64>(key) << 32) | static_cast<uint32_t>(~(ch.c0 + i)));
-      }
-    }
+    for (int b = s0; b < s1; b += kBatch)
+      batch(b, has, [&](float z, int id) {
+        if (member(z, id)) {
+          const uint32_t at = dsm_add32(&sh.list_n, 0, 1);
+          if (at < kSampList) dsm_st64(&sh.list[at], 0, compose(z, id));
+        }
+      });
     samp_sync();
     if (rank == 0) {
       const int n = static_cast<int>(min(members, static_cast<u64>(kSampList)));
@@ -948,85 +981,37 @@ __global__ void __launch_bounds__(kSampThreads, 1) sample_row_kernel(const SampP
       for (int i = n + tid; i < P; i += kSampThreads) sh.list[i] = 0;
       __syncthreads();
       bitonic_desc(sh.list, P);
-      u64 w[2] = {0, 0}, c[2] = {0, 0}, pc, pw, tc, tw;
+      u64 x[2] = {0, 0}, px, pt, tx, tt;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        if (tid * 2 + j < n) {
-          w[j] = R.weight(key_value(static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32)));
-          c[j] = 1;
-        }
-      block_scan2(c[0] + c[1], w[0] + w[1], &pc, &pw, &tc, &tw, sh.c.red);
-      pc += bc;
-      pw += bw;
+        if (tid * 2 + j < n) x[j] = by_w ? R.weight(key_value(static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32))) : 1;
+      block_scan2(x[0] + x[1], 0, &px, &pt, &tx, &tt, sh.red);
+      px += by_w ? bw : bc;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const u64 lo = by_w ? pw : pc;
-        pc += c[j];
-        pw += w[j];
-        const u64 hi = by_w ? pw : pc;
-        if (lo < target && target <= hi)
-          for (int r = 0; r < C; ++r) {
-            dsm_st64(&sh.cut[0], r, sh.list[tid * 2 + j]);
-            dsm_st64(&sh.cut[1], r, pw);
-          }
+        if (px < target && target <= px + x[j])
+          for (int r = 0; r < C; ++r) dsm_st64(&sh.cut, r, sh.list[tid * 2 + j]);
+        px += x[j];
       }
       if (tid == 0) sh.list_n = 0;
     }
     samp_sync();
+    return sh.cut;
   };
 
-  u64 cut = 0;  // nothing is cut: every (key, id) is above
-  {
-    u64 sum = 0;
-    for_chunk(ch.src, len, ch.mis, [&](float z, int) {
-      const int b = R.bucket(z);
-      if (b < kSampBuckets) {
-        sum += R.fast_weight(z);
-        if (f.k > 0 || f.use_p) atomicAdd(&sh.chist[b], 1u);
-        if (f.use_p) atomicAdd(&sh.whist[b], R.weight(z));
-      }
-    });
-    sum = warp_sum64(sum);
-    __syncthreads();
-    if (lane == 0) sh.c.red[0][warp] = sum;
-    __syncthreads();
-    if (tid < C) {
-      u64 t = 0;
-      for (int w = 0; w < kSampWarps; ++w) t += sh.c.red[0][w];
-      dsm_st64(&sh.c.tot_f[rank], tid, t);
-    }
+  u64 cut = 0;  // every (key, id) is above
+  if (f.k > 0) cut = prefix(false, 0);
+  if (f.use_p) {
+    samp_sync();  // cut is read before it is written again
+    cut = prefix(true, cut);
   }
-  if (f.k > 0 || f.use_p) {
-    merge(&before_c, &before_w, &all_c, &all_w);
-    u64 kept_w = all_w;
-    if (f.k > 0 && all_c >= static_cast<u64>(f.k)) {
-      search(false, f.k, hc, hw, before_c, before_w);
-      finish(false, f.k);
-      cut = sh.cut[0];
-      kept_w = sh.cut[1];
-      samp_sync();  // cut and found are read before they are written again
-    }
-    if (f.use_p) {
-      const u64 target = f.p_target(kept_w);
-      search(true, target, hc, hw, before_c, before_w);
-      finish(true, target);
-      cut = max(cut, sh.cut[0]);
-    }
-  }
-
-  // ---- the token
-  const int id = locate(
-      [&](float z, int i) -> u64 {
-        const u64 x = (static_cast<u64>(sort_key(z)) << 32) | static_cast<uint32_t>(~i);
-        return x < cut || R.y64(z) < f.low64 ? 0 : R.weight(z);
-      },
-      [&](u64 all) { return f.draw_at(all); });
+  const float cut_z = cut ? key_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
+  const int id = locate([&](float m) { return m >= cut_z; },
+                        [&](float z, int i) -> u64 { return compose(z, i) < cut || R.y64(z) < f.low64 ? 0 : R.weight(z); },
+                        [&](u64 all) { return f.draw_at(all); });
   if (id >= 0 && lane == 0) {
-    u64 rough = 0;
-    for (int r = 0; r < C; ++r) rough += sh.c.tot_f[r];
     p.tokens[row] = id;
-    if (p.logprob)
-      p.logprob[row] = samp_logprob(R, as_float(ch.src[id - ch.c0]), static_cast<double>(rough) / __hiloint2double((1023 + kFastF) << 20, 0));
+    if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), p.rsum[row]);
   }
 }
 
