@@ -177,10 +177,11 @@ struct SampSpace {
 };
 SampSpace sample_space(int64_t N, int64_t V) {
   SampSpace s;
+  const size_t blocks = static_cast<size_t>(N) * cdiv(V, kBlock);
   s.gsum = sizeof(WsHeader);
-  s.rsum = align_up(s.gsum + static_cast<size_t>(N) * cdiv(V, kSum) * 8);
-  s.gmax = align_up(s.rsum + static_cast<size_t>(N) * 8);
-  s.total = align_up(s.gmax + static_cast<size_t>(N) * cdiv(V, kGroup) * 4);
+  s.rsum = align_up(s.gsum + blocks * 8);
+  s.gmax = align_up(s.rsum + static_cast<size_t>(N) * 16);
+  s.total = align_up(s.gmax + blocks * kGroups * 4);
   return s;
 }
 

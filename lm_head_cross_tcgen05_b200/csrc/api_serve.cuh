@@ -237,23 +237,24 @@ extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
 
 namespace {
 
-// CTAs per row of the row kernel: 1, 2, 4 or 8. No result depends on it. With many rows one CTA
-// each keeps the GPU busy without waiting for others; few rows are spread over more SMs.
-int sample_cluster(int64_t N, int64_t V, int sms) {
+// CTAs per row of the row kernel: 1, 2, 4 or 8, at least 4096 logits each. No result depends on
+// it. How many rows are left to that kernel only the device knows; it is made for few.
+int sample_cluster(int64_t V) {
   int C = 1;
-  while (C < kSampMaxC && N * C * 2 <= sms && V / (2 * C) >= 4096) C *= 2;
+  while (C < kSampMaxC && V / (2 * C) >= 4096) C *= 2;
   return C;
 }
 
 // The kernels of one call, each waiting for the one before at its own start, so that its launch
 // overlaps that one's end.
 template <class K>
-lmh_status launch_sample(K kernel, const SampParams& p, int64_t grid, int threads, int cluster,
-                         bool follows, cudaStream_t st) {
+lmh_status launch_sample(K kernel, const SampParams& p, int64_t grid, int threads, size_t smem,
+                         int cluster, bool follows, cudaStream_t st) {
   if (grid > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];
   int n = 0;
@@ -280,20 +281,26 @@ lmh_status launch_sample(K kernel, const SampParams& p, int64_t grid, int thread
 
 // may_leave: a row may be left to the row kernel.
 template <class T>
-lmh_status run_sample(SampParams p, bool may_leave, int sms, cudaStream_t st) {
+lmh_status run_sample(SampParams p, bool may_leave, int dev, cudaStream_t st) {
   {
     ProfScope ps(KID_SAMPLE_GROUPS, st);
-    LMH_TRY(launch_sample(sample_groups_kernel<T>, p, p.N * cdiv(p.g256, kGroupWarps * kGroupPer),
-                          32 * kGroupWarps, 0, false, st));
+    LMH_TRY(launch_sample(sample_groups_kernel<T>, p, p.N * cdiv(p.blocks, kGroupWarps * kGroupPer),
+                          32 * kGroupWarps, 0, 0, false, st));
   }
   {
     ProfScope ps(KID_SAMPLE, st);
-    LMH_TRY(launch_sample(sample_list_kernel<T>, p, p.N, kSampThreads, 0, true, st));
+    LMH_TRY(launch_sample(sample_list_kernel<T>, p, p.N, kSampThreads, 0, 0, true, st));
   }
   if (!may_leave) return LMH_OK;
-  p.C = sample_cluster(p.N, p.V, sms);
+  static std::atomic<uint64_t> done{0};
+  LMH_TRY(allow_smem(sample_row_kernel<T>, kMaxDynSmem, dev, &done));
+  p.C = sample_cluster(p.V);
+  p.L = static_cast<int>(cdiv(cdiv(p.V, p.C), 8) * 8);
+  size_t smem = sizeof(RowShared) + static_cast<size_t>(p.L) * sizeof(T) + 16;  // 16: the row's alignment
+  p.resident = smem <= kMaxDynSmem ? 1 : 0;
+  if (!p.resident) smem = sizeof(RowShared);
   ProfScope ps(KID_SAMPLE_ROWS, st);
-  return launch_sample(sample_row_kernel<T>, p, p.N * p.C, kSampThreads, p.C, true, st);
+  return launch_sample(sample_row_kernel<T>, p, p.N * p.C, kSampThreads, smem, p.C, true, st);
 }
 
 }  // namespace
@@ -323,8 +330,7 @@ extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt
   SampParams p{};
   p.N = shape->N;
   p.V = static_cast<int>(shape->V);
-  p.g32 = static_cast<int>(cdiv(shape->V, kGroup));
-  p.g256 = static_cast<int>(cdiv(shape->V, kSum));
+  p.blocks = static_cast<int>(cdiv(shape->V, kBlock));
   const SampSpace space = sample_space(shape->N, shape->V);
   p.gmax = ws.at<float>(space.gmax);
   p.gsum = ws.at<double>(space.gsum);
@@ -349,6 +355,6 @@ extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt
   const bool filtered = opt->row_top_k || opt->row_top_p || opt->row_min_p ||
                         (opt->top_k > 0 && opt->top_k < shape->V) || opt->top_p < 1.f || opt->min_p > 0.f;
   const bool may_leave = shape->V > kSampList && filtered;
-  return dtype == LMH_DTYPE_F32 ? run_sample<float>(p, may_leave, sms, st)
-                                : run_sample<__nv_bfloat16>(p, may_leave, sms, st);
+  return dtype == LMH_DTYPE_F32 ? run_sample<float>(p, may_leave, dev, st)
+                                : run_sample<__nv_bfloat16>(p, may_leave, dev, st);
 }

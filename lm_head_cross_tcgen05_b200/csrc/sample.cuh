@@ -2,18 +2,18 @@
 // uniform number. Candidates are ordered by logit, the largest first, equal ones by id; every
 // filter keeps a prefix of that order. Three kernels:
 //
-//  * sample_groups_kernel streams the logits once: the maximum of every 32 of a row, and the sum
-//    of exponentials of every 256 relative to their own maximum. This is the pass that is bound
+//  * sample_groups_kernel streams the logits once: of every 256 of a row (a block), eight maxima
+//    of 32 each and the sum of exponentials relative to the largest of them. This is the pass that is bound
 //    by memory; no thread waits for another beyond its warp.
 //  * sample_list_kernel, one CTA per row, draws the token from those records and a few logits.
 //    Unfiltered, the running sums of the groups lead to the one whose 256 logits decide. With a
-//    short prefix, everything that can be in it is collected and sorted (up to 1024 candidates):
+//    short prefix, everything that can be in it is collected and sorted (up to 2048 candidates):
 //    at least k logits lie at or above the k-th largest group maximum, so only groups whose
 //    maximum lies there are read again, 128 bytes for most of k candidates. A top-p prefix
-//    without top-k ends where the candidates' weight reaches a part of the whole sum, which is
-//    known from fp32 exponentials within a bound; if that does not decide it, the row is left.
-//  * sample_row_kernel takes the rows left over (long prefixes), a cluster of 1 to 8 CTAs each. A
-//    prefix that reaches a count or a weight is found by a histogram over 2048 linear buckets of
+//    without top-k ends where the candidates' weight reaches a part of the whole sum; 256 groups
+//    are tried, then 1024.
+//  * sample_row_kernel takes the rows left over (long prefixes), a cluster of 1 to 8 CTAs each,
+//    which hold the row in shared memory (where it fits; else they read it again). A prefix that reaches a count or a weight is found by a histogram over 2048 linear buckets of
 //    (zmax - z) / tau, whose threshold bucket's few members go to the first CTA and are sorted
 //    there. Adding every weight to its bucket in shared memory would cost more than the rest, so
 //    counts of an eighth of the row first give a window of buckets; the pass over the row adds
@@ -37,18 +37,19 @@ namespace lmh {
 constexpr uint32_t kErrSampling = 0x10u;
 constexpr int kSampThreads = 512, kSampWarps = kSampThreads / 32;
 constexpr int kSampBuckets = 2048;
-constexpr int kSampList = 1024;   // candidates that the first CTA sorts
-constexpr int kSampListK = 512;   // largest top-k that takes the list
+constexpr int kSampList = 2048;   // candidates that one CTA sorts
+constexpr int kSampListK = 1024;  // largest top-k that takes the list
 constexpr int kSampMaxC = 8;
-constexpr int kGroup = 32;        // logits per maximum
-constexpr int kSum = 256;         // logits per sum
-constexpr int kBatch = 16;        // groups that a warp of the row kernel loads at once
-constexpr int kParts = 64;        // partial sums per warp that locate() keeps
+constexpr int kBlock = 256;       // logits per sum of exponentials
+constexpr int kGroups = 8;        // maxima per block: group g has the logits 32 j + 4 g + i of the
+                                  // block, j < 8 and i < 4 (what four lanes load)
+constexpr int kParts = 16;        // partial sums per warp that locate() keeps
 constexpr int kSampPending = -2;  // tokens[row] of a row that the list kernel leaves
 
 struct SampParams {
   long long N;
-  int V, C;             // row length; row kernel: CTAs per row
+  int V;                // row length
+  int C, L, resident;   // row kernel: CTAs per row, logits per CTA, whether these are copied
   int F;                // weights are fractions of 2^F
   const void* logits;   // [N, V]
   const float* u;       // [N]
@@ -62,10 +63,10 @@ struct SampParams {
   int32_t* tokens;      // [N]
   float* logprob;       // [N] or null
   uint32_t* err;
-  int g32, g256;        // groups per row
-  float* gmax;          // [N, g32] largest logit of each 32 (NaN if one is)
-  double* gsum;         // [N, g256] sum of exp((z - max) / tau) over each 256, max their largest
-  double* rsum;         // [N] sum of exp((z - zmax) / tau), of the rows left by the list kernel
+  int blocks;           // blocks per row
+  float* gmax;          // [N, blocks, 8] largest logit of each group (NaN if one is NaN)
+  double* gsum;         // [N, blocks] sum of exp((z - max) / tau), max the block's largest
+  double* rsum;         // [N, 2] of the rows left by the list kernel: sum of exp((z - zmax) / tau), zmax
 };
 
 typedef unsigned long long u64;
@@ -111,28 +112,43 @@ struct ListShared {
   double table[64];
   u64 red[2][kSampWarps];
   double dred[kSampWarps];
-  u64 list[kSampList];       // candidates, key << 32 | ~id
-  u64 wlist[kSampList];      // their weights, once sorted
-  uint32_t queue[kSampList]; // groups that hold candidates
-  uint4 chist[kSampBuckets / 4];
+  u64 list[kSampList];           // candidates, key << 32 | ~id
+  union {
+    u64 wlist[kSampList];        // their weights, once sorted
+    struct {
+      uint32_t queue[kSampList]; // groups that hold candidates
+      uint4 chist[kSampBuckets / 4];
+    };
+  };
   uint32_t list_n, queue_n;
-  int pick[2];
+  int pick;
   u64 base;
 };
-struct RowShared {
+struct alignas(16) RowShared {
   double table[64];
   u64 red[2][kSampWarps];
-  u64 whist[kSampBuckets];
+  union {
+    u64 whist[kSampBuckets];     // dead once a search is done
+    u64 list[kSampList];         // members of a bucket, on the cluster's first CTA
+  };
   uint4 chist[kSampBuckets / 4];
-  u64 list[kSampList];                       // members of a bucket, on the cluster's first CTA
+  float keep[kSampWarps][64];                // weigh(): logits whose weights are still to be added
   u64 part[kSampWarps][kParts];              // locate(): partial sums of each warp's segment
-  u64 tot_a[kSampMaxC], tot_b[kSampMaxC];    // per CTA, written by each into all
-  u64 tot_l[kSampMaxC];                      // the same, of locate()
+  u64 tot_a[kSampMaxC], tot_l[kSampMaxC];    // per CTA, written by each into all: sum_row(), locate()
+  u64 tot_b[kSampMaxC];
   u64 found[4];                              // bin, its members, count before, weight before
   u64 cut;                                   // (key << 32 | ~id) of the last kept
   uint32_t list_n;
   int hit, window[2];
 };
+static_assert(sizeof(RowShared) % 16 == 0, "the row's copy follows, in 16-byte vectors");
+
+// A float as a double by its bits: a conversion runs at a quarter of this rate. Zeros and subnormal
+// numbers come out below 2^-125, infinities as +-2^128.
+__device__ __forceinline__ double widen(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return __hiloint2double(static_cast<int>((b & 0x80000000u) | (((b & 0x7fffffffu) >> 3) + 0x38000000u)), static_cast<int>(b << 29));
+}
 
 // 2^up 2^(y / 64) as e * sc: with n the whole number next to y and g = (y - n) ln2 / 64, the
 // table's 2^(n / 64) times the Taylor polynomial of e^g, |g| <= ln2 / 128, whose first left-out
@@ -164,22 +180,17 @@ struct SampRow {
     return x < static_cast<float>(kSampBuckets) ? static_cast<int>(x) : kSampBuckets;
   }
   // 64 log2 of the probability over the largest one's
-  __device__ __forceinline__ double y64(float z) const { return (static_cast<double>(z) - zmaxd) * c64; }
+  __device__ __forceinline__ double y64(float z) const { return (widen(z) - zmaxd) * c64; }
   // 2^F 2^(y / 64) as a whole number, read from the low bits of a sum with 2^52: an addition
   // where a conversion of 64-bit types runs at a fraction of that rate
   __device__ __forceinline__ u64 weight(float z) const {
     const double y = y64(z);
-    if (y < -64.0 * (F + 1)) return 0;
+    if (y < -64.0 * (F + 1) || !(z > -INFINITY)) return 0;
     double e, sc;
     exp2_64(y, F, table, &e, &sc);
     return static_cast<u64>(__double_as_longlong(fma(e, sc, 4503599627370496.0))) - 0x4330000000000000ull;
   }
 };
-// Bound on the relative error of a row's sum of fp32 exponentials 2^y: 2^-22 of ex2.approx, four
-// roundings of y (|y| <= 50 where it matters), 50 * 4 * 2^-24 * ln2 < 2^-16.8, and 13 additions
-// (2^-24 each).
-constexpr double kFastErr = 1.0 / 65536;
-
 __device__ __forceinline__ u64 warp_sum64(u64 x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -194,37 +205,43 @@ __device__ __forceinline__ u64 warp_scan64(u64 x, int lane) {  // inclusive
   return x;
 }
 
-// Exclusive prefix of two values over the block's threads, and their totals.
-__device__ __forceinline__ void block_scan2(u64 a, u64 b, u64* pa, u64* pb, u64* ta, u64* tb, u64 (*red)[kSampWarps]) {
+// Exclusive prefix of a value over the block's threads, and its total.
+__device__ __forceinline__ void block_scan(u64 a, u64* pa, u64* ta, u64* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const u64 ia = warp_scan64(a, lane), ib = warp_scan64(b, lane);
+  const u64 ia = warp_scan64(a, lane);
   __syncthreads();
-  if (lane == 31) {
-    red[0][warp] = ia;
-    red[1][warp] = ib;
-  }
+  if (lane == 31) red[warp] = ia;
   __syncthreads();
-  u64 ba = 0, bb = 0, sa = 0, sb = 0;
-  for (int w = 0; w < kSampWarps; ++w) {
-    if (w == warp) {
-      ba = sa;
-      bb = sb;
-    }
-    sa += red[0][w];
-    sb += red[1][w];
-  }
-  *pa = ba + ia - a;
-  *pb = bb + ib - b;
-  *ta = sa;
-  *tb = sb;
+  const u64 s = warp_scan64(lane < kSampWarps ? red[lane] : 0, lane);
+  const u64 before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+  *pa = (warp ? before : 0) + ia - a;
+  *ta = __shfl_sync(0xffffffffu, s, kSampWarps - 1);
 }
 
-// Sorts a[0 .. P) in descending order; P a power of two, at most 2 * kSampThreads. All threads.
-__device__ __forceinline__ void bitonic_desc(u64* a, int P) {
+// Sorts a[0 .. n) in descending order, all values different and not 0; a has room for the next
+// power of two. By counting the larger ones up to 256 values (n reads a thread, no barriers
+// between them), by a bitonic network above. All threads; a barrier before and after.
+__device__ __forceinline__ void sort_desc(u64* a, int n) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (n <= 256) {
+    const u64 x = tid < n ? a[tid] : 0;
+    int at = 0;
+    if (tid < n)
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) at += a[j] > x;
+    __syncthreads();
+    if (tid < n) a[at] = x;
+    __syncthreads();
+    return;
+  }
+  int P = 512;
+  while (P < n) P <<= 1;
+  for (int i = n + tid; i < P; i += kSampThreads) a[i] = 0;
+  __syncthreads();
   for (int size = 2; size <= P; size <<= 1)
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      const int t = threadIdx.x;
-      if (t < P / 2) {
+      for (int t = tid; t < P / 2; t += kSampThreads) {
         const int i = 2 * t - (t & (stride - 1)), j = i + stride;
         const u64 x = a[i], y = a[j];
         if ((x < y) == ((i & size) == 0)) {
@@ -232,10 +249,8 @@ __device__ __forceinline__ void bitonic_desc(u64* a, int P) {
           a[j] = x;
         }
       }
-      if (P > 64) __syncthreads();  // up to 64 are warp 0's own
-      else __syncwarp();
+      __syncthreads();
     }
-  __syncthreads();
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -287,22 +302,27 @@ struct SampFilter {
     const u64 t = top_p > 0.f ? __double2ull_ru(static_cast<double>(top_p) * static_cast<double>(all)) : 1;
     return t < 1 ? 1 : (t > all ? all : t);
   }
+  // A sum of weights, the largest being 1, in units of 2^-F.
+  __device__ __forceinline__ static u64 whole(double total, int F) {
+    return __double2ull_rn(total * __hiloint2double((1023 + F) << 20, 0));
+  }
   // Whether the list kernel may draw the row: nothing is filtered, or the prefix may be short.
   __device__ __forceinline__ bool listed(int V) const { return V <= kSampList || k <= kSampListK; }
-  __device__ __forceinline__ bool exact() const { return k == 0 && !use_p && !use_m; }
+  __device__ __forceinline__ bool off() const { return k == 0 && !use_p && !use_m; }
 };
-// SampFilter::exact() of a row: its groups' sums alone decide the token, so they are fp64.
+// Whether the sum of the whole row decides the token: nothing is filtered, or top-p is a part of
+// all. The blocks' sums are fp64 then; for the log-prob alone fp32 exponentials do.
 __device__ __forceinline__ bool samp_exact(const SampParams& p, long long row) {
   const int k = p.row_top_k ? p.row_top_k[row] : p.top_k;
   const float top_p = p.row_top_p ? p.row_top_p[row] : p.top_p;
   const float min_p = p.row_min_p ? p.row_min_p[row] : p.min_p;
-  return (k <= 0 || k >= p.V) && !(top_p < 1.f) && !(min_p > 0.f);
+  return (k <= 0 || k >= p.V) && (top_p < 1.f || !(min_p > 0.f));
 }
 
 __device__ __forceinline__ SampRow samp_row(const SampParams& p, float zmax, double tau, const double* table) {
   const double c = 1.4426950408889634 / tau;
   SampRow R;
-  R.zmaxd = zmax;
+  R.zmaxd = widen(zmax);
   R.c64 = 64.0 * c;
   R.half_max = 0.5f * zmax;
   R.bucket_scale = static_cast<float>(fmin(c * (2.0 * kSampBuckets / p.F), 3e38));
@@ -331,71 +351,74 @@ __device__ __forceinline__ float warp_max_nan(float x) {
   return r;
 }
 
-// One warp per 256 logits of a row at a time, two such under way.
+// One warp per block at a time, two under way.
 constexpr int kGroupWarps = 8, kGroupPer = 2;
 template <class T>
 __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const SampParams p) {
   __shared__ double table[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_row = (p.g256 + kGroupWarps * kGroupPer - 1) / (kGroupWarps * kGroupPer);
+  const int per_row = (p.blocks + kGroupWarps * kGroupPer - 1) / (kGroupWarps * kGroupPer);
   const long long row = blockIdx.x / per_row;
-  const int g0 = (static_cast<int>(blockIdx.x - row * per_row) * kGroupWarps + warp) * kGroupPer;
-  const T* src = static_cast<const T*>(p.logits) + row * p.V;
+  const int b0 = (static_cast<int>(blockIdx.x - row * per_row) * kGroupWarps + warp) * kGroupPer;
+  const T* src = static_cast<const T*>(p.logits) + row * p.V + static_cast<long long>(b0) * kBlock + lane;
+  const long long left = p.V - static_cast<long long>(b0) * kBlock - lane;  // logits from src on
   float z[kGroupPer][8];
+  if (left >= kGroupPer * kBlock) {
 #pragma unroll
-  for (int q = 0; q < kGroupPer; ++q)
+    for (int q = 0; q < kGroupPer; ++q)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const long long i = static_cast<long long>(g0 + q) * kSum + j * kGroup + lane;
-      z[q][j] = i < p.V ? as_float(src[i]) : -INFINITY;
-    }
+      for (int j = 0; j < 8; ++j) z[q][j] = as_float(src[q * kBlock + j * 32]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < kGroupPer; ++q)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[q][j] = q * kBlock + j * 32 < left ? as_float(src[q * kBlock + j * 32]) : -INFINITY;
+  }
   float tau = 1.f;
   if (p.row_tau) {
     tau = p.row_tau[row];
     if (!temperature_ok(tau)) tau = 1.f;
   }
-  const bool exact = samp_exact(p, row);  // of the whole block
+  const bool exact = samp_exact(p, row);  // of the whole block of threads
   if (exact) {
     if (threadIdx.x < 64) table[threadIdx.x] = exp2(threadIdx.x / 64.0);
     __syncthreads();
   }
   const double c64 = exact ? 64.0 * 1.4426950408889634 / (static_cast<double>(tau) * p.tau) : 0.0;
-  const float c2 = fminf(2.8853900817779268f / p.tau / tau, 3e38f);  // 2 log2(e) / tau
+  // 2 log2(e) / tau, kept off 0 so that masked logits stay at 2^-inf
+  const float c2 = fmaxf(fminf(2.8853900817779268f / p.tau / tau, 3e38f), 1.2e-38f);
 #pragma unroll
   for (int q = 0; q < kGroupPer; ++q) {
-    if (g0 + q >= p.g256) break;
-    float mine = -INFINITY, m = -INFINITY;
+    if (b0 + q >= p.blocks) break;
+    float m = z[q][0];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = warp_max_nan(z[q][j]);
-      if (lane == j) mine = x;
-      m = max_nan(m, x);
-    }
-    const int g = (g0 + q) * 8 + lane;
-    if (lane < 8 && g < p.g32) p.gmax[row * p.g32 + g] = mine;
+    for (int j = 1; j < 8; ++j) m = max_nan(m, z[q][j]);
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    if ((lane & 3) == 0) p.gmax[(row * p.blocks + b0 + q) * kGroups + (lane >> 2)] = m;
+    m = warp_max_nan(m);
     double s = 0.0;
     if (fabsf(m) <= 3.402823466e38f) {  // else no finite logit, or the row has no finite sum
       if (exact) {
+        const double md = widen(m);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const double y = (static_cast<double>(z[q][j]) - m) * c64;
+          const double y = (widen(z[q][j]) - md) * c64;
           double e = 0.0, sc = 0.0;
-          if (y > -64.0 * 100) exp2_64(y, 0, table, &e, &sc);  // less cannot be drawn
+          if (y > -64.0 * 100 && z[q][j] > -INFINITY) exp2_64(y, 0, table, &e, &sc);  // less cannot be drawn
           s = fma(e, sc, s);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       } else {
+        const float hm = 0.5f * m;
         float e = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float x = fmaf(-0.5f, z[q][j], 0.5f * m);
-          e += x < INFINITY ? fast_exp2(-x * c2) : 0.f;  // c2 may be 0
-        }
+        for (int j = 0; j < 8; ++j) e += fast_exp2(-fmaf(-0.5f, z[q][j], hm) * c2);
         s = warp_sum(e);
       }
     }
-    if (lane == 0) p.gsum[row * p.g256 + g0 + q] = s;
+    if (lane == 0) p.gsum[row * p.blocks + b0 + q] = s;
   }
 }
 
@@ -406,59 +429,69 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
   const long long row = blockIdx.x;
   const SampFilter f(p, row);
   if (tid < 64) sh.table[tid] = exp2(tid / 64.0);
-  if (tid < 2) sh.pick[tid] = kSampBuckets - 1;
-  if (tid == 0) sh.list_n = sh.queue_n = 0;
-  for (int i = tid; i < kSampBuckets / 4; i += kSampThreads) sh.chist[i] = make_uint4(0, 0, 0, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the groups' records
   const T* src = static_cast<const T*>(p.logits) + row * p.V;
-  const float* gmax = p.gmax + row * p.g32;
-  const double* gsum = p.gsum + row * p.g256;
+  const float* gmax = p.gmax + row * p.blocks * kGroups;
+  const double* gsum = p.gsum + row * p.blocks;
+  const int groups = p.blocks * kGroups;
+  // fn(maximum, group) over the groups, four loads under way
+  auto each_group = [&](auto fn) {
+#pragma unroll 1
+    for (int g0 = tid; g0 < groups; g0 += 4 * kSampThreads) {
+      float m[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = g0 + j * kSampThreads < groups ? gmax[g0 + j * kSampThreads] : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fn(m[j], g0 + j * kSampThreads);
+    }
+  };
 
   float tmax = -INFINITY;
-  for (int g = tid; g < p.g32; g += kSampThreads) tmax = max_nan(tmax, gmax[g]);
+  each_group([&](float m, int) { tmax = max_nan(tmax, m); });
   tmax = warp_max_nan(tmax);
   if (lane == 0) sh.red[0][warp] = __float_as_uint(tmax);
   __syncthreads();
-  float zmax = -INFINITY;
-  for (int w = 0; w < kSampWarps; ++w) zmax = max_nan(zmax, __uint_as_float(static_cast<uint32_t>(sh.red[0][w])));
+  const float zmax = warp_max_nan(__uint_as_float(static_cast<uint32_t>(sh.red[0][lane & (kSampWarps - 1)])));
   if (no_sum(p, row, zmax, tid == 0)) return;
   if (f.flag && tid == 0) atomicOr(p.err, f.flag);
   const SampRow R = samp_row(p, zmax, f.tau, sh.table);
-  // the largest logit of 256
-  auto max256 = [&](int g) {
-    float m = -INFINITY;
-    for (int j = g * 8; j < min(g * 8 + 8, p.g32); ++j) m = fmaxf(m, gmax[j]);
-    return m;
+  // block b's sum of exponentials relative to the row's maximum
+  auto block_sum = [&](int b) -> double {
+    const double s = gsum[b];
+    const float4 u = reinterpret_cast<const float4*>(gmax)[b * 2], v = reinterpret_cast<const float4*>(gmax)[b * 2 + 1];
+    const float m = fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+    const double y = R.y64(m);
+    if (!(s > 0.0) || y < -64.0 * 100) return 0.0;  // less than 2^-100 of the largest weight
+    double e, sc;
+    exp2_64(y, 0, sh.table, &e, &sc);
+    return s * (e * sc);
   };
 
-  if (f.exact()) {
-    // whole numbers of 2^-F again; each thread has a run of groups
+  if (f.off()) {
+    // whole numbers of 2^-F again; each thread has a run of blocks
     const double up = __hiloint2double((1023 + p.F) << 20, 0);
-    const int run = (p.g256 + kSampThreads - 1) / kSampThreads;
-    const int r0 = min(p.g256, tid * run), r1 = min(p.g256, r0 + run);
-    auto group_weight = [&](int g) -> u64 {
-      const double s = gsum[g];
-      return s > 0.0 ? __double2ull_rn(s * exp2(R.y64(max256(g)) / 64.0) * up) : 0;
-    };
-    u64 s = 0, before, px, total, tx;
-    for (int g = r0; g < r1; ++g) s += group_weight(g);
-    block_scan2(s, 0, &before, &px, &total, &tx, sh.red);
+    const int run = (p.blocks + kSampThreads - 1) / kSampThreads;
+    const int r0 = min(p.blocks, tid * run), r1 = min(p.blocks, r0 + run);
+    auto block_weight = [&](int b) -> u64 { return __double2ull_rn(block_sum(b) * up); };
+    u64 s = 0, before, total;
+    for (int b = r0; b < r1; ++b) s += block_weight(b);
+    block_scan(s, &before, &total, sh.red[1]);
     const u64 r = f.draw_at(total);
     if (before <= r && r < before + s) {
-      int g = r0;
-      for (; g < r1 - 1; ++g) {
-        const u64 w = group_weight(g);
+      int b = r0;
+      for (; b < r1 - 1; ++b) {
+        const u64 w = block_weight(b);
         if (r < before + w) break;
         before += w;
       }
-      sh.pick[0] = g;
+      sh.pick = b;
       sh.base = r - before;
     }
     __syncthreads();
     if (warp != 0) return;
-    // within the group, 8 adjacent logits a lane; its weights' sum is its rounded sum up to their
+    // within the block, 8 adjacent logits a lane; its weights' sum is its rounded sum up to their
     // own roundings, so a remainder past the last goes to the last that can be drawn
-    const long long i0 = static_cast<long long>(sh.pick[0]) * kSum + lane * 8;
+    const long long i0 = static_cast<long long>(sh.pick) * kBlock + lane * 8;
     const u64 rest = sh.base;
     u64 w[8], sum = 0;
     int last = -1;
@@ -468,8 +501,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       sum += w[j];
       if (w[j] > 0) last = j;
     }
-    const u64 incl = warp_scan64(sum, lane);
-    u64 at = incl - sum;
+    u64 at = warp_scan64(sum, lane) - sum;
     int hit = -1;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -488,73 +520,75 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
   }
 
   // ---- the row's sum, in a fixed order
-  double part = 0.0;
-  for (int g = tid; g < p.g256; g += kSampThreads) {
-    const double s = gsum[g];
-    if (s > 0.0) part += s * exp2(R.y64(max256(g)) / 64.0);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-  if (lane == 0) sh.dred[warp] = part;
-  if (!f.listed(p.V)) {
-    __syncthreads();
-    if (tid == 0) {
-      double total = 0.0;
-      for (int w = 0; w < kSampWarps; ++w) total += sh.dred[w];
-      p.rsum[row] = total;
-      p.tokens[row] = kSampPending;
-    }
-    return;
-  }
-
-  // ---- candidates lie in the buckets up to b0
-  const bool all_listed = p.V <= kSampList;
-  int b0 = kSampBuckets - 1;
-  if (!all_listed && (f.k > 0 || f.use_p)) {
-    const u64 want = f.k > 0 ? f.k : kSampListK / 2;
-    uint32_t* hist = reinterpret_cast<uint32_t*>(sh.chist);
-    for (int g = tid; g < p.g32; g += kSampThreads) {
-      const int b = R.bucket(gmax[g]);
-      if (b < kSampBuckets) atomicAdd(&hist[b], 1u);
-    }
-    __syncthreads();
-    const uint4 h = sh.chist[tid];
-    const uint32_t hv[4] = {h.x, h.y, h.z, h.w};
-    u64 pc, px, tc, tx;
-    block_scan2(h.x + h.y + h.z + h.w, 0, &pc, &px, &tc, &tx, sh.red);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (pc < want && want <= pc + hv[j]) sh.pick[0] = tid * 4 + j;
-      pc += hv[j];
-    }
-    __syncthreads();
-    b0 = sh.pick[0];
-  }
-  if (f.use_m && !f.use_p) {
-    const double bm = -f.low64 / 64.0 * (kSampBuckets / static_cast<double>(p.F)) + 1.0;
-    if (bm < b0) b0 = static_cast<int>(bm);
-  }
-  for (int g = tid; g < p.g32; g += kSampThreads)
-    if (R.bucket(gmax[g]) <= b0) {
-      const uint32_t at = atomicAdd(&sh.queue_n, 1u);
-      if (at < kSampList) sh.queue[at] = g;
-    }
-  __syncthreads();
   double total = 0.0;
-  for (int w = 0; w < kSampWarps; ++w) total += sh.dred[w];
-  // every queued group holds a candidate: more of them than the list holds leave the row
-  const int groups = static_cast<int>(min(sh.queue_n, static_cast<uint32_t>(kSampList)));
-  if (sh.queue_n <= kSampList) {
-    for (int q0 = warp; q0 < groups; q0 += 4 * kSampWarps) {
+  for (int b = tid; b < p.blocks; b += kSampThreads) total += block_sum(b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) sh.dred[warp] = total;
+  __syncthreads();
+  total = sh.dred[lane & (kSampWarps - 1)];
+#pragma unroll
+  for (int o = kSampWarps / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+
+  const bool all_listed = p.V <= kSampList;
+  // top-p without top-k: few candidates first, then as many as there is room for
+  int want = f.k > 0 ? f.k : 256;
+  for (bool more = f.listed(p.V); more;) {
+    // ---- candidates lie in the buckets up to b0
+    more = false;
+    int b0 = kSampBuckets - 1;
+    if (tid == 0) {
+      sh.pick = kSampBuckets - 1;
+      sh.list_n = sh.queue_n = 0;
+    }
+    if (!all_listed && (f.k > 0 || f.use_p)) {
+      for (int i = tid; i < kSampBuckets / 4; i += kSampThreads) sh.chist[i] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+      uint32_t* hist = reinterpret_cast<uint32_t*>(sh.chist);
+      each_group([&](float m, int) {
+        const int b = R.bucket(m);
+        if (b < kSampBuckets) atomicAdd(&hist[b], 1u);
+      });
+      __syncthreads();
+      const uint4 h = sh.chist[tid];
+      const uint32_t hv[4] = {h.x, h.y, h.z, h.w};
+      u64 pc, tc;
+      block_scan(h.x + h.y + h.z + h.w, &pc, &tc, sh.red[0]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (pc < static_cast<u64>(want) && static_cast<u64>(want) <= pc + hv[j]) sh.pick = tid * 4 + j;
+        pc += hv[j];
+      }
+      __syncthreads();
+      b0 = sh.pick;
+    }
+    if (f.use_m && !f.use_p) {
+      const double bm = -f.low64 / 64.0 * (kSampBuckets / static_cast<double>(p.F)) + 1.0;
+      if (bm < b0) b0 = static_cast<int>(bm);
+    }
+    __syncthreads();
+    each_group([&](float m, int g) {
+      if (R.bucket(m) <= b0) {
+        const uint32_t at = atomicAdd(&sh.queue_n, 1u);
+        if (at < kSampList) sh.queue[at] = g;
+      }
+    });
+    __syncthreads();
+    // every queued group holds a candidate: more of them than the list holds leave the row
+    if (sh.queue_n > kSampList) break;
+    const int queued = static_cast<int>(sh.queue_n);
+#pragma unroll 1
+    for (int q0 = warp; q0 < queued; q0 += 4 * kSampWarps) {
       float z[4];
       int id[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int q = q0 + j * kSampWarps;
-        id[j] = q < groups ? static_cast<int>(sh.queue[q]) * kGroup + lane : -1;
-        const bool in = id[j] >= 0 && id[j] < p.V;
-        z[j] = in ? as_float(src[id[j]]) : 0.f;
-        if (!in) id[j] = -1;
+        const uint32_t g = q < queued ? sh.queue[q] : 0;
+        const long long i = static_cast<long long>(g / kGroups) * kBlock + (lane >> 2) * 32 + (g % kGroups) * 4 + (lane & 3);
+        const bool in = q < queued && i < p.V;
+        z[j] = in ? as_float(src[i]) : 0.f;
+        id[j] = in ? static_cast<int>(i) : -1;
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -566,88 +600,85 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
         if (hit && at < kSampList) sh.list[at] = (static_cast<u64>(sort_key(z[j])) << 32) | static_cast<uint32_t>(~id[j]);
       }
     }
-  }
-  __syncthreads();
-  const int n = static_cast<int>(min(sh.list_n, static_cast<uint32_t>(kSampList)));
-  bool ok = sh.queue_n <= kSampList && sh.list_n <= kSampList;  // alike in all threads, as every `ok` below
-  if (ok) {
-    int P = 2;
-    while (P < n) P <<= 1;
-    for (int i = n + tid; i < P; i += kSampThreads) sh.list[i] = 0;
-    if (tid < 2) sh.pick[tid] = -1;
     __syncthreads();
-    bitonic_desc(sh.list, P);
-    // this thread's two candidates, and the weight before them
-    u64 w[2] = {0, 0}, pw, px, tw, tx;
-    bool in_m[2] = {false, false};
+    if (sh.list_n > kSampList) break;
+    const int n = static_cast<int>(sh.list_n);
+    sort_desc(sh.list, n);
+
+    // ---- kept: nk by count, the first by min-p, and by top-p up to the first whose running
+    // weight reaches its part of what top-k kept, or of the row
     const int nk = f.k > 0 ? min(n, f.k) : n;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (tid * 2 + j < nk) {
-        const float z = key_value(static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32));
-        w[j] = R.weight(z);
-        in_m[j] = R.y64(z) >= f.low64;
-        sh.wlist[tid * 2 + j] = w[j];
+    u64 before = 0, sum = 0, weight = 0, by_m = 0;
+    for (int c = 0; c < nk; c += kSampThreads) {
+      const int i = c + tid;
+      u64 w = 0, in = 0;
+      if (i < nk) {
+        const float z = key_value(static_cast<uint32_t>(sh.list[i] >> 32));
+        w = R.weight(z);
+        in = !f.use_m || R.y64(z) >= f.low64;
+        sh.wlist[i] = w;
       }
-    block_scan2(w[0] + w[1], static_cast<u64>(in_m[0]) + in_m[1], &pw, &px, &tw, &tx, sh.red);
-    // kept: nk by count, tx by min-p, and by top-p up to the first whose running weight reaches
-    // the target; without top-k and with candidates outside the list, the target is only known
-    // to lie in [t0, t1]
-    int nkeep = min(nk, static_cast<int>(tx));
+      block_scan(w, &before, &sum, sh.red[0]);
+      weight += sum;
+      block_scan(in, &before, &sum, sh.red[1]);
+      by_m += sum;
+    }
+    int keep = min(nk, static_cast<int>(by_m));
     if (f.use_p) {
-      u64 t0, t1;
-      if (f.k > 0 || all_listed) {
-        t0 = t1 = f.p_target(tw);
-      } else if (!(f.top_p > 0.f)) {
-        t0 = t1 = 1;
-      } else {
-        const double s = static_cast<double>(f.top_p) * total * __hiloint2double((1023 + p.F) << 20, 0);
-        t0 = max(static_cast<u64>(s * (1.0 - kFastErr)), 1ull);
-        t1 = static_cast<u64>(s * (1.0 + kFastErr)) + 2;
-      }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (pw < t0 && t0 <= pw + w[j]) sh.pick[0] = tid * 2 + j;
-        if (pw < t1 && t1 <= pw + w[j]) sh.pick[1] = tid * 2 + j;
-        pw += w[j];
+      const u64 target = f.p_target(f.k > 0 ? weight : f.whole(total, p.F));
+      if (tid == 0) sh.pick = -1;
+      u64 run = 0;
+      for (int c = 0; c < nk; c += kSampThreads) {
+        const int i = c + tid;
+        const u64 w = i < nk ? sh.wlist[i] : 0;
+        block_scan(w, &before, &sum, sh.red[0]);
+        before += run;
+        if (before < target && target <= before + w) sh.pick = i;
+        run += sum;
       }
       __syncthreads();
-      ok = sh.pick[0] >= 0 && sh.pick[0] == sh.pick[1];
-      nkeep = min(nkeep, sh.pick[0] + 1);
+      const int at = sh.pick;
+      __syncthreads();
+      if (at >= 0) {
+        keep = min(keep, at + 1);
+      } else if (!all_listed) {  // else all are listed, and the target past them by a rounding
+        more = f.k == 0 && want < kSampListK;
+        want = kSampListK;
+        continue;
+      }
     }
-    if (ok) {
-      // in the order of the ids
-      u64 x[2] = {0, 0};
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (tid * 2 + j < nkeep) x[j] = (sh.list[tid * 2 + j] << 32) | static_cast<uint32_t>(tid * 2 + j);
-      __syncthreads();
-      P = 2;
-      while (P < nkeep) P <<= 1;
-      if (tid * 2 < P) {
-        sh.list[tid * 2] = x[0];
-        sh.list[tid * 2 + 1] = x[1];
-      }
-      __syncthreads();
-      bitonic_desc(sh.list, P);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) w[j] = tid * 2 + j < nkeep ? sh.wlist[static_cast<uint32_t>(sh.list[tid * 2 + j])] : 0;
-      block_scan2(w[0] + w[1], 0, &pw, &px, &tw, &tx, sh.red);
-      const u64 r = f.draw_at(tw);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (pw <= r && r < pw + w[j]) {
-          const int id = static_cast<int>(~static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32));
-          p.tokens[row] = id;
-          if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), total);
-        }
-        pw += w[j];
-      }
-      return;
+
+    // ---- the kept in the order of their ids, their weights found by their old places
+    for (int c = 0; c < keep; c += kSampThreads) {
+      const u64 x = c + tid < keep ? (sh.list[c + tid] << 32) | static_cast<uint32_t>(c + tid) : 0;
+      if (c + tid < keep) sh.list[c + tid] = x;
     }
+    sort_desc(sh.list, keep);
+    u64 all = 0;
+    for (int c = 0; c < keep; c += kSampThreads) {
+      const int i = c + tid;
+      block_scan(i < keep ? sh.wlist[static_cast<uint32_t>(sh.list[i])] : 0, &before, &sum, sh.red[0]);
+      all += sum;
+    }
+    const u64 r = f.draw_at(all);
+    u64 run = 0;
+    for (int c = 0; c < keep; c += kSampThreads) {
+      const int i = c + tid;
+      const u64 w = i < keep ? sh.wlist[static_cast<uint32_t>(sh.list[i])] : 0;
+      if (keep > kSampThreads) block_scan(w, &before, &sum, sh.red[0]);  // else it is that of above
+      before += run;
+      run += sum;
+      if (before <= r && r < before + w) {
+        const int id = static_cast<int>(~static_cast<uint32_t>(sh.list[i] >> 32));
+        p.tokens[row] = id;
+        if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), total);
+      }
+    }
+    return;
   }
   if (tid == 0) {
-    p.rsum[row] = total;
+    p.rsum[2 * row] = total;
+    p.rsum[2 * row + 1] = zmax;
     p.tokens[row] = kSampPending;
   }
 }
@@ -655,7 +686,8 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
 // One row per cluster; rows that are not pending cost an exit.
 template <class T>
 __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampParams p) {
-  __shared__ RowShared sh;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  RowShared& sh = *reinterpret_cast<RowShared*>(dyn);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank();
   const int C = p.C;
@@ -663,68 +695,65 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the list kernel's tokens
   if (p.tokens[row] != kSampPending) return;          // in every CTA alike
   cluster_arrive();  // before any CTA writes another's shared memory, all have started
+
+  // ---- this CTA's chunk of the row, in shared memory at the row's own alignment
+  const int c0 = static_cast<int>(min(static_cast<long long>(rank) * p.L, static_cast<long long>(p.V)));
+  const int len = min(p.L, p.V - c0);
+  const T* src = static_cast<const T*>(p.logits) + row * p.V + c0;
+  if (p.resident) {
+    constexpr int E = 16 / sizeof(T);
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));
+    T* chunk = reinterpret_cast<T*>(dyn + sizeof(RowShared)) + mis;
+    const int head = min(len, mis ? E - mis : 0), nv = (len - head) / E, tail = head + nv * E;
+    if (tid < head) chunk[tid] = src[tid];
+    if (tail + tid < len) chunk[tail + tid] = src[tail + tid];
+    const uint4* from = reinterpret_cast<const uint4*>(src + head);
+    uint4* to = reinterpret_cast<uint4*>(chunk + head);
+    for (int j0 = tid; j0 < nv; j0 += 4 * kSampThreads) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j * kSampThreads < nv) v[j] = from[j0 + j * kSampThreads];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j * kSampThreads < nv) to[j0 + j * kSampThreads] = v[j];
+    }
+    src = chunk;
+  }
   const SampFilter f(p, row);
-  const T* src = static_cast<const T*>(p.logits) + row * p.V;
-  const float* gmax = p.gmax + row * p.g32;
   uint32_t* chist = reinterpret_cast<uint32_t*>(sh.chist);
   if (tid < 64) sh.table[tid] = exp2(tid / 64.0);
   if (tid == 0) sh.list_n = 0;
-  float zmax = -INFINITY;
-  for (int g = tid; g < p.g32; g += kSampThreads) zmax = fmaxf(zmax, gmax[g]);  // finite: the list kernel saw it
-  zmax = warp_max_nan(zmax);
-  if (lane == 0) sh.red[0][warp] = __float_as_uint(zmax);
-  __syncthreads();
-  for (int w = 0; w < kSampWarps; ++w) zmax = fmaxf(zmax, __uint_as_float(static_cast<uint32_t>(sh.red[0][w])));
-  const SampRow R = samp_row(p, zmax, f.tau, sh.table);
+  const double total = p.rsum[2 * row];
+  const SampRow R = samp_row(p, static_cast<float>(p.rsum[2 * row + 1]), f.tau, sh.table);
   cluster_wait();
+  __syncthreads();
 
-  // groups [s0, s1) are this warp's: contiguous, in the order of the CTAs and their warps
-  const int per_cta = (p.g32 + C - 1) / C;
-  const int cta0 = min(p.g32, static_cast<int>(rank) * per_cta), cta1 = min(p.g32, cta0 + per_cta);
-  const int per_warp = ((cta1 - cta0 + kSampWarps - 1) / kSampWarps + kBatch - 1) / kBatch * kBatch;
-  const int s0 = min(cta1, cta0 + warp * per_warp), s1 = min(cta1, s0 + per_warp);
-  // fn(z, id) for every logit of the batch's groups whose maximum passes `pred` (-inf past the
-  // row's end)
-  auto batch = [&](int b, auto pred, auto fn) {
-    const bool mine = lane < kBatch && b + lane < s1;
-    const uint32_t mask = __ballot_sync(0xffffffffu, mine && pred(mine ? gmax[b + lane] : 0.f));
-    if (!mask) return;
-    float z[kBatch];
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const long long i = static_cast<long long>(b + j) * kGroup + lane;
-      z[j] = ((mask >> j) & 1) && i < p.V ? as_float(src[i]) : -INFINITY;
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j)
-      if ((mask >> j) & 1) fn(z[j], (b + j) * kGroup + lane);
+  // [s0, s1) of the chunk are this warp's: contiguous, in the order of the CTAs and their warps
+  const int per_warp = ((len + kSampWarps - 1) / kSampWarps + 31) / 32 * 32;
+  const int s0 = min(len, warp * per_warp), s1 = min(len, s0 + per_warp);
+  // fn(z, id) for 32 logits at a time of the warp's [b0, b1), every `step` th 32 (-inf past the end)
+  auto sweep = [&](int b0, int b1, int step, auto fn) {
+#pragma unroll 1
+    for (int i = b0 + lane; i - lane < b1; i += 32 * step) fn(i < b1 ? as_float(src[i]) : -INFINITY, c0 + i);
   };
   auto compose = [](float z, int id) { return (static_cast<u64>(sort_key(z)) << 32) | static_cast<uint32_t>(~id); };
-  // Sums over the row of two values per thread, in every thread of the cluster.
-  auto sum2 = [&](u64 a, u64 b, u64* ta, u64* tb) {
+  // Sum over the row of a value per thread, in every thread of the cluster.
+  auto sum_row = [&](u64 a) -> u64 {
     a = warp_sum64(a);
-    b = warp_sum64(b);
     __syncthreads();
-    if (lane == 0) {
-      sh.red[0][warp] = a;
-      sh.red[1][warp] = b;
-    }
+    if (lane == 0) sh.red[0][warp] = a;
     __syncthreads();
     if (tid < C) {
-      u64 x = 0, y = 0;
-      for (int w = 0; w < kSampWarps; ++w) {
-        x += sh.red[0][w];
-        y += sh.red[1][w];
-      }
+      u64 x = 0;
+      for (int w = 0; w < kSampWarps; ++w) x += sh.red[0][w];
       dsm_st64(&sh.tot_a[rank], tid, x);
-      dsm_st64(&sh.tot_b[rank], tid, y);
     }
     samp_sync();
-    *ta = *tb = 0;
-    for (int r = 0; r < C; ++r) {
-      *ta += sh.tot_a[r];
-      *tb += sh.tot_b[r];
-    }
+    u64 t = 0;
+    for (int r = 0; r < C; ++r) t += sh.tot_a[r];
+    samp_sync();  // read before they are written again
+    return t;
   };
   auto zero = [&](bool w) {
     for (int i = tid; i < kSampBuckets / 4; i += kSampThreads) sh.chist[i] = make_uint4(0, 0, 0, 0);
@@ -736,6 +765,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
   auto bins = [&](bool w, u64 (&hc)[4], u64 (&hw)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) hc[j] = hw[j] = 0;
+#pragma unroll 1
     for (int r = 0; r < C; ++r) {
       const uint4 h = dsm_ld128(&sh.chist[tid], r);
       hc[0] += h.x;
@@ -747,42 +777,64 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
         for (int j = 0; j < 4; ++j) hw[j] += dsm_ld64(&sh.whist[tid * 4 + j], r);
     }
   };
-  // The bin in which the running count or weight, from (bc, bw), reaches the target: sh.found in
+  // The bin in which the running count or weight, from `base`, reaches the target: sh.found in
   // every CTA, which each works out for itself; false if none does.
-  auto search = [&](bool by_w, u64 target, u64 bc, u64 bw) -> bool {
-    u64 hc[4], hw[4], pc, pw, tc, tw;
+  auto search = [&](bool by_w, u64 target, u64 base) -> bool {
+    u64 hc[4], hw[4], at, all;
     bins(by_w, hc, hw);
     if (tid == 0) sh.hit = 0;
-    block_scan2(hc[0] + hc[1] + hc[2] + hc[3], hw[0] + hw[1] + hw[2] + hw[3], &pc, &pw, &tc, &tw, sh.red);
-    pc += bc;
-    pw += bw;
+    block_scan(by_w ? hw[0] + hw[1] + hw[2] + hw[3] : hc[0] + hc[1] + hc[2] + hc[3], &at, &all, sh.red[0]);
+    at += base;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const u64 lo = by_w ? pw : pc, hi = lo + (by_w ? hw[j] : hc[j]);
-      if (lo < target && target <= hi) {
+      const u64 end = at + (by_w ? hw[j] : hc[j]);
+      if (at < target && target <= end) {
         sh.found[0] = tid * 4 + j;
         sh.found[1] = hc[j];
-        sh.found[2] = pc;
-        sh.found[3] = pw;
+        sh.found[2] = at;
         sh.hit = 1;
       }
-      pc += hc[j];
-      pw += hw[j];
+      at = end;
     }
     samp_sync();  // also: every CTA has read the histograms
     return sh.hit != 0;
   };
+  // This lane's part of the sum of the weights in the warp's [b0, b1) that `has` keeps. Kept logits
+  // are gathered until they fill the warp: where few are, their weights cost few of its
+  // instructions.
+  auto weigh = [&](int b0, int b1, auto has) -> u64 {
+    float* keep = sh.keep[warp];
+    int n = 0;
+    u64 s = 0;
+    sweep(b0, b1, 1, [&](float z, int id) {
+      const bool mine = has(z, id);
+      const uint32_t mask = __ballot_sync(0xffffffffu, mine);
+      if (!mask) return;
+      if (mine) keep[n + __popc(mask & ((1u << lane) - 1))] = z;
+      n += __popc(mask);
+      if (n >= 32) {
+        __syncwarp();
+        const float x = keep[lane], rest = keep[32 + lane];
+        __syncwarp();
+        n -= 32;
+        if (lane < n) keep[lane] = rest;
+        s += R.weight(x);
+      }
+    });
+    __syncwarp();
+    if (lane < n) s += R.weight(keep[lane]);
+    __syncwarp();
+    return s;
+  };
   // The id at which the running sum, in vocabulary order, of fn(z, id) passes r = target(sum over
-  // the row), fn being 0 in groups whose maximum fails `pred`; -1 where another warp holds it.
-  auto locate = [&](auto pred, auto fn, auto target) -> int {
-    const int nb = (s1 - s0 + kBatch - 1) / kBatch, span = (nb + kParts - 1) / kParts;  // batches per part
+  // the row); -1 where another warp holds it. part(b0, b1) is this lane's part of the sum of fn.
+  auto locate = [&](auto fn, auto part, auto target) -> int {
+    const int span = ((s1 - s0 + kParts - 1) / kParts + 31) / 32 * 32;  // logits per part
     u64 mine = 0;
+#pragma unroll 1
     for (int q = 0; q < kParts; ++q) {
-      if (q * span >= nb) break;
-      u64 s = 0;
-      for (int b = q * span; b < min(nb, (q + 1) * span); ++b)
-        batch(s0 + b * kBatch, pred, [&](float z, int id) { s += fn(z, id); });
-      s = warp_sum64(s);
+      if (s0 + q * span >= s1) break;
+      const u64 s = warp_sum64(part(s0 + q * span, min(s1, s0 + (q + 1) * span)));
       if (lane == 0) sh.part[warp][q] = s;
       mine += s;
     }
@@ -810,36 +862,30 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
       base += s;
     }
     int found = -1;
-    for (int b = q * span; b < min(nb, (q + 1) * span) && found < 0; ++b)
-      batch(s0 + b * kBatch, pred, [&](float z, int id) {
-        const u64 x = warp_scan64(fn(z, id), lane);
-        const uint32_t hit = __ballot_sync(0xffffffffu, r < base + x);
-        if (found < 0 && hit) found = __shfl_sync(0xffffffffu, id, __ffs(hit) - 1);
-        base += __shfl_sync(0xffffffffu, x, 31);
-      });
+    sweep(s0 + q * span, min(s1, s0 + (q + 1) * span), 1, [&](float z, int id) {
+      const u64 x = warp_scan64(fn(z, id), lane);
+      const uint32_t hit = __ballot_sync(0xffffffffu, r < base + x);
+      if (found < 0 && hit) found = __shfl_sync(0xffffffffu, id, __ffs(hit) - 1);
+      base += __shfl_sync(0xffffffffu, x, 31);
+    });
     return found;
   };
 
-  // The last candidate of the shortest prefix of those at or above `from` that reaches top-k's
-  // count (by_w false) or top-p's weight; 0 if all of them do not reach it.
-  auto prefix = [&](bool by_w, u64 from) -> u64 {
-    const float from_z = from ? key_value(static_cast<uint32_t>(from >> 32)) : -INFINITY;
-    auto in_range = [&](float m) { return m >= from_z && R.bucket(m) < kSampBuckets; };
+  // The last candidate of the shortest prefix of those at or above `from` whose count (by_w false)
+  // or weight reaches the target; 0 if all of them do not reach it.
+  auto prefix = [&](bool by_w, u64 from, u64 target) -> u64 {
     // a window of buckets from an eighth of the row; all buckets for a short one
     int lo = 0, hi = kSampBuckets - 1;
-    if (p.g32 > 64 * kBatch) {
+    if (p.V > 32768) {
       zero(false);
-      int seen = 0;
-      for (int b = s0 + (warp & 7) * kBatch; b < s1; b += 8 * kBatch) {
-        seen += min(s1 - b, kBatch);
-        batch(b, in_range, [&](float z, int id) {
-          const int k = R.bucket(z);
-          if (k < kSampBuckets && compose(z, id) >= from) atomicAdd(&chist[k], 1u);
-        });
-      }
-      u64 groups, none;
-      sum2(lane == 0 ? seen : 0, 0, &groups, &none);
-      u64 hc[4], hw[4], pc, px, tc, tx;
+      u64 sampled = 0;
+      sweep(s0 + (warp & 7) * 32, s1, 8, [&](float z, int id) {
+        const int k = R.bucket(z);
+        ++sampled;
+        if (k < kSampBuckets && compose(z, id) >= from) atomicAdd(&chist[k], 1u);
+      });
+      sampled = sum_row(sampled);
+      u64 hc[4], hw[4], at, all;
       bins(false, hc, hw);
       if (tid == 0) {
         sh.window[0] = 0;
@@ -848,55 +894,51 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
       u64 own = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {  // counts, or counts times the weight of the bucket's middle
-        hw[j] = by_w ? static_cast<u64>(static_cast<double>(hc[j]) * exp2(30.0 - (tid * 4 + j + 0.5) * p.F / kSampBuckets)) : hc[j];
+        hw[j] = hc[j];
+        if (by_w && hc[j]) {
+          double e, sc;
+          exp2_64(-64.0 * p.F / kSampBuckets * (tid * 4 + j + 0.5), 30, sh.table, &e, &sc);
+          hw[j] = static_cast<u64>(static_cast<double>(hc[j]) * (e * sc));
+        }
         own += hw[j];
       }
-      block_scan2(own, 0, &pc, &px, &tc, &tx, sh.red);
-      const double t = by_w ? static_cast<double>(f.top_p) * static_cast<double>(tc)
-                            : static_cast<double>(f.k) * static_cast<double>(groups) / p.g32;
-      const double t0 = by_w ? 0.94 * t : 0.9 * t - 16.0, t1 = by_w ? t + 0.06 * static_cast<double>(tc) : 1.1 * t + 16.0;
+      block_scan(own, &at, &all, sh.red[0]);
+      const double t = by_w ? static_cast<double>(f.top_p) * static_cast<double>(all)
+                            : static_cast<double>(target) * static_cast<double>(sampled) / p.V;
+      const double t0 = by_w ? 0.94 * t : 0.9 * t - 16.0, t1 = by_w ? t + 0.06 * static_cast<double>(all) : 1.1 * t + 16.0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const double a = static_cast<double>(pc), b = static_cast<double>(pc + hw[j]);
+        const double a = static_cast<double>(at), b = static_cast<double>(at + hw[j]);
         if (a < t0 && t0 <= b) sh.window[0] = tid * 4 + j;
         if (a < t1 && t1 <= b) sh.window[1] = tid * 4 + j;
-        pc += hw[j];
+        at += hw[j];
       }
       samp_sync();  // also: every CTA has read the histograms
       lo = sh.window[0];
       hi = sh.window[1];
     }
-    u64 target = f.k;
-    for (int pass = 0; pass < 2; ++pass) {  // the second with all buckets, one of which holds it
+    for (int pass = 0;; ++pass) {  // the second with all buckets
       zero(by_w);
-      u64 above = 0, total = 0;
-      for (int b = s0; b < s1; b += kBatch)
-        batch(b, in_range, [&](float z, int id) {
-          const int k = R.bucket(z);
-          if (k >= kSampBuckets || compose(z, id) < from) return;
-          const u64 w = by_w ? R.weight(z) : 1;
-          total += w;
-          if (k < lo) above += w;
-          else if (k <= hi) {
-            atomicAdd(&chist[k], 1u);
-            if (by_w) atomicAdd(&sh.whist[k], w);
-          }
-        });
-      u64 ta, tt;
-      sum2(above, total, &ta, &tt);
-      if (by_w) target = f.p_target(tt);
-      else if (tt < target) {
-        samp_sync();  // the sums are read before they are written again
-        return 0;
-      }
-      if (search(by_w, target, ta, ta)) break;
+      u64 above = 0;
+      if (by_w && lo > 0) above = weigh(s0, s1, [&](float z, int id) { return R.bucket(z) < lo && compose(z, id) >= from; });
+      sweep(s0, s1, 1, [&](float z, int id) {
+        const int k = R.bucket(z);
+        if (k > hi || compose(z, id) < from) return;
+        if (k < lo) {
+          above += !by_w;
+          return;
+        }
+        atomicAdd(&chist[k], 1u);
+        if (by_w) atomicAdd(&sh.whist[k], R.weight(z));
+      });
+      if (search(by_w, target, sum_row(above))) break;
+      if (pass == 1 || (lo == 0 && hi == kSampBuckets - 1)) return 0;
       lo = 0;
       hi = kSampBuckets - 1;
     }
     const int bucket0 = static_cast<int>(sh.found[0]);
-    u64 members = sh.found[1], bc = sh.found[2], bw = sh.found[3];
+    u64 members = sh.found[1], before = sh.found[2];
     uint32_t klo = 0, khi = 0xffffffffu;
-    auto has = [&](float m) { return R.bucket(m) <= bucket0; };
     auto member = [&](float z, int id) {
       const uint32_t key = sort_key(z);
       return key >= klo && key <= khi && R.bucket(z) == bucket0 && compose(z, id) >= from;
@@ -904,13 +946,12 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
     // 2048 ranges a level: after three levels a range is one key
     for (int level = 0; level < 4 && members > kSampList; ++level) {
       uint32_t l = 0xffffffffu, h = 0;  // the members' smallest and largest key
-      for (int b = s0; b < s1; b += kBatch)
-        batch(b, has, [&](float z, int id) {
-          if (member(z, id)) {
-            l = min(l, sort_key(z));
-            h = max(h, sort_key(z));
-          }
-        });
+      sweep(s0, s1, 1, [&](float z, int id) {
+        if (member(z, id)) {
+          l = min(l, sort_key(z));
+          h = max(h, sort_key(z));
+        }
+      });
       l = __reduce_min_sync(0xffffffffu, l);
       h = __reduce_max_sync(0xffffffffu, h);
       zero(by_w);  // its barrier also parts the uses of red
@@ -936,62 +977,58 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
         khi = max(khi, static_cast<uint32_t>(sh.tot_b[r]));
       }
       if (klo == khi) {  // equal logits: the first ones in vocabulary order
-        u64 need = target - bc;
+        u64 need = target - before;
         if (by_w) {
           const u64 w = R.weight(key_value(klo));
-          need = (target - bw + w - 1) / w;
+          need = (need + w - 1) / w;
         }
-        const int id = locate(has, [&](float z, int i) -> u64 { return member(z, i); }, [&](u64) -> u64 { return need - 1; });
+        auto one = [&](float z, int i) -> u64 { return member(z, i); };
+        const int id = locate(one, [&](int b0, int b1) {
+          u64 s = 0;
+          sweep(b0, b1, 1, [&](float z, int i) { s += one(z, i); });
+          return s;
+        }, [&](u64) -> u64 { return need - 1; });
         if (id >= 0 && lane == 0)
           for (int r = 0; r < C; ++r) dsm_st64(&sh.cut, r, (static_cast<u64>(klo) << 32) | static_cast<uint32_t>(~id));
         samp_sync();
         return sh.cut;
       }
       const int shift = max(0, 32 - __clz(khi - klo) - 11);
-      for (int b = s0; b < s1; b += kBatch)
-        batch(b, has, [&](float z, int id) {
-          if (member(z, id)) {
-            const int k = (khi - sort_key(z)) >> shift;
-            atomicAdd(&chist[k], 1u);
-            if (by_w) atomicAdd(&sh.whist[k], R.weight(z));
-          }
-        });
+      sweep(s0, s1, 1, [&](float z, int id) {
+        if (member(z, id)) {
+          const int k = (khi - sort_key(z)) >> shift;
+          atomicAdd(&chist[k], 1u);
+          if (by_w) atomicAdd(&sh.whist[k], R.weight(z));
+        }
+      });
       samp_sync();
-      search(by_w, target, bc, bw);
+      search(by_w, target, before);
       members = sh.found[1];
-      bc = sh.found[2];
-      bw = sh.found[3];
+      before = sh.found[2];
       khi -= static_cast<uint32_t>(sh.found[0]) << shift;
       const uint32_t low = khi - ((1u << shift) - 1);
       klo = low > khi ? klo : max(klo, low);
     }
     // the members go to the first CTA and are sorted
-    for (int b = s0; b < s1; b += kBatch)
-      batch(b, has, [&](float z, int id) {
-        if (member(z, id)) {
-          const uint32_t at = dsm_add32(&sh.list_n, 0, 1);
-          if (at < kSampList) dsm_st64(&sh.list[at], 0, compose(z, id));
-        }
-      });
+    sweep(s0, s1, 1, [&](float z, int id) {
+      if (member(z, id)) {
+        const uint32_t at = dsm_add32(&sh.list_n, 0, 1);
+        if (at < kSampList) dsm_st64(&sh.list[at], 0, compose(z, id));
+      }
+    });
     samp_sync();
     if (rank == 0) {
       const int n = static_cast<int>(min(members, static_cast<u64>(kSampList)));
-      int P = 2;
-      while (P < n) P <<= 1;
-      for (int i = n + tid; i < P; i += kSampThreads) sh.list[i] = 0;
-      __syncthreads();
-      bitonic_desc(sh.list, P);
-      u64 x[2] = {0, 0}, px, pt, tx, tt;
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (tid * 2 + j < n) x[j] = by_w ? R.weight(key_value(static_cast<uint32_t>(sh.list[tid * 2 + j] >> 32))) : 1;
-      block_scan2(x[0] + x[1], 0, &px, &pt, &tx, &tt, sh.red);
-      px += by_w ? bw : bc;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (px < target && target <= px + x[j])
-          for (int r = 0; r < C; ++r) dsm_st64(&sh.cut, r, sh.list[tid * 2 + j]);
-        px += x[j];
+      sort_desc(sh.list, n);
+      for (int c = 0; c < n; c += kSampThreads) {
+        const int i = c + tid;
+        const u64 x = i >= n ? 0 : (by_w ? R.weight(key_value(static_cast<uint32_t>(sh.list[i] >> 32))) : 1);
+        u64 at, sum;
+        block_scan(x, &at, &sum, sh.red[0]);
+        at += before;
+        before += sum;
+        if (at < target && target <= at + x)
+          for (int r = 0; r < C; ++r) dsm_st64(&sh.cut, r, sh.list[i]);
       }
       if (tid == 0) sh.list_n = 0;
     }
@@ -1000,18 +1037,27 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
   };
 
   u64 cut = 0;  // every (key, id) is above
-  if (f.k > 0) cut = prefix(false, 0);
-  if (f.use_p) {
+  if (f.k > 0) {
+    cut = prefix(false, 0, f.k);
     samp_sync();  // cut is read before it is written again
-    cut = prefix(true, cut);
   }
-  const float cut_z = cut ? key_value(static_cast<uint32_t>(cut >> 32)) : -INFINITY;
-  const int id = locate([&](float m) { return m >= cut_z; },
-                        [&](float z, int i) -> u64 { return compose(z, i) < cut || R.y64(z) < f.low64 ? 0 : R.weight(z); },
-                        [&](u64 all) { return f.draw_at(all); });
+  if (f.use_p) {
+    u64 all = f.whole(total, p.F);
+    if (f.k > 0) all = sum_row(weigh(s0, s1, [&](float z, int id) { return R.bucket(z) < kSampBuckets && compose(z, id) >= cut; }));
+    cut = max(cut, prefix(true, cut, f.p_target(all)));  // 0 if the target is past all by a rounding
+  }
+  // min-p as a bucket, to pass over most of the row; a logit's own test is in fp64
+  const double bm = f.use_m ? -f.low64 / 64.0 * (kSampBuckets / static_cast<double>(p.F)) + 1.0 : kSampBuckets;
+  const int last = static_cast<int>(fmin(bm, kSampBuckets - 1.0));
+  auto kept = [&](float z, int id) {
+    if (R.bucket(z) > last || compose(z, id) < cut) return false;
+    return !f.use_m || R.y64(z) >= f.low64;
+  };
+  const int id = locate([&](float z, int i) -> u64 { return kept(z, i) ? R.weight(z) : 0; },
+                        [&](int b0, int b1) { return weigh(b0, b1, kept); }, [&](u64 all) { return f.draw_at(all); });
   if (id >= 0 && lane == 0) {
     p.tokens[row] = id;
-    if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), p.rsum[row]);
+    if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(static_cast<const T*>(p.logits)[row * p.V + id]), total);
   }
 }
 

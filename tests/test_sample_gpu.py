@@ -139,7 +139,7 @@ def test_masked_rows(dtype):
     z[8] = -torch.inf
     z[8, -1] = low
     z[9, 3] = -low
-    for kw in (dict(), dict(k=50), dict(p=0.9), dict(k=20, p=0.5, m=0.1), dict(tau=0.01, p=0.99), dict(tau=1e30, p=0.5), dict(m=0.5)):
+    for kw in (dict(), dict(k=50), dict(p=0.9), dict(k=20, p=0.5, m=0.1), dict(tau=0.01, p=0.99), dict(tau=1e30, p=0.5), dict(tau=1e38), dict(tau=1e38, p=0.9, k=300), dict(m=0.5)):
         o = check(z, u, flags=L.DEVERR_NONFINITE, **kw)
         assert o["tokens"][[1, 4, 5]].tolist() == [-1] * 3 and torch.all(o["logprob"][[1, 4, 5]] == 0)
 
