@@ -43,7 +43,7 @@ constexpr int kSampMaxC = 8;
 constexpr int kBlock = 256;       // logits per sum of exponentials
 constexpr int kGroups = 8;        // maxima per block: group g has the logits 32 j + 4 g + i of the
                                   // block, j < 8 and i < 4 (what four lanes load)
-constexpr int kParts = 16;        // partial sums per warp that locate() keeps
+constexpr int kParts = 4;         // partial sums per warp that locate() keeps
 constexpr int kSampPending = -2;  // tokens[row] of a row that the list kernel leaves
 
 struct SampParams {
@@ -127,12 +127,12 @@ struct ListShared {
 struct alignas(16) RowShared {
   double table[64];
   u64 red[2][kSampWarps];
-  union {
-    u64 whist[kSampBuckets];     // dead once a search is done
-    u64 list[kSampList];         // members of a bucket, on the cluster's first CTA
+  union {                                    // one at a time
+    u64 whist[kSampBuckets];
+    u64 list[kSampList];                     // members of a bucket, on the cluster's first CTA
+    float keep[kSampWarps][256];             // weigh(): logits whose weights are still to be added
   };
   uint4 chist[kSampBuckets / 4];
-  float keep[kSampWarps][64];                // weigh(): logits whose weights are still to be added
   u64 part[kSampWarps][kParts];              // locate(): partial sums of each warp's segment
   u64 tot_a[kSampMaxC], tot_l[kSampMaxC];    // per CTA, written by each into all: sum_row(), locate()
   u64 tot_b[kSampMaxC];
@@ -218,24 +218,32 @@ __device__ __forceinline__ void block_scan(u64 a, u64* pa, u64* ta, u64* red) {
   *ta = __shfl_sync(0xffffffffu, s, kSampWarps - 1);
 }
 
-// Sorts a[0 .. n) in descending order, all values different and not 0; a has room for the next
-// power of two. By counting the larger ones up to 256 values (n reads a thread, no barriers
-// between them), by a bitonic network above. All threads; a barrier before and after.
+// Sorts a[0 .. n) in descending order, all values different and not 0; a (16-byte aligned) has room
+// for the next power of two. By counting the larger ones up to 512 values (no barriers between its
+// steps: 1100 cycles for 64, where the network took 3900), by a bitonic network above. All
+// threads; a barrier before and after.
 __device__ __forceinline__ void sort_desc(u64* a, int n) {
   const int tid = threadIdx.x;
   __syncthreads();
-  if (n <= 256) {
+  if (n <= kSampThreads) {
+    if (tid == 0 && (n & 1)) a[n] = 0;
     const u64 x = tid < n ? a[tid] : 0;
+    __syncthreads();
     int at = 0;
-    if (tid < n)
+    if (tid < n) {
+      const ulonglong2* v = reinterpret_cast<const ulonglong2*>(a);
 #pragma unroll 8
-      for (int j = 0; j < n; ++j) at += a[j] > x;
+      for (int j = 0; j < (n + 1) / 2; ++j) {
+        const ulonglong2 y = v[j];
+        at += (y.x > x) + (y.y > x);
+      }
+    }
     __syncthreads();
     if (tid < n) a[at] = x;
     __syncthreads();
     return;
   }
-  int P = 512;
+  int P = 2 * kSampThreads;
   while (P < n) P <<= 1;
   for (int i = n + tid; i < P; i += kSampThreads) a[i] = 0;
   __syncthreads();
@@ -249,7 +257,9 @@ __device__ __forceinline__ void sort_desc(u64* a, int n) {
           a[j] = x;
         }
       }
-      __syncthreads();
+      // a warp's pairs at strides up to 32 lie in its own 64 values
+      if (stride > 32 || (stride == 1 && size >= 64)) __syncthreads();
+      else __syncwarp();
     }
 }
 
@@ -434,10 +444,10 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
   const float* gmax = p.gmax + row * p.blocks * kGroups;
   const double* gsum = p.gsum + row * p.blocks;
   const int groups = p.blocks * kGroups;
-  // fn(maximum, group) over the groups, four loads under way
+  // fn(maximum, group) over the groups (-inf past the last), whole warps, four loads under way
   auto each_group = [&](auto fn) {
 #pragma unroll 1
-    for (int g0 = tid; g0 < groups; g0 += 4 * kSampThreads) {
+    for (int g0 = tid; g0 - tid < groups; g0 += 4 * kSampThreads) {
       float m[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) m[j] = g0 + j * kSampThreads < groups ? gmax[g0 + j * kSampThreads] : -INFINITY;
@@ -568,21 +578,25 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
     }
     __syncthreads();
     each_group([&](float m, int g) {
-      if (R.bucket(m) <= b0) {
-        const uint32_t at = atomicAdd(&sh.queue_n, 1u);
-        if (at < kSampList) sh.queue[at] = g;
-      }
+      const bool hit = R.bucket(m) <= b0;  // not -inf
+      const uint32_t mask = __ballot_sync(0xffffffffu, hit);
+      if (!mask) return;
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&sh.queue_n, __popc(mask));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1));
+      if (hit && at < kSampList) sh.queue[at] = g;
     });
     __syncthreads();
     // every queued group holds a candidate: more of them than the list holds leave the row
     if (sh.queue_n > kSampList) break;
     const int queued = static_cast<int>(sh.queue_n);
+    // eight groups at a time, their candidates counted in one step: the counter is one address
 #pragma unroll 1
-    for (int q0 = warp; q0 < queued; q0 += 4 * kSampWarps) {
-      float z[4];
-      int id[4];
+    for (int q0 = warp; q0 < queued; q0 += 8 * kSampWarps) {
+      float z[8];
+      int id[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         const int q = q0 + j * kSampWarps;
         const uint32_t g = q < queued ? sh.queue[q] : 0;
         const long long i = static_cast<long long>(g / kGroups) * kBlock + (lane >> 2) * 32 + (g % kGroups) * 4 + (lane & 3);
@@ -590,14 +604,21 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
         z[j] = in ? as_float(src[i]) : 0.f;
         id[j] = in ? static_cast<int>(i) : -1;
       }
+      uint32_t mask[8], count = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool hit = id[j] >= 0 && R.bucket(z[j]) <= b0;
-        const uint32_t mask = __ballot_sync(0xffffffffu, hit);
-        uint32_t at = 0;
-        if (mask && lane == 0) at = atomicAdd(&sh.list_n, __popc(mask));
-        at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1));
-        if (hit && at < kSampList) sh.list[at] = (static_cast<u64>(sort_key(z[j])) << 32) | static_cast<uint32_t>(~id[j]);
+      for (int j = 0; j < 8; ++j) {
+        mask[j] = __ballot_sync(0xffffffffu, id[j] >= 0 && R.bucket(z[j]) <= b0);
+        count += __popc(mask[j]);
+      }
+      uint32_t at = 0;
+      if (lane == 0) at = atomicAdd(&sh.list_n, count);
+      at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t to = at + __popc(mask[j] & ((1u << lane) - 1));
+        if (((mask[j] >> lane) & 1) && to < kSampList)
+          sh.list[to] = (static_cast<u64>(sort_key(z[j])) << 32) | static_cast<uint32_t>(~id[j]);
+        at += __popc(mask[j]);
       }
     }
     __syncthreads();
@@ -732,10 +753,17 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
   // [s0, s1) of the chunk are this warp's: contiguous, in the order of the CTAs and their warps
   const int per_warp = ((len + kSampWarps - 1) / kSampWarps + 31) / 32 * 32;
   const int s0 = min(len, warp * per_warp), s1 = min(len, s0 + per_warp);
-  // fn(z, id) for 32 logits at a time of the warp's [b0, b1), every `step` th 32 (-inf past the end)
+  // fn(z, id) for 32 logits at a time of the warp's [b0, b1), every `step` th 32 (-inf past the
+  // end), four at a time: the arithmetic of one is a long chain, and the SM has few warps
   auto sweep = [&](int b0, int b1, int step, auto fn) {
 #pragma unroll 1
-    for (int i = b0 + lane; i - lane < b1; i += 32 * step) fn(i < b1 ? as_float(src[i]) : -INFINITY, c0 + i);
+    for (int i = b0 + lane; i - lane < b1; i += 128 * step) {
+      float z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = i + 32 * step * j < b1 ? as_float(src[i + 32 * step * j]) : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fn(z[j], c0 + i + 32 * step * j);
+    }
   };
   auto compose = [](float z, int id) { return (static_cast<u64>(sort_key(z)) << 32) | static_cast<uint32_t>(~id); };
   // Sum over the row of a value per thread, in every thread of the cluster.
@@ -800,29 +828,43 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
     return sh.hit != 0;
   };
   // This lane's part of the sum of the weights in the warp's [b0, b1) that `has` keeps. Kept logits
-  // are gathered until they fill the warp: where few are, their weights cost few of its
-  // instructions.
+  // are gathered until they are four for each lane: where few are, their weights cost few of the
+  // warp's instructions.
   auto weigh = [&](int b0, int b1, auto has) -> u64 {
     float* keep = sh.keep[warp];
     int n = 0;
     u64 s = 0;
-    sweep(b0, b1, 1, [&](float z, int id) {
-      const bool mine = has(z, id);
-      const uint32_t mask = __ballot_sync(0xffffffffu, mine);
-      if (!mask) return;
-      if (mine) keep[n + __popc(mask & ((1u << lane) - 1))] = z;
-      n += __popc(mask);
-      if (n >= 32) {
-        __syncwarp();
-        const float x = keep[lane], rest = keep[32 + lane];
-        __syncwarp();
-        n -= 32;
-        if (lane < n) keep[lane] = rest;
-        s += R.weight(x);
+    auto add = [&]() {  // up to 128 of them; the rest moves down
+      __syncwarp();
+      float x[4], rest[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = lane + 32 * j < n ? keep[lane + 32 * j] : -INFINITY;
+        rest[j] = keep[128 + lane + 32 * j];
       }
-    });
-    __syncwarp();
-    if (lane < n) s += R.weight(keep[lane]);
+      __syncwarp();
+      n = max(n - 128, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (lane + 32 * j < n) keep[lane + 32 * j] = rest[j];
+        s += R.weight(x[j]);
+      }
+    };
+#pragma unroll 1
+    for (int i = b0 + lane; i - lane < b1; i += 128) {
+      float z[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j] = i + 32 * j < b1 ? as_float(src[i + 32 * j]) : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool mine = has(z[j], c0 + i + 32 * j);
+        const uint32_t mask = __ballot_sync(0xffffffffu, mine);
+        if (mine) keep[n + __popc(mask & ((1u << lane) - 1))] = z[j];
+        n += __popc(mask);
+      }
+      if (n >= 128) add();
+    }
+    if (n) add();
     __syncwarp();
     return s;
   };
@@ -918,9 +960,10 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
       hi = sh.window[1];
     }
     for (int pass = 0;; ++pass) {  // the second with all buckets
-      zero(by_w);
       u64 above = 0;
       if (by_w && lo > 0) above = weigh(s0, s1, [&](float z, int id) { return R.bucket(z) < lo && compose(z, id) >= from; });
+      __syncthreads();
+      zero(by_w);
       sweep(s0, s1, 1, [&](float z, int id) {
         const int k = R.bucket(z);
         if (k > hi || compose(z, id) < from) return;
