@@ -10,8 +10,8 @@
 //    short prefix, everything that can be in it is collected and sorted (up to 2048 candidates):
 //    at least k logits lie at or above the k-th largest group maximum, so only groups whose
 //    maximum lies there are read again, 128 bytes for most of k candidates. A top-p prefix
-//    without top-k ends where the candidates' weight reaches a part of the whole sum; 256 groups
-//    are tried, then 1024.
+//    without top-k ends where the candidates' weight reaches a part of the whole sum; those of
+//    256 groups are tried, then, if they may suffice, those of 1024.
 //  * sample_row_kernel takes the rows left over (long prefixes), a cluster of 1 to 8 CTAs each,
 //    which hold the row in shared memory (where it fits; else they read it again). A prefix that reaches a count or a weight is found by a histogram over 2048 linear buckets of
 //    (zmax - z) / tau, whose threshold bucket's few members go to the first CTA and are sorted
@@ -80,11 +80,6 @@ __device__ __forceinline__ void samp_sync() {
 __device__ __forceinline__ void dsm_st64(const void* p, uint32_t rank, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(map_to_rank(smem_u32(p), rank)), "l"(v) : "memory");
 }
-__device__ __forceinline__ u64 dsm_ld64(const void* p, uint32_t rank) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
-  return v;
-}
 __device__ __forceinline__ uint4 dsm_ld128(const void* p, uint32_t rank) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -128,7 +123,9 @@ struct alignas(16) RowShared {
   double table[64];
   u64 red[2][kSampWarps];
   union {                                    // one at a time
-    u64 whist[kSampBuckets];
+    struct {
+      uint32_t lo[kSampBuckets], hi[kSampBuckets];
+    } whist;                                 // halves of the bins' weights
     u64 list[kSampList];                     // members of a bucket, on the cluster's first CTA
     float keep[kSampWarps][256];             // weigh(): logits whose weights are still to be added
   };
@@ -663,8 +660,10 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       if (at >= 0) {
         keep = min(keep, at + 1);
       } else if (!all_listed) {  // else all are listed, and the target past them by a rounding
-        more = f.k == 0 && want < kSampListK;
+        // each missing one weighs at most what the last listed one does
+        more = f.k == 0 && want < kSampListK && (target - weight) / max(sh.wlist[n - 1], 1ull) < kSampListK;
         want = kSampListK;
+        __syncthreads();  // the list is read before it is written again
         continue;
       }
     }
@@ -786,30 +785,43 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
   auto zero = [&](bool w) {
     for (int i = tid; i < kSampBuckets / 4; i += kSampThreads) sh.chist[i] = make_uint4(0, 0, 0, 0);
     if (w)
-      for (int i = tid; i < kSampBuckets; i += kSampThreads) sh.whist[i] = 0;
+      for (int i = tid; i < kSampBuckets / 2; i += kSampThreads) reinterpret_cast<uint4*>(&sh.whist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   };
+  // 64-bit additions in shared memory are loops of compare-and-swap; two of 32 bits with a carry
+  // are not, and their sum does not depend on their order either.
+  auto add_weight = [&](int k, u64 w) {
+    const uint32_t lo = static_cast<uint32_t>(w), old = atomicAdd(&sh.whist.lo[k], lo);
+    atomicAdd(&sh.whist.hi[k], static_cast<uint32_t>(w >> 32) + (old + lo < old ? 1u : 0u));
+  };
   // This thread's four bins of the cluster's histograms. The barrier before it has been passed.
-  auto bins = [&](bool w, u64 (&hc)[4], u64 (&hw)[4]) {
+  // Bins outside [b0, b1] are not read: a cluster reading all of all its histograms takes longer
+  // than the pass that fills them.
+  auto bins = [&](bool w, int b0, int b1, u64 (&hc)[4], u64 (&hw)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) hc[j] = hw[j] = 0;
-#pragma unroll 1
+    if (tid * 4 + 3 < b0 || tid * 4 > b1) return;
+#pragma unroll 2
     for (int r = 0; r < C; ++r) {
       const uint4 h = dsm_ld128(&sh.chist[tid], r);
       hc[0] += h.x;
       hc[1] += h.y;
       hc[2] += h.z;
       hc[3] += h.w;
-      if (w)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) hw[j] += dsm_ld64(&sh.whist[tid * 4 + j], r);
+      if (w) {
+        const uint4 l = dsm_ld128(&sh.whist.lo[tid * 4], r), g = dsm_ld128(&sh.whist.hi[tid * 4], r);
+        hw[0] += (static_cast<u64>(g.x) << 32) + l.x;
+        hw[1] += (static_cast<u64>(g.y) << 32) + l.y;
+        hw[2] += (static_cast<u64>(g.z) << 32) + l.z;
+        hw[3] += (static_cast<u64>(g.w) << 32) + l.w;
+      }
     }
   };
   // The bin in which the running count or weight, from `base`, reaches the target: sh.found in
   // every CTA, which each works out for itself; false if none does.
-  auto search = [&](bool by_w, u64 target, u64 base) -> bool {
+  auto search = [&](bool by_w, u64 target, u64 base, int b0, int b1) -> bool {
     u64 hc[4], hw[4], at, all;
-    bins(by_w, hc, hw);
+    bins(by_w, b0, b1, hc, hw);
     if (tid == 0) sh.hit = 0;
     block_scan(by_w ? hw[0] + hw[1] + hw[2] + hw[3] : hc[0] + hc[1] + hc[2] + hc[3], &at, &all, sh.red[0]);
     at += base;
@@ -923,12 +935,12 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
       u64 sampled = 0;
       sweep(s0 + (warp & 7) * 32, s1, 8, [&](float z, int id) {
         const int k = R.bucket(z);
-        ++sampled;
+        sampled += id < c0 + s1;
         if (k < kSampBuckets && compose(z, id) >= from) atomicAdd(&chist[k], 1u);
       });
       sampled = sum_row(sampled);
       u64 hc[4], hw[4], at, all;
-      bins(false, hc, hw);
+      bins(false, 0, kSampBuckets - 1, hc, hw);
       if (tid == 0) {
         sh.window[0] = 0;
         sh.window[1] = kSampBuckets - 1;
@@ -947,7 +959,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
       block_scan(own, &at, &all, sh.red[0]);
       const double t = by_w ? static_cast<double>(f.top_p) * static_cast<double>(all)
                             : static_cast<double>(target) * static_cast<double>(sampled) / p.V;
-      const double t0 = by_w ? 0.94 * t : 0.9 * t - 16.0, t1 = by_w ? t + 0.06 * static_cast<double>(all) : 1.1 * t + 16.0;
+      const double t0 = by_w ? t - 0.02 * static_cast<double>(all) : 0.9 * t - 16.0;
+      const double t1 = by_w ? t + 0.02 * static_cast<double>(all) : 1.1 * t + 16.0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const double a = static_cast<double>(at), b = static_cast<double>(at + hw[j]);
@@ -972,9 +985,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
           return;
         }
         atomicAdd(&chist[k], 1u);
-        if (by_w) atomicAdd(&sh.whist[k], R.weight(z));
+        if (by_w) add_weight(k, R.weight(z));
       });
-      if (search(by_w, target, sum_row(above))) break;
+      if (search(by_w, target, sum_row(above), lo, hi)) break;
       if (pass == 1 || (lo == 0 && hi == kSampBuckets - 1)) return 0;
       lo = 0;
       hi = kSampBuckets - 1;
@@ -1041,11 +1054,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
         if (member(z, id)) {
           const int k = (khi - sort_key(z)) >> shift;
           atomicAdd(&chist[k], 1u);
-          if (by_w) atomicAdd(&sh.whist[k], R.weight(z));
+          if (by_w) add_weight(k, R.weight(z));
         }
       });
       samp_sync();
-      search(by_w, target, before);
+      search(by_w, target, before, 0, kSampBuckets - 1);
       members = sh.found[1];
       before = sh.found[2];
       khi -= static_cast<uint32_t>(sh.found[0]) << shift;
