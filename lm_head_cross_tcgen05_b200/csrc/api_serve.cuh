@@ -13,6 +13,40 @@ void norm_threads(int64_t d, int* vpt, int* threads) {
   *threads = static_cast<int>(cdiv(cdiv(nv, *vpt), 32) * 32);
 }
 
+// Shared memory above the default has to be asked for once per kernel and device.
+template <class K>
+lmh_status allow_smem(K kernel, int bytes, int dev, std::atomic<uint64_t>* done) {
+  const uint64_t bit = 1ull << dev;
+  if (done->load() & bit) return LMH_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return LMH_ERR_CUDA;
+  done->fetch_or(bit);
+  return LMH_OK;
+}
+
+// Blocks of the forward: as many as can be resident (threads, shared memory), or a row each.
+template <int VPT>
+lmh_status launch_norm(const NormParams& p, int threads, int dev, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const int smem = norm_stages(VPT) * 2 * threads * VPT * 16;
+  LMH_TRY(allow_smem(rms_norm_kernel<VPT>, norm_stages(VPT) * 2 * 512 * VPT * 16, dev, &done));
+  const int by_smem = 220 * 1024 / (smem + 1024), by_threads = 1536 / threads;
+  const int64_t most = static_cast<int64_t>(sms) * (by_smem < by_threads ? by_smem : by_threads);
+  ProfScope ps(KID_RMS_NORM, st);
+  rms_norm_kernel<VPT><<<static_cast<unsigned>(p.N < most ? p.N : most), threads, smem, st>>>(p);
+  return last_launch();
+}
+
+template <int VPT>
+lmh_status launch_norm_bwd(const NormBwdParams& p, int threads, int dev, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  LMH_TRY(allow_smem(rms_norm_bwd_kernel<VPT>, norm_bwd_stages(VPT) * 3 * 512 * VPT * 16, dev, &done));
+  ProfScope ps(KID_RMS_NORM_BWD, st);
+  rms_norm_bwd_kernel<VPT><<<static_cast<unsigned>(p.slices), threads,
+                              norm_bwd_stages(VPT) * 3 * threads * VPT * 16, st>>>(p);
+  return last_launch();
+}
+
 }  // namespace
 
 extern "C" lmh_status lmh_rms_norm(int64_t N, int64_t d, const lmh_bf16* x,
@@ -43,14 +77,9 @@ extern "C" lmh_status lmh_rms_norm(int64_t N, int64_t d, const lmh_bf16* x,
   p.rstd = rstd;
   int vpt, threads;
   norm_threads(d, &vpt, &threads);
-  const int ry = threads <= 32 ? 4 : (threads <= 64 ? 2 : 1);  // rows per block: 128 threads or more
-  const dim3 block(threads, ry);
-  const unsigned grid = static_cast<unsigned>(cdiv(N, ry));
-  ProfScope ps(KID_RMS_NORM, st);
-  if (vpt == 1) rms_norm_kernel<1><<<grid, block, 0, st>>>(p);
-  else if (vpt == 2) rms_norm_kernel<2><<<grid, block, 0, st>>>(p);
-  else rms_norm_kernel<4><<<grid, block, 0, st>>>(p);
-  return last_launch();
+  if (vpt == 1) return launch_norm<1>(p, threads, dev, sms, st);
+  if (vpt == 2) return launch_norm<2>(p, threads, dev, sms, st);
+  return launch_norm<4>(p, threads, dev, sms, st);
 }
 
 extern "C" lmh_status lmh_rms_norm_bwd(int64_t N, int64_t d, const lmh_bf16* sum,
@@ -90,14 +119,9 @@ extern "C" lmh_status lmh_rms_norm_bwd(int64_t N, int64_t d, const lmh_bf16* sum
   p.h = ws.h;
   int vpt, threads;
   norm_threads(d, &vpt, &threads);
-  {
-    ProfScope ps(KID_RMS_NORM_BWD, st);
-    const unsigned grid = static_cast<unsigned>(slices);
-    if (vpt == 1) rms_norm_bwd_kernel<1><<<grid, threads, 0, st>>>(p);
-    else if (vpt == 2) rms_norm_bwd_kernel<2><<<grid, threads, 0, st>>>(p);
-    else rms_norm_bwd_kernel<4><<<grid, threads, 0, st>>>(p);
-  }
-  LMH_TRY(last_launch());
+  if (vpt == 1) LMH_TRY(launch_norm_bwd<1>(p, threads, dev, st));
+  else if (vpt == 2) LMH_TRY(launch_norm_bwd<2>(p, threads, dev, st));
+  else LMH_TRY(launch_norm_bwd<4>(p, threads, dev, st));
   if (!dweight) return LMH_OK;
   ProfScope ps(KID_NORM_DWEIGHT, st);
   norm_dweight_kernel<<<static_cast<unsigned>(d / 32), dim3(32, 16), 0, st>>>(
@@ -143,17 +167,6 @@ bool tmap_8bit(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Shared memory above the default has to be asked for once per kernel and device.
-template <class K>
-lmh_status allow_smem(K kernel, int bytes, int dev, std::atomic<uint64_t>* done) {
-  const uint64_t bit = 1ull << dev;
-  if (done->load() & bit) return LMH_OK;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return LMH_ERR_CUDA;
-  done->fetch_or(bit);
-  return LMH_OK;
 }
 
 template <int TN, class Out>

@@ -28,16 +28,18 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
   return (a < kAmaxFloor ? kAmaxFloor : a) / kE4m3Max;  // NaN stays NaN
 }
 
-// Eight values over the scale, rounded to nearest even e4m3 (saturating; NaN stays NaN). The
-// division is exact to half a step, so a block's largest value always becomes 448.
-__device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float scale) {
+// Eight values times 1 / scale, rounded to nearest even e4m3 (saturating; NaN stays NaN). The
+// reciprocal's and the product's roundings move a quotient by less than 2^-22 of itself, so a
+// block's largest value still becomes 448; eight divisions instead bound the kernel (quantising
+// 151936 x 5120: 706 us with them, see below).
+__device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float inv) {
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(y[4 * h], scale), __fdiv_rn(y[4 * h + 1], scale)), __NV_SATFINITE, __NV_E4M3);
-    const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
-        make_float2(__fdiv_rn(y[4 * h + 2], scale), __fdiv_rn(y[4 * h + 3], scale)), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t a =
+        __nv_cvt_float2_to_fp8x2(make_float2(y[4 * h] * inv, y[4 * h + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const __nv_fp8x2_storage_t b =
+        __nv_cvt_float2_to_fp8x2(make_float2(y[4 * h + 2] * inv, y[4 * h + 3] * inv), __NV_SATFINITE, __NV_E4M3);
     w[h] = static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
   }
   return make_uint2(w[0], w[1]);
@@ -57,18 +59,32 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// Sum over the blockDim.x threads of this threadIdx.y (whole warps): every thread gets it.
-__device__ __forceinline__ float row_sum(float x, float* sh) {
+// Sum over the block's threads (whole warps): every thread gets it.
+__device__ __forceinline__ float row_sum(float x, float* s) {
   x = warp_sum(x);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return x;
-  float* s = sh + threadIdx.y * 32;
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
   __syncthreads();
   float t = 0.f;
   for (int w = 0; w < warps; ++w) t += s[w];
   return t;
 }
+
+// Rows on their way from memory: every thread copies its own vectors of the next rows to its own
+// places in shared memory and waits for its own copies alone, so a ring of rows needs no barrier.
+// What bounds these kernels is the number of bytes under way; registers hold one row at most.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Rows of the ring, that under work included: up to 96 KB, or 192 KB for the longest rows.
+__host__ __device__ constexpr int norm_stages(int vpt) { return vpt == 1 ? 4 : 3; }
+__host__ __device__ constexpr int norm_bwd_stages(int vpt) { return vpt == 1 ? 4 : 2; }
 
 struct NormParams {
   long long N;
@@ -84,73 +100,89 @@ struct NormParams {
   float* rstd;     // or null
 };
 
-// One row per threadIdx.y, VPT vectors of 8 per thread at v = threadIdx.x + j * blockDim.x. The
-// sum is rounded to bf16 before the norm: the norm is that of the stream as it is stored, which
-// is what the backward pass and a next layer read. A scale's 16 vectors lie in 16 adjacent lanes
-// (blockDim.x is a multiple of 32), so the block's maximum is four shuffles.
+// Row blockIdx.x + i * gridDim.x; VPT vectors of 8 per thread at v = threadIdx.x + j * blockDim.x.
+// The sum is rounded to bf16 before the norm: the norm is that of the stream as it is stored,
+// which is what the backward pass and a next layer read. A scale's 16 vectors lie in 16 adjacent
+// lanes (blockDim.x is a multiple of 32), so the block's maximum is four shuffles.
 template <int VPT>
 __global__ void __launch_bounds__(512) rms_norm_kernel(const NormParams p) {
-  __shared__ float sh[4 * 32];
-  const long long row = static_cast<long long>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const bool live = row < p.N;
-  const int nv = p.d >> 3;
-  const long long base = row * nv;
-  uint4 s[VPT];
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float sh[2][32];
+  constexpr int S = norm_stages(VPT);
+  const int nv = p.d >> 3, nb = (p.d + kQBlock - 1) / kQBlock;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t tensor = blockDim.x * VPT * 16, stage = 2 * tensor;
+  auto fetch = [&](long long row, int at) {
+    if (row < p.N)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < nv) {
+          const uint32_t dst = mine + at * stage + j * blockDim.x * 16;
+          copy_async16(dst, p.x + row * nv + v);
+          if (p.residual) copy_async16(dst + tensor, p.residual + row * nv + v);
+        }
+      }
+    copy_commit();  // empty past the last row: the groups are counted
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
+  uint4 wv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = threadIdx.x + j * blockDim.x;
-    s[j] = (live && v < nv) ? __ldcs(p.x + base + v) : make_uint4(0, 0, 0, 0);
+    wv[j] = v < nv ? __ldg(p.weight + v) : make_uint4(0, 0, 0, 0);
   }
-  if (p.residual) {
-    uint4 r[VPT];
+  int at = 0, flip = 0;
+  for (long long row = blockIdx.x; row < p.N; row += gridDim.x, at = (at + 1) % S, flip ^= 1) {
+    const long long base = row * nv;
+    fetch(row + static_cast<long long>(S - 1) * gridDim.x, (at + S - 1) % S);
+    copy_wait<S - 1>();
+    uint4 s[VPT];
+    float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
-      r[j] = (live && v < nv) ? __ldcs(p.residual + base + v) : make_uint4(0, 0, 0, 0);
+      const uint32_t src = mine + at * stage + j * blockDim.x * 16;
+      s[j] = v < nv ? ld_shared_v4(src) : make_uint4(0, 0, 0, 0);
+      float a[8];
+      unpack8(s[j], a);
+      if (p.residual) {
+        float b[8];
+        unpack8(v < nv ? ld_shared_v4(src + tensor) : make_uint4(0, 0, 0, 0), b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] += b[e];
+        s[j] = pack8(a);
+        unpack8(s[j], a);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
     }
+    ss = row_sum(ss, sh[flip]);  // a barrier lies between the uses of either half
+    const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
+    if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      float a[8], b[8];
+      const int v = threadIdx.x + j * blockDim.x;
+      const bool in = v < nv;
+      float a[8], w[8];
       unpack8(s[j], a);
-      unpack8(r[j], b);
+      unpack8(wv[j], w);
+      if (in && p.sum) p.sum[base + v] = s[j];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] += b[e];
-      s[j] = pack8(a);
-    }
-  }
-  float ss = 0.f;
+      for (int e = 0; e < 8; ++e) a[e] = in ? a[e] * rstd * w[e] : 0.f;
+      if (in && p.y) p.y[base + v] = pack8(a);
+      if (p.q) {
+        uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    float a[8];
-    unpack8(s[j], a);
+        for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
-  }
-  ss = row_sum(ss, sh);
-  const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
-  if (live && p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-  const int nb = (p.d + kQBlock - 1) / kQBlock;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int v = threadIdx.x + j * blockDim.x;
-    const bool in = live && v < nv;
-    float a[8], w[8];
-    unpack8(s[j], a);
-    unpack8(in ? __ldg(p.weight + v) : make_uint4(0, 0, 0, 0), w);
-    if (in && p.sum) p.sum[base + v] = s[j];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) a[e] = in ? a[e] * rstd * w[e] : 0.f;
-    if (in && p.y) p.y[base + v] = pack8(a);
-    if (p.q) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float sc = block_scale(m);
-      if (in) {
-        p.q[base + v] = to_e4m3x8(a, sc);
-        if ((v & 15) == 0) p.scale[row * nb + (v >> 4)] = sc;
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float sc = block_scale(m);
+        if (in) {
+          p.q[base + v] = to_e4m3x8(a, 1.f / sc);
+          if ((v & 15) == 0) p.scale[row * nb + (v >> 4)] = sc;
+        }
       }
     }
   }
@@ -160,7 +192,7 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const NormParams p) {
 // With n = r rstd and c = mean(w dy n):  dx = rstd (w dy - n c) + dsum,  dw = sum_rows dy n.
 // Slice blockIdx.x of the rows, one row at a time; a thread keeps its columns' share of dw in
 // registers over the slice and leaves it in part[slice]. The slices depend on N alone.
-constexpr int kNormSlices = 592;  // four blocks of 512 threads on each of 148 SMs
+constexpr int kNormSlices = 296;  // two blocks of 512 threads on each of 148 SMs
 
 struct NormBwdParams {
   long long N;
@@ -176,11 +208,31 @@ struct NormBwdParams {
 };
 
 template <int VPT>
-__global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(512, VPT == 4 ? 1 : 2) rms_norm_bwd_kernel(const NormBwdParams p) {
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][32];
+  constexpr int S = norm_bwd_stages(VPT);
   if (blockIdx.x == 0 && threadIdx.x == 0) p.h->err = 0;
   const int nv = p.d >> 3;
   const long long r0 = p.N * blockIdx.x / p.slices, r1 = p.N * (blockIdx.x + 1) / p.slices;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t tensor = blockDim.x * VPT * 16, stage = 3 * tensor;
+  auto fetch = [&](long long row, int at) {
+    if (row < r1)
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < nv) {
+          const uint32_t dst = mine + at * stage + j * blockDim.x * 16;
+          copy_async16(dst, p.sum + row * nv + v);
+          copy_async16(dst + tensor, p.dy + row * nv + v);
+          if (p.dsum) copy_async16(dst + 2 * tensor, p.dsum + row * nv + v);
+        }
+      }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) fetch(r0 + i, i);
   float acc[VPT][8] = {};
   uint4 w[VPT];
 #pragma unroll
@@ -188,24 +240,20 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const NormBwdParams p
     const int v = threadIdx.x + j * blockDim.x;
     w[j] = v < nv ? __ldg(p.weight + v) : make_uint4(0, 0, 0, 0);
   }
-  int flip = 0;
-  for (long long row = r0; row < r1; ++row, flip ^= 1) {
+  int at = 0, flip = 0;
+  for (long long row = r0; row < r1; ++row, at = (at + 1) % S, flip ^= 1) {
     const long long base = row * nv;
     const float rstd = p.rstd[row];
-    uint4 s[VPT], g[VPT], t[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = threadIdx.x + j * blockDim.x;
-      s[j] = g[j] = t[j] = make_uint4(0, 0, 0, 0);
-      if (v < nv) {
-        s[j] = __ldcs(p.sum + base + v);
-        g[j] = __ldcs(p.dy + base + v);
-        if (p.dsum) t[j] = __ldcs(p.dsum + base + v);
-      }
-    }
+    fetch(row + S - 1, (at + S - 1) % S);
+    copy_wait<S - 1>();
+    uint4 s[VPT], g[VPT];
     float c = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      const uint32_t src = mine + at * stage + j * blockDim.x * 16;
+      s[j] = v < nv ? ld_shared_v4(src) : make_uint4(0, 0, 0, 0);
+      g[j] = v < nv ? ld_shared_v4(src + tensor) : make_uint4(0, 0, 0, 0);
       float n[8], dy[8], wf[8];
       unpack8(s[j], n);
       unpack8(g[j], dy);
@@ -227,7 +275,7 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const NormBwdParams p
       unpack8(s[j], n);
       unpack8(g[j], dy);
       unpack8(w[j], wf);
-      unpack8(t[j], ds);
+      unpack8(p.dsum ? ld_shared_v4(mine + at * stage + j * blockDim.x * 16 + 2 * tensor) : make_uint4(0, 0, 0, 0), ds);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         ds[e] = fmaf(rstd, wf[e] * dy[e] - n[e] * rstd * c, ds[e]);
@@ -253,6 +301,7 @@ __global__ void __launch_bounds__(512) norm_dweight_kernel(int slices, int d,
   __shared__ float sh[16][32];
   const int c = blockIdx.x * 32 + threadIdx.x;  // d is a multiple of 64
   float a = 0.f;
+#pragma unroll 8
   for (int s = threadIdx.y; s < slices; s += 16) a += part[static_cast<long long>(s) * d + c];
   sh[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
@@ -283,7 +332,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(long long rows, int 
   for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!in) return;
   const float sc = block_scale(m);
-  q[row * nv + v] = to_e4m3x8(a, sc);
+  q[row * nv + v] = to_e4m3x8(a, 1.f / sc);
   if ((threadIdx.x & 15) == 0) scale[row * nb + b] = sc;
 }
 
@@ -318,6 +367,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(long long rows, in
 #pragma unroll
   for (int w = 0; w < 8; ++w) m = max(m, sh[w]);
   const float sc = block_scale(m);
+  const float inv = 1.f / sc;
   if (threadIdx.x == 0) scale[rb * nb + b] = sc;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -325,7 +375,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(long long rows, in
     if (r < rows && v < nv) {
       float a[8];
       unpack8(t[i], a);
-      q[r * nv + v] = to_e4m3x8(a, sc);
+      q[r * nv + v] = to_e4m3x8(a, inv);
     }
   }
 }
