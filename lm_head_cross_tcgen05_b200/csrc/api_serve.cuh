@@ -67,6 +67,7 @@ extern "C" lmh_status lmh_rms_norm(int64_t N, int64_t d, const lmh_bf16* x,
   p.N = N;
   p.d = static_cast<int>(d);
   p.eps = eps;
+  p.inv_d = 1.f / static_cast<float>(d);
   p.x = reinterpret_cast<const uint4*>(x);
   p.residual = reinterpret_cast<const uint4*>(residual);
   p.weight = reinterpret_cast<const uint4*>(weight);
@@ -112,6 +113,7 @@ extern "C" lmh_status lmh_rms_norm_bwd(int64_t N, int64_t d, const lmh_bf16* sum
   p.sum = reinterpret_cast<const uint4*>(sum);
   p.weight = reinterpret_cast<const uint4*>(weight);
   p.rstd = rstd;
+  p.inv_d = 1.f / static_cast<float>(d);
   p.dy = reinterpret_cast<const uint4*>(dy);
   p.dsum = reinterpret_cast<const uint4*>(dsum);
   p.dx = reinterpret_cast<uint4*>(dx);

@@ -17,21 +17,24 @@ constexpr int kQBlock = 128;       // columns per scale
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxFloor = 7.888609052210118e-31f;  // 2^-100
 
-// Bits of |x|: as unsigned numbers they order like the values, with NaN above everything, so an
-// integer maximum propagates a NaN into the block's scale.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Larger of m and |x|, NaN if either is: a NaN reaches its block's scale.
+__device__ __forceinline__ float max_abs(float m, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+  return r;
+}
 
-// Scale of a block whose largest magnitude has these bits: max(amax, 2^-100) / 448. The floor
-// keeps the scale and its reciprocal normal numbers, for a block of zeros too.
-__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
-  const float a = __uint_as_float(amax_bits);
-  return (a < kAmaxFloor ? kAmaxFloor : a) / kE4m3Max;  // NaN stays NaN
+// Scale of a block with this largest magnitude: max(amax, 2^-100) / 448, as a product with 1 / 448
+// (off by at most 2^-23 of itself). The floor keeps the scale and its reciprocal normal numbers,
+// for a block of zeros too; NaN stays NaN.
+__device__ __forceinline__ float block_scale(float amax) {
+  return amax < kAmaxFloor ? kAmaxFloor / kE4m3Max : amax * (1.f / kE4m3Max);
 }
 
 // Eight values times 1 / scale, rounded to nearest even e4m3 (saturating; NaN stays NaN). The
-// reciprocal's and the product's roundings move a quotient by less than 2^-22 of itself, so a
-// block's largest value still becomes 448; eight divisions instead bound the kernel (quantising
-// 151936 x 5120: 706 us with them, see below).
+// scale's, the reciprocal's and the product's roundings move a quotient by less than 2^-21 of
+// itself, so a block's largest value still becomes 448; eight divisions instead bound the kernels
+// (quantising 151936 x 5120 took 706 us with them, 426 without).
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float inv) {
   uint32_t w[2];
 #pragma unroll
@@ -59,16 +62,28 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-// Sum over the block's threads (whole warps): every thread gets it.
+// bf16 sums, each rounded once (the unit adds in fp32).
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 s = __hadd2_rn(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
+}
+__device__ __forceinline__ uint4 add8(const uint4& a, const uint4& b) {
+  return make_uint4(add_bf16x2(a.x, b.x), add_bf16x2(a.y, b.y), add_bf16x2(a.z, b.z), add_bf16x2(a.w, b.w));
+}
+
+// Sum over the block's threads (whole warps, 16 at most): every thread gets it. The warps' sums
+// are added by a butterfly too.
 __device__ __forceinline__ float row_sum(float x, float* s) {
   x = warp_sum(x);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return x;
-  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) s[threadIdx.x >> 5] = x;
   __syncthreads();
-  float t = 0.f;
-  for (int w = 0; w < warps; ++w) t += s[w];
-  return t;
+  x = lane < warps ? s[lane] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return __shfl_sync(0xffffffffu, x, 0);
 }
 
 // Rows on their way from memory: every thread copies its own vectors of the next rows to its own
@@ -89,7 +104,7 @@ __host__ __device__ constexpr int norm_bwd_stages(int vpt) { return vpt == 1 ? 4
 struct NormParams {
   long long N;
   int d;
-  float eps;
+  float eps, inv_d;
   const uint4* x;
   const uint4* residual;  // or null
   const uint4* weight;
@@ -127,11 +142,11 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const NormParams p) {
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) fetch(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
-  uint4 wv[VPT];
+  float w[VPT][8];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v = threadIdx.x + j * blockDim.x;
-    wv[j] = v < nv ? __ldg(p.weight + v) : make_uint4(0, 0, 0, 0);
+    unpack8(v < nv ? __ldg(p.weight + v) : make_uint4(0, 0, 0, 0), w[j]);
   }
   int at = 0, flip = 0;
   for (long long row = blockIdx.x; row < p.N; row += gridDim.x, at = (at + 1) % S, flip ^= 1) {
@@ -145,42 +160,34 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const NormParams p) {
       const int v = threadIdx.x + j * blockDim.x;
       const uint32_t src = mine + at * stage + j * blockDim.x * 16;
       s[j] = v < nv ? ld_shared_v4(src) : make_uint4(0, 0, 0, 0);
+      if (p.residual && v < nv) s[j] = add8(s[j], ld_shared_v4(src + tensor));
       float a[8];
       unpack8(s[j], a);
-      if (p.residual) {
-        float b[8];
-        unpack8(v < nv ? ld_shared_v4(src + tensor) : make_uint4(0, 0, 0, 0), b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] += b[e];
-        s[j] = pack8(a);
-        unpack8(s[j], a);
-      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], ss);
     }
     ss = row_sum(ss, sh[flip]);  // a barrier lies between the uses of either half
-    const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
+    const float rstd = rsqrtf(fmaf(ss, p.inv_d, p.eps));
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       const bool in = v < nv;
-      float a[8], w[8];
+      float a[8];
       unpack8(s[j], a);
-      unpack8(wv[j], w);
       if (in && p.sum) p.sum[base + v] = s[j];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = in ? a[e] * rstd * w[e] : 0.f;
+      for (int e = 0; e < 8; ++e) a[e] = a[e] * rstd * w[j][e];  // 0 (or NaN, as the row) past the row's end
       if (in && p.y) p.y[base + v] = pack8(a);
       if (p.q) {
-        uint32_t m = 0;
+        float m = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
+        for (int e = 0; e < 8; ++e) m = max_abs(m, a[e]);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float sc = block_scale(m);
         if (in) {
-          p.q[base + v] = to_e4m3x8(a, 1.f / sc);
+          p.q[base + v] = to_e4m3x8(a, __fdividef(1.f, sc));
           if ((v & 15) == 0) p.scale[row * nb + (v >> 4)] = sc;
         }
       }
@@ -200,6 +207,7 @@ struct NormBwdParams {
   const uint4* sum;
   const uint4* weight;
   const float* rstd;
+  float inv_d;
   const uint4* dy;
   const uint4* dsum;  // or null
   uint4* dx;          // or null; may be dy or dsum
@@ -254,31 +262,31 @@ __global__ void __launch_bounds__(512, VPT == 4 ? 1 : 2) rms_norm_bwd_kernel(con
       const uint32_t src = mine + at * stage + j * blockDim.x * 16;
       s[j] = v < nv ? ld_shared_v4(src) : make_uint4(0, 0, 0, 0);
       g[j] = v < nv ? ld_shared_v4(src + tensor) : make_uint4(0, 0, 0, 0);
-      float n[8], dy[8], wf[8];
-      unpack8(s[j], n);
+      float r[8], dy[8], wf[8];
+      unpack8(s[j], r);
       unpack8(g[j], dy);
       unpack8(w[j], wf);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float dn = dy[e] * (n[e] * rstd);
-        c = fmaf(wf[e], dn, c);
-        acc[j][e] += dn;
+        const float dr = dy[e] * r[e];
+        c = fmaf(wf[e], dr, c);
+        acc[j][e] = fmaf(dr, rstd, acc[j][e]);
       }
     }
     if (!p.dx) continue;
-    c = row_sum(c, sh[flip]) / static_cast<float>(p.d);
+    // dx = rstd w dy - r rstd^3 mean(w dy r) + dsum
+    c = row_sum(c, sh[flip]) * p.inv_d * rstd * rstd * rstd;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
       if (v >= nv) continue;
-      float n[8], dy[8], wf[8], ds[8];
-      unpack8(s[j], n);
+      float r[8], dy[8], wf[8], ds[8];
+      unpack8(s[j], r);
       unpack8(g[j], dy);
       unpack8(w[j], wf);
       unpack8(p.dsum ? ld_shared_v4(mine + at * stage + j * blockDim.x * 16 + 2 * tensor) : make_uint4(0, 0, 0, 0), ds);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        ds[e] = fmaf(rstd, wf[e] * dy[e] - n[e] * rstd * c, ds[e]);
+      for (int e = 0; e < 8; ++e) ds[e] = fmaf(rstd, wf[e] * dy[e], fmaf(-c, r[e], ds[e]));
       p.dx[base + v] = pack8(ds);
     }
   }
@@ -325,14 +333,14 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(long long rows, int 
   const bool in = row < rows && v < nv;
   float a[8];
   unpack8(in ? __ldcs(x + row * nv + v) : make_uint4(0, 0, 0, 0), a);
-  uint32_t m = 0;
+  float m = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
+  for (int e = 0; e < 8; ++e) m = max_abs(m, a[e]);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!in) return;
   const float sc = block_scale(m);
-  q[row * nv + v] = to_e4m3x8(a, 1.f / sc);
+  q[row * nv + v] = to_e4m3x8(a, __fdividef(1.f, sc));
   if ((threadIdx.x & 15) == 0) scale[row * nb + b] = sc;
 }
 
@@ -341,7 +349,7 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(long long rows, in
                                                               const uint4* __restrict__ x,
                                                               uint2* __restrict__ q,
                                                               float* __restrict__ scale) {
-  __shared__ uint32_t sh[8];
+  __shared__ float sh[8];
   const int nb = (d + kQBlock - 1) / kQBlock, nv = d >> 3;
   const long long rb = blockIdx.x / nb;
   const int b = static_cast<int>(blockIdx.x - rb * nb);
@@ -353,21 +361,22 @@ __global__ void __launch_bounds__(256) quantize_blocks_kernel(long long rows, in
     const long long r = r0 + 16 * i;
     t[i] = (r < rows && v < nv) ? __ldcs(x + r * nv + v) : make_uint4(0, 0, 0, 0);
   }
-  uint32_t m = 0;
+  float m = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float a[8];
     unpack8(t[i], a);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, abs_bits(a[e]));
+    for (int e = 0; e < 8; ++e) m = max_abs(m, a[e]);
   }
-  m = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = max(m, sh[w]);
+  for (int w = 0; w < 8; ++w) m = max_abs(m, sh[w]);
   const float sc = block_scale(m);
-  const float inv = 1.f / sc;
+  const float inv = __fdividef(1.f, sc);
   if (threadIdx.x == 0) scale[rb * nb + b] = sc;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
