@@ -6,13 +6,6 @@ namespace {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Vectors of 8 per thread (1, 2 or 4) and threads per row (a multiple of 32, at most 512).
-void norm_threads(int64_t d, int* vpt, int* threads) {
-  const int64_t nv = d / 8;
-  *vpt = nv <= 512 ? 1 : (nv <= 1024 ? 2 : 4);
-  *threads = static_cast<int>(cdiv(cdiv(nv, *vpt), 32) * 32);
-}
-
 // Shared memory above the default has to be asked for once per kernel and device.
 template <class K>
 lmh_status allow_smem(K kernel, int bytes, int dev, std::atomic<uint64_t>* done) {
@@ -94,7 +87,7 @@ extern "C" lmh_status lmh_rms_norm_bwd(int64_t N, int64_t d, const lmh_bf16* sum
       !aligned16(dx) || !aligned16(dweight) || !aligned4(rstd) ||
       (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)) != 0)
     return LMH_ERR_ALIGNMENT;
-  const int slices = norm_slices(N);
+  const int slices = norm_slices(N, d);
   if (workspace_bytes < norm_bwd_bytes(N, d))
     return LMH_ERR_WORKSPACE_TOO_SMALL;
   int dev, sms;
@@ -140,7 +133,9 @@ extern "C" lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_ro
   if (rows > 0 && (!x || !q || !scale)) return LMH_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return LMH_ERR_ALIGNMENT;
   const int64_t nb = cdiv(d, kQBlock);
-  const int64_t grid = block_rows == 1 ? cdiv(rows * nb, 16) : cdiv(rows, kQBlock) * nb;
+  // a warp a row where the rows fill the GPU, a block of threads a row where they do not
+  const int per = rows < 8 * 148 ? 256 : 32;
+  const int64_t grid = block_rows == 1 ? cdiv(rows, 256 / per) : cdiv(rows, kQBlock) * nb;
   if (grid > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
   int dev, sms;
   LMH_TRY(current_device(&dev, &sms));
@@ -149,7 +144,7 @@ extern "C" lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_ro
   ProfScope ps(KID_QUANTIZE, st);
   if (block_rows == 1)
     quantize_rows_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(
-        rows, static_cast<int>(d), reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(q), scale);
+        rows, static_cast<int>(d), per, reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(q), scale);
   else
     quantize_blocks_kernel<<<static_cast<unsigned>(grid), 256, 0, st>>>(
         rows, static_cast<int>(d), reinterpret_cast<const uint4*>(x), reinterpret_cast<uint2*>(q), scale);

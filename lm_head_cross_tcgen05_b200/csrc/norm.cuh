@@ -34,7 +34,7 @@ __device__ __forceinline__ float block_scale(float amax) {
 // Eight values times 1 / scale, rounded to nearest even e4m3 (saturating; NaN stays NaN). The
 // scale's, the reciprocal's and the product's roundings move a quotient by less than 2^-21 of
 // itself, so a block's largest value still becomes 448; eight divisions instead bound the kernels
-// (quantising 151936 x 5120 took 706 us with them, 426 without).
+// (quantising 151936 x 5120 took 706 us with them, 430 without).
 __device__ __forceinline__ uint2 to_e4m3x8(const float (&y)[8], float inv) {
   uint32_t w[2];
 #pragma unroll
@@ -99,7 +99,7 @@ __device__ __forceinline__ void copy_wait() {  // all but the last N groups have
 }
 // Rows of the ring, that under work included: up to 96 KB, or 192 KB for the longest rows.
 __host__ __device__ constexpr int norm_stages(int vpt) { return vpt == 1 ? 4 : 3; }
-__host__ __device__ constexpr int norm_bwd_stages(int vpt) { return vpt == 1 ? 4 : 2; }
+__host__ __device__ constexpr int norm_bwd_stages(int vpt) { return vpt == 1 ? 4 : (vpt == 2 ? 3 : 2); }
 
 struct NormParams {
   long long N;
@@ -198,8 +198,7 @@ __global__ void __launch_bounds__(512) rms_norm_kernel(const NormParams p) {
 // ---------------------------------------------------------------------------- backward
 // With n = r rstd and c = mean(w dy n):  dx = rstd (w dy - n c) + dsum,  dw = sum_rows dy n.
 // Slice blockIdx.x of the rows, one row at a time; a thread keeps its columns' share of dw in
-// registers over the slice and leaves it in part[slice]. The slices depend on N alone.
-constexpr int kNormSlices = 296;  // two blocks of 512 threads on each of 148 SMs
+// registers over the slice and leaves it in part[slice]. The slices depend on N and d alone.
 
 struct NormBwdParams {
   long long N;
@@ -216,7 +215,7 @@ struct NormBwdParams {
 };
 
 template <int VPT>
-__global__ void __launch_bounds__(512, VPT == 4 ? 1 : 2) rms_norm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float sh[2][32];
   constexpr int S = norm_bwd_stages(VPT);
@@ -320,32 +319,43 @@ __global__ void __launch_bounds__(512) norm_dweight_kernel(int slices, int d,
 }
 
 // ---------------------------------------------------------------------------- quantisation
-// One scale per row and 128 columns: 16 adjacent lanes hold a block.
-__global__ void __launch_bounds__(256) quantize_rows_kernel(long long rows, int d,
+// One scale per row and 128 columns: 16 adjacent lanes hold a block. `per` threads (whole warps) a
+// row, four vectors of each under way.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(long long rows, int d, int per,
                                                             const uint4* __restrict__ x,
                                                             uint2* __restrict__ q,
                                                             float* __restrict__ scale) {
-  const int nb = (d + kQBlock - 1) / kQBlock, nv = d >> 3;
-  const long long blk = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
-  const long long row = blk / nb;
-  const int b = static_cast<int>(blk - row * nb);
-  const int v = b * 16 + (threadIdx.x & 15);
-  const bool in = row < rows && v < nv;
-  float a[8];
-  unpack8(in ? __ldcs(x + row * nv + v) : make_uint4(0, 0, 0, 0), a);
-  float m = 0.f;
+  const int nb = (d + kQBlock - 1) / kQBlock, nv = d >> 3, l = threadIdx.x % per;
+  const long long row = static_cast<long long>(blockIdx.x) * (256 / per) + threadIdx.x / per;
+  if (row >= rows) return;  // whole warps
+  for (int c = l - (l & 31); c < nv; c += 4 * per) {
+    uint4 t[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = max_abs(m, a[e]);
+    for (int j = 0; j < 4; ++j) {
+      const int v = c + j * per + (l & 31);
+      t[j] = v < nv ? __ldcs(x + row * nv + v) : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (!in) return;
-  const float sc = block_scale(m);
-  q[row * nv + v] = to_e4m3x8(a, __fdividef(1.f, sc));
-  if ((threadIdx.x & 15) == 0) scale[row * nb + b] = sc;
+    for (int j = 0; j < 4; ++j) {
+      const int v = c + j * per + (l & 31);
+      float a[8], m = 0.f;
+      unpack8(t[j], a);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max_abs(m, a[e]);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float sc = block_scale(m);
+      if (v < nv) {
+        q[row * nv + v] = to_e4m3x8(a, __fdividef(1.f, sc));
+        if ((v & 15) == 0) scale[row * nb + (v >> 4)] = sc;
+      }
+    }
+  }
 }
 
-// One scale per 128 x 128 block, one block of threads each: 16 lanes per row, 8 rows a thread.
-__global__ void __launch_bounds__(256) quantize_blocks_kernel(long long rows, int d,
+// One scale per 128 x 128 block, one block of threads each: 16 lanes per row, 8 rows a thread, four
+// blocks an SM (151936 x 5120: 345 us, 6.8 TB/s; 430 us with the three that 85 registers leave).
+__global__ void __launch_bounds__(256, 4) quantize_blocks_kernel(long long rows, int d,
                                                               const uint4* __restrict__ x,
                                                               uint2* __restrict__ q,
                                                               float* __restrict__ scale) {

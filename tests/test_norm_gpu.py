@@ -72,8 +72,9 @@ def test_backward(N, d):
         terms = terms + (0 if dsum is None else np.abs(f64(dsum)))
         # c's terms, added in at most 56 steps, are each off by rstd's error twice
         assert np.all(np.abs(f64(b["dx"]) - dx) <= BF * np.abs(dx) + 3 * E32 * terms)
-        # dweight: at most ceil(N / 296) rows per slice, then 19 + 16 slices; rstd's error per term
-        steps = -(-N // 296) + 35
+        # dweight: at most ceil(N / 148) rows per slice, then every 16th of at most 2368 slices and
+        # these 16 sums; rstd's error per term
+        steps = -(-N // 148) + 148 + 16
         mags = (np.abs(g) * n).sum(0)
         assert np.all(np.abs(f64(b["dweight"]) - dw) <= BF * np.abs(dw) + (E32 + (steps + 2) * 2.0 ** -24) * mags)
 
