@@ -183,21 +183,37 @@ lmh_status launch_few(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t 
   return last_launch();
 }
 
-template <class Out>
+// Logits [N, V] for stores of 32 rows x 64 bytes.
+bool tmap_logits(CUtensorMap* m, void* base, uint64_t V, uint64_t N, bool f32) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t es = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {V, N};
+  cuuint64_t strides[1] = {V * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / es), 32};
+  cuuint32_t one[2] = {1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+            box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class Out, bool TMA>
 lmh_status launch_many(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t d, int dev, int sms,
                        cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
-  LMH_TRY(allow_smem(fp8_many_kernel<Out>, FpMany::SMEM, dev, &done));
-  CUtensorMap tw, th;
+  LMH_TRY(allow_smem(fp8_many_kernel<Out, TMA>, FpMany::SMEM, dev, &done));
+  CUtensorMap tw, th, to;
   if (!tmap_8bit(&tw, W8, d, p.V, FpMany::TV) || !tmap_8bit(&th, H8, d, p.N, kFpM))
     return LMH_ERR_CUDA;
+  to = th;
+  if (TMA && !tmap_logits(&to, p.out, p.V, p.N, sizeof(Out) == 4)) return LMH_ERR_CUDA;
   p.vtiles = static_cast<int>(cdiv(p.V, FpMany::TV));
   p.ntiles = static_cast<int>(cdiv(p.N, kFpM));
   const int64_t tiles = static_cast<int64_t>(p.vtiles) * p.ntiles;
   if (tiles > 0x7fff0000LL) return LMH_ERR_INVALID_ARG;
   ProfScope ps(KID_FP8_LOGITS, st);
-  fp8_many_kernel<Out><<<static_cast<unsigned>(tiles < sms ? tiles : sms), FpMany::THREADS,
-                         FpMany::SMEM, st>>>(tw, th, p);
+  fp8_many_kernel<Out, TMA><<<static_cast<unsigned>(tiles < sms ? tiles : sms), FpMany::THREADS,
+                              FpMany::SMEM, st>>>(tw, th, to, p);
   return last_launch();
 }
 
@@ -207,7 +223,9 @@ lmh_status launch_fp8(const FpParams& p, const uint8_t* H8, const uint8_t* W8, i
   if (p.N <= 16) return launch_few<16, Out>(p, H8, W8, d, dev, sms, st);
   if (p.N <= 32) return launch_few<32, Out>(p, H8, W8, d, dev, sms, st);
   if (p.N <= 64) return launch_few<64, Out>(p, H8, W8, d, dev, sms, st);
-  return launch_many<Out>(p, H8, W8, d, dev, sms, st);
+  const bool tma = aligned16(p.out) && p.V * sizeof(Out) % 16 == 0;
+  return tma ? launch_many<Out, true>(p, H8, W8, d, dev, sms, st)
+             : launch_many<Out, false>(p, H8, W8, d, dev, sms, st);
 }
 
 }  // namespace

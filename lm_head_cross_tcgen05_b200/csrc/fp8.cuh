@@ -244,20 +244,60 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------- many tokens
+// 32 TMEM columns of a warp's lanes, not waited for; tmem_landed() is what the values pass through.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
+// acc += (a, b) * f in both halves, one instruction for the two.
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t a, uint32_t b, uint64_t f) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+      : "+l"(acc) : "r"(a), "r"(b), "l"(f));
+}
+
 struct FpMany {
   static constexpr int TV = 256;          // vocabulary rows per tile
-  static constexpr int THREADS = 320;     // 8 epilogue warps: each half of the columns
+  static constexpr int THREADS = 384;     // a warpgroup of loads and MMAs, two of epilogue
   static constexpr int NBUF = 2, TMEM = 512;
   static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TV * kFpK, STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 4;
-  static constexpr int TRANS = 8 * 32 * 33 * 4;  // per warp: a 32 x 32 block, padded
-  static constexpr int SMEM = STAGES * STAGE + TRANS + 1024;
+  static constexpr int OUT = 8 * 4224;    // per epilogue warp: two 2 KB boxes (512-byte aligned), or 32 x 33 floats
+  static constexpr int SMEM = STAGES * STAGE + OUT + 1024;
+  // registers a thread: 384 x 168 at the launch, then 128 x 40 + 256 x 232, which is the same sum
+  static constexpr int REG_LOAD = 40, REG_EPI = 232;
 };
 
-template <class Out>
+// The epilogue warps are what bounds this kernel: per block of 128 columns each reads 128 TMEM
+// columns and adds 128 scaled values, while the tensor core needs 512 cycles for the block. So the
+// next 32 columns are under way while 32 are added, two values an instruction, and the 128 sums
+// and two sets of columns stay in registers, which the loading warps give up theirs for. TMA: the
+// output goes out by TMA from staged boxes of 32 tokens x 64 bytes, where its rows are 16-byte
+// aligned; otherwise by 32 x 32 transposes through shared memory.
+template <class Out, bool TMA>
 __global__ void __launch_bounds__(FpMany::THREADS, 1)
     fp8_many_kernel(const __grid_constant__ CUtensorMap tmW,
-                    const __grid_constant__ CUtensorMap tmH, const FpParams p) {
+                    const __grid_constant__ CUtensorMap tmH,
+                    const __grid_constant__ CUtensorMap tmOut, const FpParams p) {
   using C = FpMany;
   constexpr int STAGES = C::STAGES, NBUF = C::NBUF, TV = C::TV;
   extern __shared__ uint8_t dsmem[];
@@ -289,8 +329,9 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REG_LOAD));
+    if (warp == 0 && lane == 0) {
       tma_prefetch_desc(&tmW);
       tma_prefetch_desc(&tmH);
       uint32_t kbg = 0;
@@ -309,9 +350,7 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
         }
       }
       wait_loads<STAGES>(full_bar, kbg, p.err);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       constexpr uint32_t idesc = make_idesc_e4m3(kFpM, TV);
       uint32_t kbg = 0;
       for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
@@ -336,23 +375,26 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
       mbar_wait(smem_u32(&drain_bar), 0, p.err);
     }
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lanes 32 q .., columns 128 half ..
-    float* tr = reinterpret_cast<float*>(dsmem + (smem_base - smem_u32(dsmem)) + STAGES * C::STAGE) +
-                (warp - 2) * 32 * 33;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_EPI));
+    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns 128 half ..
+    const uint32_t room = smem_base + STAGES * C::STAGE + (warp - 4) * (TMA ? 4096 : 4224);
     Out* out = static_cast<Out*>(p.out);
-    uint32_t kbg = 0;
+    uint32_t kbg = 0, boxes = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const long long v0 = static_cast<long long>(t / p.ntiles) * TV + half * 128;
       const long long r0 = static_cast<long long>(t % p.ntiles) * kFpM + q * 32;  // warp's tokens
       const bool row_ok = r0 + lane < p.N, col_ok = v0 < p.V;
       const float* hs = p.hs + (row_ok ? r0 + lane : 0) * p.nb;
       const float* ws = p.ws + (col_ok ? v0 / kFpK : 0) * p.nb;
-      float acc[128] = {};
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0;
       float next = __ldg(hs) * __ldg(ws);
       bool ok = true;
       for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
         const uint32_t b = kbg % NBUF;
-        const float f = next;
+        uint64_t f;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(next)));
         if (kb + 1 < p.nb) next = __ldg(hs + kb + 1) * __ldg(ws + kb + 1);
         ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
         ok = __all_sync(0xffffffffu, ok);
@@ -360,37 +402,79 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
         tc_fence_after();
         const uint32_t taddr =
             tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TV + half * 128;
+        uint32_t v[2][32];
+        tmem_ld32_start(taddr, v[0]);
 #pragma unroll
-        for (int g = 0; g < 128; g += 32) {
-          float v[32];
-          tmem_ld32(taddr + g, v);
+        for (int g = 0; g < 4; ++g) {
+          tmem_landed(v[g & 1]);
+          if (g < 3) {
+            tmem_ld32_start(taddr + 32 * (g + 1), v[(g + 1) & 1]);
+          } else {  // all columns are read: the next block may be accumulated here
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[g + i] = fmaf(v[i], f, acc[g + i]);
+          for (int i = 0; i < 16; ++i) fma2(acc[g * 16 + i], v[g & 1][2 * i], v[g & 1][2 * i + 1], f);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
       }
       if (!ok) {
         abort_flag = 1;
         break;
       }
-      // a lane holds one token's columns: turn 32 x 32 blocks so that a store's 32 lanes are
-      // adjacent columns of one token, whatever V's alignment
+      if (TMA) {
+        constexpr int COLS = 64 / sizeof(Out);  // per box
 #pragma unroll
-      for (int g = 0; g < 128; g += 32) {
-        __syncwarp();
+        for (int g = 0; g < 128 / COLS; ++g) {
+          if (v0 + g * COLS >= p.V || r0 >= p.N) continue;  // of the whole warp
+          const uint32_t box = room + (boxes++ & 1) * 2048;  // of those issued, every other one
+          if (lane == 0) bulk_wait_read_le1();  // the box before last has been read
+          __syncwarp();
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) tr[lane * 33 + i] = acc[g + i];
-        __syncwarp();
-        const long long v = v0 + g + lane;
-        if (v < p.V) {
+          for (int i = 0; i < 16; ++i) {
+            if constexpr (sizeof(Out) == 4) {
+              w[i] = (i & 1) ? static_cast<uint32_t>(acc[g * 8 + i / 2] >> 32) : static_cast<uint32_t>(acc[g * 8 + i / 2]);
+            } else {
+              const uint64_t a = acc[g * 16 + i];
+              w[i] = pack_bf16x2(__uint_as_float(static_cast<uint32_t>(a)), __uint_as_float(static_cast<uint32_t>(a >> 32)));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // 64-byte rows, 16-byte chunks permuted by the row as TMA reads them
+            st_shared_v4(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4),
+                         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmOut, box, static_cast<int>(v0 + g * COLS), static_cast<int>(r0));
+            bulk_commit();
+          }
+        }
+      } else {
+        // a lane holds one token's columns: turn 32 x 32 blocks so that a store's 32 lanes are
+        // adjacent columns of one token, whatever V's alignment
+        float* tr = reinterpret_cast<float*>(dsmem + (room - smem_u32(dsmem)));
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            tr[lane * 33 + 2 * i] = __uint_as_float(static_cast<uint32_t>(acc[g * 16 + i]));
+            tr[lane * 33 + 2 * i + 1] = __uint_as_float(static_cast<uint32_t>(acc[g * 16 + i] >> 32));
+          }
+          __syncwarp();
+          const long long v = v0 + g * 32 + lane;
+          if (v < p.V) {
+            const int rows = static_cast<int>(p.N - r0 < 32 ? p.N - r0 : 32);
+            Out* o = out + r0 * p.V + v;
 #pragma unroll 8
-          for (int i = 0; i < 32; ++i)
-            if (r0 + i < p.N) put_logit(out, (r0 + i) * p.V + v, tr[i * 33 + lane]);
+            for (int i = 0; i < rows; ++i, o += p.V) put_logit(o, 0, tr[i * 33 + lane]);
+          }
         }
       }
     }
+    if (TMA && lane == 0) bulk_wait_all();  // every box has reached global memory
   }
   tc_fence_before();
   __syncthreads();
