@@ -389,30 +389,35 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
+      // block kbg's accumulator is complete: its first 32 columns start their way
+      uint32_t v[2][32];
+      auto column = [&](uint32_t kbg) {
+        return tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (kbg % NBUF) * TV + half * 128;
+      };
+      auto begin = [&](uint32_t kbg) -> bool {
+        bool ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[kbg % NBUF]), (kbg / NBUF) & 1u, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        tc_fence_after();
+        tmem_ld32_start(column(kbg), v[0]);
+        return true;
+      };
       float next = __ldg(hs) * __ldg(ws);
-      bool ok = true;
-      for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
-        const uint32_t b = kbg % NBUF;
+      bool ok = begin(kbg);
+      for (int kb = 0; kb < p.nb && ok; ++kb, ++kbg) {
         uint64_t f;
         asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(next)));
         if (kb + 1 < p.nb) next = __ldg(hs + kb + 1) * __ldg(ws + kb + 1);
-        ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr =
-            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TV + half * 128;
-        uint32_t v[2][32];
-        tmem_ld32_start(taddr, v[0]);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           tmem_landed(v[g & 1]);
           if (g < 3) {
-            tmem_ld32_start(taddr + 32 * (g + 1), v[(g + 1) & 1]);
-          } else {  // all columns are read: the next block may be accumulated here
+            tmem_ld32_start(column(kbg) + 32 * (g + 1), v[(g + 1) & 1]);
+          } else {  // all columns are read: the block after next may be accumulated here
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
+            if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[kbg % NBUF]));
+            if (kb + 1 < p.nb) ok = begin(kbg + 1);
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) fma2(acc[g * 16 + i], v[g & 1][2 * i], v[g & 1][2 * i + 1], f);
