@@ -277,22 +277,25 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint32_t a, uint32_t b, uint
 
 struct FpMany {
   static constexpr int TV = 256;          // vocabulary rows per tile
-  static constexpr int THREADS = 384;     // a warpgroup of loads and MMAs, two of epilogue
+  static constexpr int EPI = 16;          // epilogue warps: 64 columns each of a lane quarter
+  static constexpr int COLS = TV / (EPI / 4);
+  static constexpr int THREADS = 128 + 32 * EPI;
   static constexpr int NBUF = 2, TMEM = 512;
   static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TV * kFpK, STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 4;
-  static constexpr int OUT = 8 * 4224;    // per epilogue warp: two 2 KB boxes (512-byte aligned), or 32 x 33 floats
-  static constexpr int SMEM = STAGES * STAGE + OUT + 1024;
-  // registers a thread: 384 x 168 at the launch, then 128 x 40 + 256 x 232, which is the same sum
-  static constexpr int REG_LOAD = 40, REG_EPI = 232;
+  static constexpr int BOX = 2048;        // per epilogue warp: 32 tokens x 64 bytes (512-byte aligned)
+  static constexpr int SMEM = STAGES * STAGE + EPI * BOX + 1024;
+  // registers a thread: 640 x 96 at the launch (61440), then 128 x 24 + 512 x 112 (60416)
+  static constexpr int REG_LOAD = 24, REG_EPI = 112;
 };
 
-// The epilogue warps are what bounds this kernel: per block of 128 columns each reads 128 TMEM
-// columns and adds 128 scaled values, while the tensor core needs 512 cycles for the block. So the
-// next 32 columns are under way while 32 are added, two values an instruction, and the 128 sums
-// and two sets of columns stay in registers, which the loading warps give up theirs for. TMA: the
-// output goes out by TMA from staged boxes of 32 tokens x 64 bytes, where its rows are 16-byte
-// aligned; otherwise by 32 x 32 transposes through shared memory.
+// An accumulator is held from its MMAs (512 cycles) until its last column is read, and two of them
+// are all that TMEM holds; so what bounds this kernel is how long reading takes. 16 warps read at
+// once, 64 columns each with the sums in registers, which the loading warps give up theirs for;
+// the additions take two values an instruction. (4096 x 32000 x 2048 to bf16: 349 us with eight
+// warps of 128 columns, 320 with their next columns read ahead across blocks.)
+// TMA: the output goes out by TMA from staged boxes of 32 tokens x 64 bytes, where its rows are
+// 16-byte aligned; otherwise by transposes of 32 x 16 through shared memory.
 template <class Out, bool TMA>
 __global__ void __launch_bounds__(FpMany::THREADS, 1)
     fp8_many_kernel(const __grid_constant__ CUtensorMap tmW,
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
     }
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(smem_u32(&tfull_bar[b]), 1);
-      mbar_init(smem_u32(&tempty_bar[b]), 8);
+      mbar_init(smem_u32(&tempty_bar[b]), C::EPI);
     }
     mbar_init(smem_u32(&drain_bar), 1);
     abort_flag = 0;
@@ -376,51 +379,44 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_EPI));
-    const int q = warp & 3, half = (warp - 4) >> 2;  // TMEM lanes 32 q .., columns 128 half ..
-    const uint32_t room = smem_base + STAGES * C::STAGE + (warp - 4) * (TMA ? 4096 : 4224);
+    constexpr int COLS = C::COLS;
+    const int q = warp & 3, c0 = ((warp - 4) >> 2) * COLS;  // TMEM lanes 32 q .., columns c0 ..
+    const uint32_t box = smem_base + STAGES * C::STAGE + (warp - 4) * C::BOX;
     Out* out = static_cast<Out*>(p.out);
-    uint32_t kbg = 0, boxes = 0;
+    uint32_t kbg = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const long long v0 = static_cast<long long>(t / p.ntiles) * TV + half * 128;
+      const long long v0 = static_cast<long long>(t / p.ntiles) * TV + c0;
       const long long r0 = static_cast<long long>(t % p.ntiles) * kFpM + q * 32;  // warp's tokens
       const bool row_ok = r0 + lane < p.N, col_ok = v0 < p.V;
       const float* hs = p.hs + (row_ok ? r0 + lane : 0) * p.nb;
       const float* ws = p.ws + (col_ok ? v0 / kFpK : 0) * p.nb;
-      uint64_t acc[64];
+      uint64_t acc[COLS / 2];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      // block kbg's accumulator is complete: its first 32 columns start their way
-      uint32_t v[2][32];
-      auto column = [&](uint32_t kbg) {
-        return tmem_base + (static_cast<uint32_t>(q * 32) << 16) + (kbg % NBUF) * TV + half * 128;
-      };
-      auto begin = [&](uint32_t kbg) -> bool {
-        bool ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[kbg % NBUF]), (kbg / NBUF) & 1u, p.err);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        tc_fence_after();
-        tmem_ld32_start(column(kbg), v[0]);
-        return true;
-      };
+      for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
       float next = __ldg(hs) * __ldg(ws);
-      bool ok = begin(kbg);
-      for (int kb = 0; kb < p.nb && ok; ++kb, ++kbg) {
+      bool ok = true;
+      for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+        const uint32_t b = kbg % NBUF;
         uint64_t f;
         asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(next)));
         if (kb + 1 < p.nb) next = __ldg(hs + kb + 1) * __ldg(ws + kb + 1);
+        ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TV + c0;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          tmem_landed(v[g & 1]);
-          if (g < 3) {
-            tmem_ld32_start(column(kbg) + 32 * (g + 1), v[(g + 1) & 1]);
-          } else {  // all columns are read: the block after next may be accumulated here
+        for (int g = 0; g < COLS / 32; ++g) {
+          uint32_t v[32];
+          tmem_ld32_start(taddr + 32 * g, v);
+          tmem_landed(v);
+          if (g == COLS / 32 - 1) {  // all columns are read: the block after next may go here
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[kbg % NBUF]));
-            if (kb + 1 < p.nb) ok = begin(kbg + 1);
+            if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(acc[g * 16 + i], v[g & 1][2 * i], v[g & 1][2 * i + 1], f);
+          for (int i = 0; i < 16; ++i) fma2(acc[g * 16 + i], v[2 * i], v[2 * i + 1], f);
         }
       }
       if (!ok) {
@@ -428,12 +424,11 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
         break;
       }
       if (TMA) {
-        constexpr int COLS = 64 / sizeof(Out);  // per box
+        constexpr int PER = 64 / sizeof(Out);  // columns per box
 #pragma unroll
-        for (int g = 0; g < 128 / COLS; ++g) {
-          if (v0 + g * COLS >= p.V || r0 >= p.N) continue;  // of the whole warp
-          const uint32_t box = room + (boxes++ & 1) * 2048;  // of those issued, every other one
-          if (lane == 0) bulk_wait_read_le1();  // the box before last has been read
+        for (int g = 0; g < COLS / PER; ++g) {
+          if (v0 + g * PER >= p.V || r0 >= p.N) continue;  // of the whole warp
+          if (lane == 0) bulk_wait_read_all();  // the box before has been read
           __syncwarp();
           uint32_t w[16];
 #pragma unroll
@@ -452,29 +447,29 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tmOut, box, static_cast<int>(v0 + g * COLS), static_cast<int>(r0));
+            tma_store_2d(&tmOut, box, static_cast<int>(v0 + g * PER), static_cast<int>(r0));
             bulk_commit();
           }
         }
       } else {
-        // a lane holds one token's columns: turn 32 x 32 blocks so that a store's 32 lanes are
-        // adjacent columns of one token, whatever V's alignment
-        float* tr = reinterpret_cast<float*>(dsmem + (room - smem_u32(dsmem)));
+        // a lane holds one token's columns: turn 32 x 16 blocks so that half a warp stores adjacent
+        // columns of one token, whatever V's alignment; column c of row r lies at c ^ (r & 15)
+        float* tr = reinterpret_cast<float*>(dsmem + (box - smem_u32(dsmem)));
+        const int c = lane & 15;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < COLS / 16; ++g) {
           __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            tr[lane * 33 + 2 * i] = __uint_as_float(static_cast<uint32_t>(acc[g * 16 + i]));
-            tr[lane * 33 + 2 * i + 1] = __uint_as_float(static_cast<uint32_t>(acc[g * 16 + i] >> 32));
+          for (int i = 0; i < 8; ++i) {
+            tr[lane * 16 + ((2 * i) ^ (lane & 15))] = __uint_as_float(static_cast<uint32_t>(acc[g * 8 + i]));
+            tr[lane * 16 + ((2 * i + 1) ^ (lane & 15))] = __uint_as_float(static_cast<uint32_t>(acc[g * 8 + i] >> 32));
           }
           __syncwarp();
-          const long long v = v0 + g * 32 + lane;
+          const long long v = v0 + g * 16 + c;
           if (v < p.V) {
-            const int rows = static_cast<int>(p.N - r0 < 32 ? p.N - r0 : 32);
-            Out* o = out + r0 * p.V + v;
 #pragma unroll 8
-            for (int i = 0; i < rows; ++i, o += p.V) put_logit(o, 0, tr[i * 33 + lane]);
+            for (int i = lane >> 4; i < 32; i += 2)
+              if (r0 + i < p.N) put_logit(out, (r0 + i) * p.V + v, tr[i * 16 + (c ^ (i & 15))]);
           }
         }
       }
