@@ -174,9 +174,8 @@ lmh_status launch_few(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t 
   CUtensorMap tw, th;
   if (!tmap_8bit(&tw, W8, d, p.V, kFpM) || !tmap_8bit(&th, H8, d, p.N, TN)) return LMH_ERR_CUDA;
   p.vtiles = static_cast<int>(cdiv(p.V, kFpM));
-  p.ntiles = static_cast<int>(cdiv(p.N, TN));
-  const int64_t tiles = static_cast<int64_t>(p.vtiles) * p.ntiles;
-  if (tiles > 0x7fff0000LL) return LMH_ERR_INVALID_ARG;
+  p.ntiles = 1;
+  const int64_t tiles = p.vtiles;
   ProfScope ps(KID_FP8_LOGITS, st);
   fp8_few_kernel<TN, Out><<<static_cast<unsigned>(tiles < sms ? tiles : sms), FpFew<TN>::THREADS,
                             FpFew<TN>::SMEM, st>>>(tw, th, p);
@@ -220,9 +219,10 @@ lmh_status launch_many(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t
 template <class Out>
 lmh_status launch_fp8(const FpParams& p, const uint8_t* H8, const uint8_t* W8, int64_t d, int dev,
                       int sms, cudaStream_t st) {
-  if (p.N <= 16) return launch_few<16, Out>(p, H8, W8, d, dev, sms, st);
-  if (p.N <= 32) return launch_few<32, Out>(p, H8, W8, d, dev, sms, st);
-  if (p.N <= 64) return launch_few<64, Out>(p, H8, W8, d, dev, sms, st);
+  const bool few = p.nb <= kFewBlocks;
+  if (few && p.N <= 16) return launch_few<16, Out>(p, H8, W8, d, dev, sms, st);
+  if (few && p.N <= 32) return launch_few<32, Out>(p, H8, W8, d, dev, sms, st);
+  if (few && p.N <= 64) return launch_few<64, Out>(p, H8, W8, d, dev, sms, st);
   const bool tma = aligned16(p.out) && p.V * sizeof(Out) % 16 == 0;
   return tma ? launch_many<Out, true>(p, H8, W8, d, dev, sms, st)
              : launch_many<Out, false>(p, H8, W8, d, dev, sms, st);
@@ -249,8 +249,7 @@ extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
   LMH_TRY(current_device(&dev, &sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Ws ws{static_cast<uint8_t*>(workspace), static_cast<WsHeader*>(workspace)};
-  LMH_TRY(clear_header(ws, st));
-  if (shape->N == 0) return LMH_OK;
+  if (shape->N == 0) return clear_header(ws, st);  // else the kernel clears the error word
   FpParams p{};
   p.N = shape->N;
   p.V = shape->V;
@@ -353,8 +352,7 @@ extern "C" lmh_status lmh_sample(const lmh_shape* shape, const lmh_sampling* opt
   LMH_TRY(current_device(&dev, &sms));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const Ws ws{static_cast<uint8_t*>(workspace), static_cast<WsHeader*>(workspace)};
-  LMH_TRY(clear_header(ws, st));
-  if (shape->N == 0) return LMH_OK;
+  if (shape->N == 0) return clear_header(ws, st);  // else the first kernel clears the error word
   SampParams p{};
   p.N = shape->N;
   p.V = static_cast<int>(shape->V);

@@ -27,6 +27,9 @@ namespace lmh {
 constexpr int kFpK = 128;  // columns per scale block and per stage
 constexpr int kFpM = 128;  // accumulator lanes
 
+// Scale blocks per row (d up to 8192) whose token scales the few-token kernel keeps.
+constexpr int kFewBlocks = 64;
+
 template <int TN>
 struct FpFew {
   static constexpr int THREADS = 192;
@@ -34,7 +37,8 @@ struct FpFew {
   static constexpr int TMEM = TN * NBUF;
   static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TN * kFpK, STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = TN == 64 ? 8 : 10;
-  static constexpr int SMEM = STAGES * STAGE + 1024;
+  static constexpr int HS = kFewBlocks * TN * 4;  // the tokens' scales
+  static constexpr int SMEM = STAGES * STAGE + HS + 1024;
 };
 
 // kind::f8f6f4: e4m3 A and B (format 0), K-major both, fp32 accumulator.
@@ -69,11 +73,11 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
 struct FpParams {
   long long N, V;
   int nb;              // scale blocks per row
-  int vtiles, ntiles;  // tiles over the vocabulary and the tokens
+  int vtiles, ntiles;  // tiles over the vocabulary and the tokens (few tokens: one)
   const float* hs;     // [N, nb]
   const float* ws;     // [ceil(V / 128), nb]
   void* out;           // [N, V] fp32 or bf16
-  uint32_t* err;
+  uint32_t* err;       // cleared by the first block: a wait that sets it gives up seconds later
 };
 
 __device__ __forceinline__ void put_logit(float* out, long long i, float x) { out[i] = x; }
@@ -90,6 +94,12 @@ __device__ __forceinline__ void wait_loads(const uint64_t* full_bar, uint32_t is
     mbar_wait(smem_u32(&full_bar[i % STAGES]), (i / STAGES) & 1u, err);
 }
 
+// acc += (a, b) * (h * w) in both halves; the product of the scales is rounded once.
+__device__ __forceinline__ void add_scaled(uint64_t& acc, float a, float b, uint64_t h, uint64_t w) {
+  asm("{\n\t.reg .b64 v, s;\n\tmov.b64 v, {%1, %2};\n\tmul.rn.f32x2 s, %3, %4;\n\tfma.rn.f32x2 %0, v, s, %0;\n\t}"
+      : "+l"(acc) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "l"(h), "l"(w));
+}
+
 template <int TN, class Out>
 __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
     fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmH,
@@ -99,13 +109,14 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[NBUF],
       tempty_bar[NBUF], drain_bar;
-  __shared__ __align__(16) float sc[4][2][TN];  // per epilogue warp: the tokens' scales, two blocks
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
   const uint32_t smem_base = (smem_u32(dsmem) + 1023u) & ~1023u;
+  float* hs = reinterpret_cast<float*>(dsmem + (smem_base - smem_u32(dsmem)) + STAGES * C::STAGE);  // [nb][TN]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tiles = p.vtiles * p.ntiles;
+  const int tiles = p.vtiles;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -132,7 +143,7 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
       tma_prefetch_desc(&tmH);
       uint32_t kbg = 0;
       for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
-        const int v0 = (t / p.ntiles) * kFpM, n0 = (t % p.ntiles) * TN;
+        const int v0 = t * kFpM;
         for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
           const uint32_t s = kbg % STAGES;
           if (!mbar_wait(smem_u32(&empty_bar[s]), ((kbg / STAGES) & 1u) ^ 1u, p.err)) {
@@ -142,7 +153,7 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
           const uint32_t bar = smem_u32(&full_bar[s]), dst = smem_base + s * C::STAGE;
           mbar_arrive_expect_tx(bar, C::STAGE);
           tma_load_2d(dst, &tmW, bar, kb * kFpK, v0);
-          tma_load_2d(dst + C::A_BYTES, &tmH, bar, kb * kFpK, n0);
+          tma_load_2d(dst + C::A_BYTES, &tmH, bar, kb * kFpK, 0);
         }
       }
       wait_loads<STAGES>(full_bar, kbg, p.err);
@@ -174,38 +185,42 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
       mbar_wait(smem_u32(&drain_bar), 0, p.err);
     }
   } else {
-    constexpr int PL = (TN + 31) / 32;  // token scales per lane
     constexpr int G = TN >= 32 ? 32 : 16;
     const int q = warp & 3;  // TMEM lanes 32 q .. 32 q + 31
+    // every tile has the same tokens: their scales stay in shared memory, block by block
+    for (int i = threadIdx.x - 64; i < p.nb * TN; i += 128) {
+      const int n = i % TN;
+      hs[i] = n < p.N ? __ldg(p.hs + n * p.nb + i / TN) : 0.f;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");  // the four epilogue warps, which all come here
+    // a tile's scales of W8, 32 blocks in a warp's lanes, the next 32 (of the next tile, at the end)
+    // on their way
+    auto w32 = [&](int t, int kb0) {
+      return t < tiles && kb0 + lane < p.nb ? __ldg(p.ws + static_cast<long long>(t) * p.nb + kb0 + lane) : 0.f;
+    };
     uint32_t kbg = 0;
+    float wnext = w32(blockIdx.x, 0);
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-      const int vt = t / p.ntiles;
-      const long long n0 = static_cast<long long>(t % p.ntiles) * TN;
-      const float* ws = p.ws + static_cast<long long>(vt) * p.nb;
-      float acc[TN] = {};
-      float next[PL];
+      uint64_t acc[TN / 2];
 #pragma unroll
-      for (int j = 0; j < PL; ++j) {
-        const long long n = n0 + lane + 32 * j;
-        next[j] = n < p.N ? __ldg(p.hs + n * p.nb) * __ldg(ws) : 0.f;
-      }
+      for (int i = 0; i < TN / 2; ++i) acc[i] = 0;
+      float wnow = 0.f;
       bool ok = true;
       for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
-        const uint32_t b = kbg % NBUF;
-        float* mine = sc[q][kbg & 1];  // read two blocks ago: a __syncwarp lies between
-#pragma unroll
-        for (int j = 0; j < PL; ++j) {
-          const long long n = n0 + lane + 32 * j;
-          if (lane + 32 * j < TN) mine[lane + 32 * j] = next[j];
-          if (n < p.N && kb + 1 < p.nb) next[j] = __ldg(p.hs + n * p.nb + kb + 1) * __ldg(ws + kb + 1);
+        if ((kb & 31) == 0) {
+          wnow = wnext;
+          wnext = kb + 32 < p.nb ? w32(t, kb + 32) : w32(t + gridDim.x, 0);
         }
+        const float w = __shfl_sync(0xffffffffu, wnow, kb & 31);
+        uint64_t w2;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(w2) : "r"(__float_as_uint(w)));
+        const uint32_t b = kbg % NBUF;
         ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        __syncwarp();
         tc_fence_after();
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TN;
-        const float4* s4 = reinterpret_cast<const float4*>(mine);
+        const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(hs + kb * TN);  // two pairs each
 #pragma unroll
         for (int g = 0; g < TN; g += G) {
           float v[G];
@@ -213,11 +228,9 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
           else tmem_ld16(taddr + g, v);
 #pragma unroll
           for (int i = 0; i < G; i += 4) {
-            const float4 f = s4[(g + i) / 4];
-            acc[g + i] = fmaf(v[i], f.x, acc[g + i]);
-            acc[g + i + 1] = fmaf(v[i + 1], f.y, acc[g + i + 1]);
-            acc[g + i + 2] = fmaf(v[i + 2], f.z, acc[g + i + 2]);
-            acc[g + i + 3] = fmaf(v[i + 3], f.w, acc[g + i + 3]);
+            const ulonglong2 f = s2[(g + i) / 4];
+            add_scaled(acc[(g + i) / 2], v[i], v[i + 1], f.x, w2);
+            add_scaled(acc[(g + i) / 2 + 1], v[i + 2], v[i + 3], f.y, w2);
           }
         }
         tc_fence_before();
@@ -228,12 +241,13 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
         abort_flag = 1;
         break;
       }
-      const long long v = static_cast<long long>(vt) * kFpM + q * 32 + lane;
+      const long long v = static_cast<long long>(t) * kFpM + q * 32 + lane;
       if (v < p.V) {
         Out* out = static_cast<Out*>(p.out);
 #pragma unroll
         for (int i = 0; i < TN; ++i)
-          if (n0 + i < p.N) put_logit(out, (n0 + i) * p.V + v, acc[i]);
+          if (i < p.N)
+            put_logit(out, i * p.V + v, __uint_as_float(static_cast<uint32_t>(i & 1 ? acc[i / 2] >> 32 : acc[i / 2])));
       }
     }
   }
@@ -282,18 +296,23 @@ struct FpMany {
   static constexpr int THREADS = 128 + 32 * EPI;
   static constexpr int NBUF = 2, TMEM = 512;
   static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TV * kFpK, STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 4;
+  static constexpr int STAGES = 3;
+  static constexpr int SLOTS = 8;         // blocks whose scales are in shared memory
   static constexpr int BOX = 2048;        // per epilogue warp: 32 tokens x 64 bytes (512-byte aligned)
-  static constexpr int SMEM = STAGES * STAGE + EPI * BOX + 1024;
-  // registers a thread: 640 x 96 at the launch (61440), then 128 x 24 + 512 x 112 (60416)
-  static constexpr int REG_LOAD = 24, REG_EPI = 112;
+  static constexpr int SC = 132;          // floats per slot: 128 tokens', 2 vocabulary blocks'
+  static constexpr int SMEM = STAGES * STAGE + EPI * BOX + SLOTS * SC * 4 + 1024;
+  // registers a thread: 640 x 96 at the launch, then 128 x 32 + 512 x 112, which is the same sum
+  static constexpr int REG_LOAD = 32, REG_EPI = 112;
 };
 
 // An accumulator is held from its MMAs (512 cycles) until its last column is read, and two of them
-// are all that TMEM holds; so what bounds this kernel is how long reading takes. 16 warps read at
-// once, 64 columns each with the sums in registers, which the loading warps give up theirs for;
-// the additions take two values an instruction. (4096 x 32000 x 2048 to bf16: 349 us with eight
-// warps of 128 columns, 320 with their next columns read ahead across blocks.)
+// are all that TMEM holds; so what bounds this kernel is the way round: commit, wake, read, arrive,
+// wake, MMAs. 16 warps read at once, 64 columns each with the sums in registers, which the loading
+// warps give up theirs for; the additions take two values an instruction; and a spare warp brings
+// the scales to shared memory, since a load of their own would make the reading warps wait.
+// (4096 x 32000 x 2048 to bf16: 349 us with eight warps of 128 columns, 306 with 16, and see below
+// for the scales. A copy without any TMEM reads took 302 us where this took 326, and pairs of CTAs
+// that share a 256 x 256 tile, whose ways round are longer, took 660.)
 // TMA: the output goes out by TMA from staged boxes of 32 tokens x 64 bytes, where its rows are
 // 16-byte aligned; otherwise by transposes of 32 x 16 through shared memory.
 template <class Out, bool TMA>
@@ -306,22 +325,25 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
   extern __shared__ uint8_t dsmem[];
   __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[NBUF],
       tempty_bar[NBUF], drain_bar;
+  __shared__ __align__(8) uint64_t scale_bar[C::SLOTS];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
   const uint32_t smem_base = (smem_u32(dsmem) + 1023u) & ~1023u;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tiles = p.vtiles * p.ntiles;  // tokens fastest: a wave shares few tiles of W8
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&full_bar[s]), 1 + 32);  // the loads' transaction, and the scales' 32 lanes
       mbar_init(smem_u32(&empty_bar[s]), 1);
     }
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(smem_u32(&tfull_bar[b]), 1);
       mbar_init(smem_u32(&tempty_bar[b]), C::EPI);
     }
+    for (int s = 0; s < C::SLOTS; ++s) mbar_init(smem_u32(&scale_bar[s]), 32);
     mbar_init(smem_u32(&drain_bar), 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -376,34 +398,68 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
       }
       mma_commit(smem_u32(&drain_bar));
       mbar_wait(smem_u32(&drain_bar), 0, p.err);
+    } else if (warp == 2) {
+      // Scales of block kbg into slot kbg % SLOTS. That is free: stage kbg % STAGES being free, the
+      // MMAs of block kbg - STAGES are done, so they were begun, so the block NBUF before that was
+      // read, scales and all, and the slot's last block is older.
+      static_assert(C::SLOTS >= STAGES + NBUF + 1, "a slot's last block has been read");
+      uint32_t kbg = 0;
+      for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
+        const int vb = (t / p.ntiles) * (TV / kFpK), n0 = (t % p.ntiles) * kFpM;
+        const bool wv = lane < TV / kFpK && static_cast<long long>(vb + lane) * kFpK < p.V;
+        const float* ws = p.ws + (wv ? vb + lane : 0ll) * p.nb;
+        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
+          const uint32_t s = kbg % STAGES, slot = kbg % C::SLOTS;
+          if (!mbar_wait(smem_u32(&empty_bar[s]), ((kbg / STAGES) & 1u) ^ 1u, p.err)) {
+            abort_flag = 1;
+            break;
+          }
+          const uint32_t dst = smem_base + STAGES * C::STAGE + C::EPI * C::BOX + slot * C::SC * 4;
+#pragma unroll
+          for (int j = 0; j < kFpM / 32; ++j) {
+            const int n = n0 + lane + 32 * j;
+            const int bytes = n < p.N ? 4 : 0;  // 0 past the last token
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + (lane + 32 * j) * 4),
+                         "l"(p.hs + (n < p.N ? static_cast<long long>(n) * p.nb + kb : 0ll)), "r"(bytes)
+                         : "memory");
+          }
+          if (lane < TV / kFpK)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + (kFpM + lane) * 4),
+                         "l"(ws + kb), "r"(wv ? 4 : 0)
+                         : "memory");
+          // for the epilogue; and for the MMAs, which would otherwise run ahead of this warp, so
+          // that it would wait for a phase of empty_bar that lies two behind
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&scale_bar[slot])) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full_bar[s])) : "memory");
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REG_EPI));
     constexpr int COLS = C::COLS;
     const int q = warp & 3, c0 = ((warp - 4) >> 2) * COLS;  // TMEM lanes 32 q .., columns c0 ..
     const uint32_t box = smem_base + STAGES * C::STAGE + (warp - 4) * C::BOX;
+    const float* sc = reinterpret_cast<const float*>(dsmem + (smem_base - smem_u32(dsmem)) + STAGES * C::STAGE + C::EPI * C::BOX);
     Out* out = static_cast<Out*>(p.out);
     uint32_t kbg = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const long long v0 = static_cast<long long>(t / p.ntiles) * TV + c0;
       const long long r0 = static_cast<long long>(t % p.ntiles) * kFpM + q * 32;  // warp's tokens
-      const bool row_ok = r0 + lane < p.N, col_ok = v0 < p.V;
-      const float* hs = p.hs + (row_ok ? r0 + lane : 0) * p.nb;
-      const float* ws = p.ws + (col_ok ? v0 / kFpK : 0) * p.nb;
       uint64_t acc[COLS / 2];
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
-      float next = __ldg(hs) * __ldg(ws);
       bool ok = true;
       for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
-        const uint32_t b = kbg % NBUF;
-        uint64_t f;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(next)));
-        if (kb + 1 < p.nb) next = __ldg(hs + kb + 1) * __ldg(ws + kb + 1);
-        ok = !abort_flag && mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
+        const uint32_t b = kbg % NBUF, slot = kbg % C::SLOTS;
+        ok = !abort_flag && mbar_wait(smem_u32(&scale_bar[slot]), (kbg / C::SLOTS) & 1u, p.err) &&
+             mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
+        const float s = sc[slot * C::SC + q * 32 + lane] * sc[slot * C::SC + kFpM + c0 / kFpK];
+        uint64_t f;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(s)));
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TV + c0;
 #pragma unroll
         for (int g = 0; g < COLS / 32; ++g) {

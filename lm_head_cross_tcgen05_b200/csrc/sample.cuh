@@ -364,6 +364,7 @@ template <class T>
 __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const SampParams p) {
   __shared__ double table[64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;  // the kernels that follow set its bits
   const int per_row = (p.blocks + kGroupWarps * kGroupPer - 1) / (kGroupWarps * kGroupPer);
   const long long row = blockIdx.x / per_row;
   const int b0 = (static_cast<int>(blockIdx.x - row * per_row) * kGroupWarps + warp) * kGroupPer;

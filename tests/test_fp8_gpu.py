@@ -148,3 +148,19 @@ def test_another_stream_and_two_graphs():
         streams[0].synchronize()
         assert torch.equal(z, got)
         check(z, *ops)
+
+
+@pytest.mark.parametrize("N", [3, 40, 70])
+def test_long_rows(N):
+    """More scale blocks than the few-token kernel keeps, and just as many."""
+    for d in (8192, 8256, 16448):
+        ops = operands(N, 260, d, seed=d)
+        check(L.fp8_logits(*ops)["logits"], *ops)
+
+
+def test_stale_error_word_is_cleared():
+    ops = operands(2, 300, 128)
+    shape = L.make_shape(2, 128, 300)
+    ws = torch.full((L.lmh_workspace_size(shape, L.ENTRY_FP8_LOGITS),), 255, dtype=torch.uint8, device="cuda")
+    L.fp8_logits(*ops, ws=ws)
+    assert L.lmh_read_errors(ws) == 0
