@@ -24,7 +24,7 @@
 
 namespace lmh {
 
-constexpr int kFpK = 128;  // columns per scale block and per stage
+constexpr int kFpK = 128;  // columns per scale block
 constexpr int kFpM = 128;  // accumulator lanes
 
 // Scale blocks per row (d up to 8192) whose token scales the few-token kernel keeps.
@@ -35,8 +35,11 @@ struct FpFew {
   static constexpr int THREADS = 192;
   static constexpr int NBUF = 4;  // TMEM accumulators
   static constexpr int TMEM = TN * NBUF;
-  static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TN * kFpK, STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = TN == 64 ? 8 : 10;
+  // A stage is KB blocks: the MMA thread's wait and commit per stage hold up the next loads.
+  // 128256 x 4096, 1 / 64 tokens: one block a stage 100.6 / 116 us, two 87.3 / 104.5, four (two
+  // stages) 87.1 / 102.5.
+  static constexpr int KB = 2, A_BYTES = kFpM * kFpK, B_BYTES = TN * kFpK, STAGE = KB * (A_BYTES + B_BYTES);
+  static constexpr int STAGES = TN == 64 ? 4 : 5;
   static constexpr int HS = kFewBlocks * TN * 4;  // the tokens' scales
   static constexpr int SMEM = STAGES * STAGE + HS + 1024;
 };
@@ -141,45 +144,55 @@ __global__ void __launch_bounds__(FpFew<TN>::THREADS, 1)
     if (lane == 0) {
       tma_prefetch_desc(&tmW);
       tma_prefetch_desc(&tmH);
-      uint32_t kbg = 0;
+      uint32_t it = 0;
       for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
         const int v0 = t * kFpM;
-        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
-          const uint32_t s = kbg % STAGES;
-          if (!mbar_wait(smem_u32(&empty_bar[s]), ((kbg / STAGES) & 1u) ^ 1u, p.err)) {
+        for (int kb = 0; kb < p.nb; kb += C::KB, ++it) {
+          const uint32_t s = it % STAGES;
+          if (!mbar_wait(smem_u32(&empty_bar[s]), ((it / STAGES) & 1u) ^ 1u, p.err)) {
             abort_flag = 1;
             break;
           }
           const uint32_t bar = smem_u32(&full_bar[s]), dst = smem_base + s * C::STAGE;
           mbar_arrive_expect_tx(bar, C::STAGE);
-          tma_load_2d(dst, &tmW, bar, kb * kFpK, v0);
-          tma_load_2d(dst + C::A_BYTES, &tmH, bar, kb * kFpK, 0);
+#pragma unroll
+          for (int j = 0; j < C::KB; ++j) {  // past the last block: zeros
+            tma_load_2d(dst + j * C::A_BYTES, &tmW, bar, (kb + j) * kFpK, v0);
+            tma_load_2d(dst + C::KB * C::A_BYTES + j * C::B_BYTES, &tmH, bar, (kb + j) * kFpK, 0);
+          }
         }
       }
-      wait_loads<STAGES>(full_bar, kbg, p.err);
+      wait_loads<STAGES>(full_bar, it, p.err);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = make_idesc_e4m3(kFpM, TN);
-      uint32_t kbg = 0;
-      for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
-        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
-          const uint32_t s = kbg % STAGES, b = kbg % NBUF;
-          if (!mbar_wait(smem_u32(&tempty_bar[b]), ((kbg / NBUF) & 1u) ^ 1u, p.err) ||
-              !mbar_wait(smem_u32(&full_bar[s]), (kbg / STAGES) & 1u, p.err)) {
-            abort_flag = 1;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t a = smem_base + s * C::STAGE, h = a + C::A_BYTES;
+      uint32_t kbg = 0, it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        for (int kb = 0; kb < p.nb && ok; kb += C::KB, ++it) {
+          const uint32_t s = it % STAGES;
+          ok = !abort_flag && mbar_wait(smem_u32(&full_bar[s]), (it / STAGES) & 1u, p.err);
 #pragma unroll
-          for (int k = 0; k < kFpK / 32; ++k)
-            mma_e4m3(tmem_base + b * TN, make_sw128_desc(a + k * 32, 16, 1024),
-                     make_sw128_desc(h + k * 32, 16, 1024), idesc, k != 0);
-          mma_commit(smem_u32(&empty_bar[s]));
-          mma_commit(smem_u32(&tfull_bar[b]));
+          for (int j = 0; j < C::KB; ++j) {
+            if (!ok || kb + j >= p.nb) break;
+            const uint32_t b = kbg % NBUF;
+            ok = mbar_wait(smem_u32(&tempty_bar[b]), ((kbg / NBUF) & 1u) ^ 1u, p.err);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = smem_base + s * C::STAGE + j * C::A_BYTES;
+            const uint32_t h = smem_base + s * C::STAGE + C::KB * C::A_BYTES + j * C::B_BYTES;
+#pragma unroll
+            for (int k = 0; k < kFpK / 32; ++k)
+              mma_e4m3(tmem_base + b * TN, make_sw128_desc(a + k * 32, 16, 1024),
+                       make_sw128_desc(h + k * 32, 16, 1024), idesc, k != 0);
+            mma_commit(smem_u32(&tfull_bar[b]));
+            ++kbg;
+          }
+          if (ok) mma_commit(smem_u32(&empty_bar[s]));
         }
       }
+      if (!ok) abort_flag = 1;
       // No MMA may still be writing TMEM when the columns are released.
       mma_commit(smem_u32(&drain_bar));
       mbar_wait(smem_u32(&drain_bar), 0, p.err);
