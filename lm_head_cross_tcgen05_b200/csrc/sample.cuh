@@ -110,11 +110,9 @@ struct ListShared {
   u64 list[kSampList];           // candidates, key << 32 | ~id
   union {
     u64 wlist[kSampList];        // their weights, once sorted
-    struct {
-      uint32_t queue[kSampList]; // groups that hold candidates
-      uint4 chist[kSampBuckets / 4];
-    };
+    uint32_t queue[kSampList];   // groups that hold candidates
   };
+  uint4 chist[kSampBuckets / 4];
   uint32_t list_n, queue_n;
   int pick;
   u64 base;
@@ -258,6 +256,54 @@ __device__ __forceinline__ void sort_desc(u64* a, int n) {
       if (stride > 32 || (stride == 1 && size >= 64)) __syncthreads();
       else __syncwarp();
     }
+}
+
+// The same for up to 2048 values, bucket(x) from 0 to 2047 never falling as x does: by a histogram of
+// the buckets, then within each, unless one has more than 64. 330 values take 3000 cycles and 1400 values 5000,
+// where counting took 5500 and the network 29000.
+template <class B>
+__device__ __forceinline__ void sort_buckets(u64* a, int n, uint4* chist, u64* red, B bucket) {
+  const int tid = threadIdx.x;
+  if (n <= 128) return sort_desc(a, n);
+  constexpr int PER = kSampList / kSampThreads;
+  uint32_t* hist = reinterpret_cast<uint32_t*>(chist);
+  static_assert(kSampBuckets == 4 * kSampThreads, "four buckets a thread");
+  chist[tid] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  u64 x[PER];
+  int b[PER], at[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    x[j] = tid + j * kSampThreads < n ? a[tid + j * kSampThreads] : 0;
+    if (x[j]) {
+      b[j] = bucket(x[j]);
+      at[j] = static_cast<int>(atomicAdd(&hist[b[j]], 1u));
+    }
+  }
+  __syncthreads();
+  const uint4 h = chist[tid];
+  if (__syncthreads_or(max(max(h.x, h.y), max(h.z, h.w)) > 64u)) return sort_desc(a, n);
+  u64 before, all;
+  block_scan(h.x + h.y + h.z + h.w, &before, &all, red);
+  const uint32_t c = static_cast<uint32_t>(before);
+  chist[tid] = make_uint4(c, c + h.x, c + h.x + h.y, c + h.x + h.y + h.z);
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (x[j]) a[hist[b[j]] + at[j]] = x[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (!x[j]) continue;
+    const int from = hist[b[j]], to = b[j] + 1 < kSampBuckets ? static_cast<int>(hist[b[j] + 1]) : n;
+    at[j] = from;
+    for (int i = from; i < to; ++i) at[j] += a[i] > x[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (x[j]) a[at[j]] = x[j];
+  __syncthreads();
 }
 
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -575,54 +621,83 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       if (bm < b0) b0 = static_cast<int>(bm);
     }
     __syncthreads();
-    each_group([&](float m, int g) {
-      const bool hit = R.bucket(m) <= b0;  // not -inf
-      const uint32_t mask = __ballot_sync(0xffffffffu, hit);
-      if (!mask) return;
+    // up_to(z): bucket(z) <= b0, z not -inf
+    const float last_x = static_cast<float>(b0 + 1);
+    auto up_to = [&](float z) { return fmaf(-0.5f, z, R.half_max) * R.bucket_scale < last_x; };
+#pragma unroll 1
+    for (int g0 = tid; g0 - tid < groups; g0 += 4 * kSampThreads) {
+      float m[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m[j] = g0 + j * kSampThreads < groups ? gmax[g0 + j * kSampThreads] : -INFINITY;
+      uint32_t mask[4], count = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mask[j] = __ballot_sync(0xffffffffu, up_to(m[j]));
+        count += __popc(mask[j]);
+      }
+      if (!count) continue;
       uint32_t at = 0;
-      if (lane == 0) at = atomicAdd(&sh.queue_n, __popc(mask));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1));
-      if (hit && at < kSampList) sh.queue[at] = g;
-    });
+      if (lane == 0) at = atomicAdd(&sh.queue_n, count);
+      at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t to = at + __popc(mask[j] & ((1u << lane) - 1));
+        if (((mask[j] >> lane) & 1) && to < kSampList) sh.queue[to] = g0 + j * kSampThreads;
+        at += __popc(mask[j]);
+      }
+    }
     __syncthreads();
     // every queued group holds a candidate: more of them than the list holds leave the row
     if (sh.queue_n > kSampList) break;
     const int queued = static_cast<int>(sh.queue_n);
-    // eight groups at a time, their candidates counted in one step: the counter is one address
-#pragma unroll 1
-    for (int q0 = warp; q0 < queued; q0 += 8 * kSampWarps) {
-      float z[8];
-      int id[8];
+    // eight groups at a time, their candidates counted in one step (the counter is one address),
+    // while the next eight are loaded
+    float z[8];
+    uint32_t id[8];
+    const uint32_t lane_at = (lane >> 2) * 32 + (lane & 3);
+    auto load = [&](int q0) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int q = q0 + j * kSampWarps;
         const uint32_t g = q < queued ? sh.queue[q] : 0;
-        const long long i = static_cast<long long>(g / kGroups) * kBlock + (lane >> 2) * 32 + (g % kGroups) * 4 + (lane & 3);
-        const bool in = q < queued && i < p.V;
-        z[j] = in ? as_float(src[i]) : 0.f;
-        id[j] = in ? static_cast<int>(i) : -1;
+        id[j] = g / kGroups * kBlock + g % kGroups * 4 + lane_at;
+        z[j] = q < queued && id[j] < static_cast<uint32_t>(p.V) ? as_float(src[id[j]]) : -INFINITY;  // no candidate
       }
-      uint32_t mask[8], count = 0;
+    };
+    if (warp < queued) load(warp);
+#pragma unroll 1
+    for (int q0 = warp; q0 < queued; q0 += 8 * kSampWarps) {
+      float y[8];
+      uint32_t mask[8], to[8], count = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        mask[j] = __ballot_sync(0xffffffffu, id[j] >= 0 && R.bucket(z[j]) <= b0);
+        y[j] = z[j];
+        to[j] = id[j];
+        mask[j] = __ballot_sync(0xffffffffu, up_to(y[j]));
         count += __popc(mask[j]);
       }
+      if (q0 + 8 * kSampWarps < queued) load(q0 + 8 * kSampWarps);
       uint32_t at = 0;
       if (lane == 0) at = atomicAdd(&sh.list_n, count);
       at = __shfl_sync(0xffffffffu, at, 0);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint32_t to = at + __popc(mask[j] & ((1u << lane) - 1));
-        if (((mask[j] >> lane) & 1) && to < kSampList)
-          sh.list[to] = (static_cast<u64>(sort_key(z[j])) << 32) | static_cast<uint32_t>(~id[j]);
+        if ((mask[j] >> lane) & 1) {
+          const uint32_t slot = at + __popc(mask[j] & ((1u << lane) - 1));
+          if (slot < kSampList) sh.list[slot] = (static_cast<u64>(sort_key(y[j])) << 32) | ~to[j];
+        }
         at += __popc(mask[j]);
       }
     }
     __syncthreads();
     if (sh.list_n > kSampList) break;
     const int n = static_cast<int>(sh.list_n);
-    sort_desc(sh.list, n);
+    // as bucket(), but those up to b0 fill all of them
+    const float finer = R.bucket_scale * (static_cast<float>(kSampBuckets) / (b0 + 1));
+    sort_buckets(sh.list, n, sh.chist, sh.red[0], [&](u64 x) {
+      const float z = key_value(static_cast<uint32_t>(x >> 32));
+      return static_cast<int>(fminf(fmaf(-0.5f, z, R.half_max) * finer, kSampBuckets - 1.f));
+    });
 
     // ---- kept: nk by count, the first by min-p, and by top-p up to the first whose running
     // weight reaches its part of what top-k kept, or of the row
@@ -661,8 +736,16 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       if (at >= 0) {
         keep = min(keep, at + 1);
       } else if (!all_listed) {  // else all are listed, and the target past them by a rounding
-        // each missing one weighs at most what the last listed one does
-        more = f.k == 0 && want < kSampListK && (target - weight) / max(sh.wlist[n - 1], 1ull) < kSampListK;
+        // The weights' fall from half of the list to its end, w(i) ~ i^-s, continued: it falls faster, so
+        // that a list with no room for what is missing by this count has none (a choice of the
+        // kernel, not of the token).
+        if (f.k == 0 && want < kSampListK) {
+          const float w = static_cast<float>(max(sh.wlist[n - 1], 1ull));
+          const float s = log2f(static_cast<float>(sh.wlist[n / 2]) / w), l = log2f(static_cast<float>(kSampList) / n);
+          const float t = (1.f - s) * l * 0.6931471805599453f;  // integral of (i / n)^-s over i / n up to 2048 / n
+          const float part = fabsf(t) > 1e-3f ? (expf(t) - 1.f) / (1.f - s) : l * 0.6931471805599453f;
+          more = static_cast<float>(target - weight) < w * n * part;
+        }
         want = kSampListK;
         __syncthreads();  // the list is read before it is written again
         continue;
@@ -674,7 +757,10 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       const u64 x = c + tid < keep ? (sh.list[c + tid] << 32) | static_cast<uint32_t>(c + tid) : 0;
       if (c + tid < keep) sh.list[c + tid] = x;
     }
-    sort_desc(sh.list, keep);
+    const float per_id = static_cast<float>(kSampBuckets) / p.V;
+    sort_buckets(sh.list, keep, sh.chist, sh.red[0], [&](u64 x) {
+      return static_cast<int>(fminf(static_cast<float>(~static_cast<uint32_t>(x >> 32)) * per_id, kSampBuckets - 1.f));
+    });
     u64 all = 0;
     for (int c = 0; c < keep; c += kSampThreads) {
       const int i = c + tid;
