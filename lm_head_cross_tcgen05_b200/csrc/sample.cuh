@@ -43,6 +43,7 @@ constexpr int kSampMaxC = 8;
 constexpr int kBlock = 256;       // logits per sum of exponentials
 constexpr int kGroups = 8;        // maxima per block: group g has the logits 32 j + 4 g + i of the
                                   // block, j < 8 and i < 4 (what four lanes load)
+constexpr int kSampBatch = 96;  // logits that a warp of the row kernel gathers before it works on them
 constexpr int kParts = 4;         // partial sums per warp that locate() keeps
 constexpr int kSampPending = -2;  // tokens[row] of a row that the list kernel leaves
 
@@ -125,10 +126,11 @@ struct alignas(16) RowShared {
       uint32_t lo[kSampBuckets], hi[kSampBuckets];
     } whist;                                 // halves of the bins' weights
     u64 list[kSampList];                     // members of a bucket, on the cluster's first CTA
-    float keep[kSampWarps][256];             // weigh(): logits whose weights are still to be added
   };
+  int keep[kSampWarps][kSampBatch + 64];     // gather(): places in the chunk
   uint4 chist[kSampBuckets / 4];
   u64 part[kSampWarps][kParts];              // locate(): partial sums of each warp's segment
+  u64 top[kSampWarps][kParts];               // prefix(): those of the weights above its window
   u64 tot_a[kSampMaxC], tot_l[kSampMaxC];    // per CTA, written by each into all: sum_row(), locate()
   u64 tot_b[kSampMaxC];
   u64 found[4];                              // bin, its members, count before, weight before
@@ -169,9 +171,10 @@ struct SampRow {
   int F;
   const double* table;
 
+  // monotone in z, as each of the two roundings is; halved, no finite difference overflows
+  __device__ __forceinline__ float place(float z) const { return fmaf(-0.5f, z, half_max) * bucket_scale; }
   __device__ __forceinline__ int bucket(float z) const {
-    // monotone in z, as each of the two roundings is; halved, no finite difference overflows
-    const float x = fmaf(-0.5f, z, half_max) * bucket_scale;
+    const float x = place(z);
     return x < static_cast<float>(kSampBuckets) ? static_cast<int>(x) : kSampBuckets;
   }
   // 64 log2 of the probability over the largest one's
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
     __syncthreads();
     // up_to(z): bucket(z) <= b0, z not -inf
     const float last_x = static_cast<float>(b0 + 1);
-    auto up_to = [&](float z) { return fmaf(-0.5f, z, R.half_max) * R.bucket_scale < last_x; };
+    auto up_to = [&](float z) { return R.place(z) < last_x; };
 #pragma unroll 1
     for (int g0 = tid; g0 - tid < groups; g0 += 4 * kSampThreads) {
       float m[4];
@@ -926,56 +929,69 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
     samp_sync();  // also: every CTA has read the histograms
     return sh.hit != 0;
   };
-  // This lane's part of the sum of the weights in the warp's [b0, b1) that `has` keeps. Kept logits
-  // are gathered until they are four for each lane: where few are, their weights cost few of the
-  // warp's instructions.
-  auto weigh = [&](int b0, int b1, auto has) -> u64 {
-    float* keep = sh.keep[warp];
+  // work(n) for the logits of the warp's [b0, b1) that `has` keeps, up to 96 of them at a time:
+  // their places in the chunk are keep[0 .. n). What a kept one costs is paid for full warps; done
+  // where they lie, with one lane in ten, a pass took three times as long.
+  int* keep = sh.keep[warp];
+  auto gather = [&](int b0, int b1, auto has, auto work) {
     int n = 0;
-    u64 s = 0;
-    auto add = [&]() {  // up to 128 of them; the rest moves down
-      __syncwarp();
-      float x[4], rest[4];
+    float z[2], next[2];
+    auto load = [&](int i) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[j] = lane + 32 * j < n ? keep[lane + 32 * j] : -INFINITY;
-        rest[j] = keep[128 + lane + 32 * j];
-      }
-      __syncwarp();
-      n = max(n - 128, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (lane + 32 * j < n) keep[lane + 32 * j] = rest[j];
-        s += R.weight(x[j]);
-      }
+      for (int j = 0; j < 2; ++j) next[j] = i + 32 * j < b1 ? as_float(src[i + 32 * j]) : -INFINITY;
     };
+    load(b0 + lane);
 #pragma unroll 1
-    for (int i = b0 + lane; i - lane < b1; i += 128) {
-      float z[4];
+    for (int i = b0 + lane; i - lane < b1; i += 64) {
+      uint32_t mask[2];
+      bool mine[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) z[j] = i + 32 * j < b1 ? as_float(src[i + 32 * j]) : -INFINITY;
+      for (int j = 0; j < 2; ++j) z[j] = next[j];
+      load(i + 64);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool mine = has(z[j], c0 + i + 32 * j);
-        const uint32_t mask = __ballot_sync(0xffffffffu, mine);
-        if (mine) keep[n + __popc(mask & ((1u << lane) - 1))] = z[j];
-        n += __popc(mask);
+      for (int j = 0; j < 2; ++j) {
+        mine[j] = has(z[j], c0 + i + 32 * j);
+        mask[j] = __ballot_sync(0xffffffffu, mine[j]);
       }
-      if (n >= 128) add();
+      if (!(mask[0] | mask[1])) continue;
+      const uint32_t below = (1u << lane) - 1;
+      if (mine[0]) keep[n + __popc(mask[0] & below)] = i;
+      n += __popc(mask[0]);
+      if (mine[1]) keep[n + __popc(mask[1] & below)] = i + 32;
+      n += __popc(mask[1]);
+      if (n >= kSampBatch) {
+        __syncwarp();
+        work(kSampBatch);
+        __syncwarp();
+        n -= kSampBatch;  // below 64; the rest moves down
+        const int x = lane < n ? keep[kSampBatch + lane] : 0, y = lane + 32 < n ? keep[kSampBatch + lane + 32] : 0;
+        if (lane < n) keep[lane] = x;
+        if (lane + 32 < n) keep[lane + 32] = y;
+      }
     }
-    if (n) add();
     __syncwarp();
+    if (n) work(n);
+    __syncwarp();
+  };
+  // This lane's part of the sum of the weights in the warp's [b0, b1) that `has` keeps.
+  auto weigh = [&](int b0, int b1, auto has) -> u64 {
+    u64 s = 0;
+    gather(b0, b1, has, [&](int n) {
+#pragma unroll
+      for (int j = 0; j < kSampBatch / 32; ++j) s += lane + 32 * j < n ? R.weight(as_float(src[keep[lane + 32 * j]])) : 0;
+    });
     return s;
   };
   // The id at which the running sum, in vocabulary order, of fn(z, id) passes r = target(sum over
-  // the row); -1 where another warp holds it. part(b0, b1) is this lane's part of the sum of fn.
+  // the row); -1 where another warp holds it. part(q, b0, b1) is this lane's part of the sum of fn
+  // over part q of the warp's logits.
+  const int span = ((s1 - s0 + kParts - 1) / kParts + 31) / 32 * 32;  // logits per part
   auto locate = [&](auto fn, auto part, auto target) -> int {
-    const int span = ((s1 - s0 + kParts - 1) / kParts + 31) / 32 * 32;  // logits per part
     u64 mine = 0;
 #pragma unroll 1
     for (int q = 0; q < kParts; ++q) {
       if (s0 + q * span >= s1) break;
-      const u64 s = warp_sum64(part(s0 + q * span, min(s1, s0 + (q + 1) * span)));
+      const u64 s = warp_sum64(part(q, s0 + q * span, min(s1, s0 + (q + 1) * span)));
       if (lane == 0) sh.part[warp][q] = s;
       mine += s;
     }
@@ -1013,8 +1029,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
   };
 
   // The last candidate of the shortest prefix of those at or above `from` whose count (by_w false)
-  // or weight reaches the target; 0 if all of them do not reach it.
-  auto prefix = [&](bool by_w, u64 from, u64 target) -> u64 {
+  // or weight reaches the target; 0 if all of them do not reach it. whole: the weight of all of them.
+  int top_lo = 0;  // sh.top has the weights of the buckets below it
+  auto prefix = [&](bool by_w, u64 from, u64 target, u64 whole) -> u64 {
     // a window of buckets from an eighth of the row; all buckets for a short one
     int lo = 0, hi = kSampBuckets - 1;
     if (p.V > 32768) {
@@ -1023,7 +1040,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
       sweep(s0 + (warp & 7) * 32, s1, 8, [&](float z, int id) {
         const int k = R.bucket(z);
         sampled += id < c0 + s1;
-        if (k < kSampBuckets && compose(z, id) >= from) atomicAdd(&chist[k], 1u);
+        if (k < kSampBuckets && (from == 0 || compose(z, id) >= from)) atomicAdd(&chist[k], 1u);
       });
       sampled = sum_row(sampled);
       u64 hc[4], hw[4], at, all;
@@ -1044,7 +1061,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
         own += hw[j];
       }
       block_scan(own, &at, &all, sh.red[0]);
-      const double t = by_w ? static_cast<double>(f.top_p) * static_cast<double>(all)
+      // the weight from the target on, as a part of the eighth's: of many small weights, where
+      // those before may be of a few large ones, which an eighth may miss
+      const double rest = static_cast<double>(whole - target) * __hiloint2double((1023 + 30 - p.F) << 20, 0) *
+                          static_cast<double>(sampled) / p.V;
+      const double t = by_w ? static_cast<double>(all) - rest
                             : static_cast<double>(target) * static_cast<double>(sampled) / p.V;
       const double t0 = by_w ? t - 0.02 * static_cast<double>(all) : 0.9 * t - 16.0;
       const double t1 = by_w ? t + 0.02 * static_cast<double>(all) : 1.1 * t + 16.0;
@@ -1061,19 +1082,44 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
     }
     for (int pass = 0;; ++pass) {  // the second with all buckets
       u64 above = 0;
-      if (by_w && lo > 0) above = weigh(s0, s1, [&](float z, int id) { return R.bucket(z) < lo && compose(z, id) >= from; });
-      __syncthreads();
       zero(by_w);
-      sweep(s0, s1, 1, [&](float z, int id) {
-        const int k = R.bucket(z);
-        if (k > hi || compose(z, id) < from) return;
-        if (k < lo) {
-          above += !by_w;
-          return;
+      // up to the window's end; those before it are counted or weighed, those in it join its buckets
+      const float hi_x = static_cast<float>(hi + 1);
+      auto up_to = [&](float z, int id) {
+        const bool in = R.place(z) < hi_x;
+        return from == 0 ? in : in && compose(z, id) >= from;
+      };
+      top_lo = by_w ? lo : 0;
+#pragma unroll 1
+      for (int q = 0; q < kParts; ++q) {
+        if (s0 + q * span >= s1) break;
+        u64 s = 0;
+        gather(s0 + q * span, min(s1, s0 + (q + 1) * span), up_to, [&](int n) {
+          float z[kSampBatch / 32];
+          u64 w[kSampBatch / 32];
+#pragma unroll
+          for (int j = 0; j < kSampBatch / 32; ++j) {
+            z[j] = lane + 32 * j < n ? as_float(src[keep[lane + 32 * j]]) : -INFINITY;
+            w[j] = by_w ? R.weight(z[j]) : 1;
+          }
+#pragma unroll
+          for (int j = 0; j < kSampBatch / 32; ++j) {
+            if (lane + 32 * j >= n) continue;
+            const int k = R.bucket(z[j]);
+            if (k < lo) {
+              s += w[j];
+            } else {
+              atomicAdd(&chist[k], 1u);
+              if (by_w) add_weight(k, w[j]);
+            }
+          }
+        });
+        above += s;
+        if (top_lo > 0) {
+          const u64 of_warp = warp_sum64(s);
+          if (lane == 0) sh.top[warp][q] = of_warp;
         }
-        atomicAdd(&chist[k], 1u);
-        if (by_w) add_weight(k, R.weight(z));
-      });
+      }
       if (search(by_w, target, sum_row(above), lo, hi)) break;
       if (pass == 1 || (lo == 0 && hi == kSampBuckets - 1)) return 0;
       lo = 0;
@@ -1081,13 +1127,19 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
     }
     const int bucket0 = static_cast<int>(sh.found[0]);
     u64 members = sh.found[1], before = sh.found[2];
+    const float bucket_from = static_cast<float>(bucket0), bucket_end = static_cast<float>(bucket0 + 1);
     uint32_t klo = 0, khi = 0xffffffffu;
+    bool all_keys = true;
     auto member = [&](float z, int id) {
+      const float x = R.place(z);
+      const bool in = (x >= bucket_from) & (x < bucket_end);
+      if (from == 0 && all_keys) return in;
       const uint32_t key = sort_key(z);
-      return key >= klo && key <= khi && R.bucket(z) == bucket0 && compose(z, id) >= from;
+      return in && key >= klo && key <= khi && compose(z, id) >= from;
     };
     // 2048 ranges a level: after three levels a range is one key
-    for (int level = 0; level < 4 && members > kSampList; ++level) {
+    int levels = 0;
+    for (; levels < 4 && members > kSampList; ++levels) {
       uint32_t l = 0xffffffffu, h = 0;  // the members' smallest and largest key
       sweep(s0, s1, 1, [&](float z, int id) {
         if (member(z, id)) {
@@ -1113,6 +1165,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
         dsm_st64(&sh.tot_b[rank], tid, y);
       }
       samp_sync();
+      all_keys = false;
       klo = 0xffffffffu;
       khi = 0;
       for (int r = 0; r < C; ++r) {
@@ -1126,7 +1179,7 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
           need = (need + w - 1) / w;
         }
         auto one = [&](float z, int i) -> u64 { return member(z, i); };
-        const int id = locate(one, [&](int b0, int b1) {
+        const int id = locate(one, [&](int, int b0, int b1) {
           u64 s = 0;
           sweep(b0, b1, 1, [&](float z, int i) { s += one(z, i); });
           return s;
@@ -1153,16 +1206,28 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
       klo = low > khi ? klo : max(klo, low);
     }
     // the members go to the first CTA and are sorted
-    sweep(s0, s1, 1, [&](float z, int id) {
-      if (member(z, id)) {
-        const uint32_t at = dsm_add32(&sh.list_n, 0, 1);
-        if (at < kSampList) dsm_st64(&sh.list[at], 0, compose(z, id));
+    gather(s0, s1, member, [&](int n) {
+      uint32_t at = 0;
+      if (lane == 0) at = dsm_add32(&sh.list_n, 0, n);
+      at = __shfl_sync(0xffffffffu, at, 0) + lane;
+#pragma unroll
+      for (int j = 0; j < kSampBatch / 32; ++j) {
+        if (lane + 32 * j >= n || at + 32 * j >= kSampList) continue;
+        const int i = keep[lane + 32 * j];
+        dsm_st64(&sh.list[at + 32 * j], 0, compose(as_float(src[i]), c0 + i));
       }
     });
     samp_sync();
     if (rank == 0) {
       const int n = static_cast<int>(min(members, static_cast<u64>(kSampList)));
-      sort_desc(sh.list, n);
+      // by the place within the bucket, or within what is left of its keys
+      const int shift = max(0, 32 - __clz(khi - klo) - 11);
+      sort_buckets(sh.list, n, sh.chist, sh.red[0], [&](u64 x) {
+        const uint32_t key = static_cast<uint32_t>(x >> 32);
+        if (levels > 0) return static_cast<int>(min((khi - key) >> shift, kSampBuckets - 1u));
+        const float at = R.place(key_value(key)) - static_cast<float>(bucket0);
+        return static_cast<int>(fminf(fmaxf(at, 0.f) * static_cast<float>(kSampBuckets), kSampBuckets - 1.f));
+      });
       for (int c = 0; c < n; c += kSampThreads) {
         const int i = c + tid;
         const u64 x = i >= n ? 0 : (by_w ? R.weight(key_value(static_cast<uint32_t>(sh.list[i] >> 32))) : 1);
@@ -1181,23 +1246,36 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
 
   u64 cut = 0;  // every (key, id) is above
   if (f.k > 0) {
-    cut = prefix(false, 0, f.k);
+    cut = prefix(false, 0, f.k, 0);
     samp_sync();  // cut is read before it is written again
   }
   if (f.use_p) {
     u64 all = f.whole(total, p.F);
     if (f.k > 0) all = sum_row(weigh(s0, s1, [&](float z, int id) { return R.bucket(z) < kSampBuckets && compose(z, id) >= cut; }));
-    cut = max(cut, prefix(true, cut, f.p_target(all)));  // 0 if the target is past all by a rounding
+    cut = max(cut, prefix(true, cut, f.p_target(all), all));  // 0 if the target is past all by a rounding
   }
   // min-p as a bucket, to pass over most of the row; a logit's own test is in fp64
   const double bm = f.use_m ? -f.low64 / 64.0 * (kSampBuckets / static_cast<double>(p.F)) + 1.0 : kSampBuckets;
   const int last = static_cast<int>(fmin(bm, kSampBuckets - 1.0));
+  // the bucket of the cut; those before it lie above, whatever their ids
+  const int cut_bucket = cut ? R.bucket(key_value(static_cast<uint32_t>(cut >> 32))) : kSampBuckets;
+  const float end_x = static_cast<float>(min(last, cut_bucket) + 1), cut_x = static_cast<float>(cut_bucket);
   auto kept = [&](float z, int id) {
-    if (R.bucket(z) > last || compose(z, id) < cut) return false;
+    const float x = R.place(z);
+    if (!(x < end_x)) return false;
+    if (x >= cut_x && compose(z, id) < cut) return false;
     return !f.use_m || R.y64(z) >= f.low64;
   };
+  // What prefix() weighed is kept whole where the cut lies below it and min-p does not cut: the
+  // rest of the row has few that are kept.
+  if (f.use_m || cut_bucket < top_lo) top_lo = 0;
+  const float top_x = static_cast<float>(top_lo);
   const int id = locate([&](float z, int i) -> u64 { return kept(z, i) ? R.weight(z) : 0; },
-                        [&](int b0, int b1) { return weigh(b0, b1, kept); }, [&](u64 all) { return f.draw_at(all); });
+                        [&](int q, int b0, int b1) {
+                          const u64 s = weigh(b0, b1, [&](float z, int i) { return R.place(z) >= top_x && kept(z, i); });
+                          return s + (top_lo > 0 && lane == 0 ? sh.top[warp][q] : 0);
+                        },
+                        [&](u64 all) { return f.draw_at(all); });
   if (id >= 0 && lane == 0) {
     p.tokens[row] = id;
     if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(static_cast<const T*>(p.logits)[row * p.V + id]), total);
