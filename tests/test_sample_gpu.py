@@ -278,3 +278,55 @@ def test_decode_step():
     x.copy_(x.flip(0)), r.copy_(r.flip(0)), u.copy_(u.flip(0))
     graph.replay()
     assert torch.equal(c["tokens"], o["tokens"].flip(0))
+
+
+@pytest.mark.parametrize("scale", [0.5, 1.5, 4.0])
+@pytest.mark.parametrize("V", [40009, 140000])
+def test_long_prefixes(V, scale):
+    """Flat rows, whose prefixes hold from a few to most of the logits."""
+    z, u = logits(2, V, seed=24, scale=scale)
+    for kw in (dict(p=0.05), dict(p=0.5), dict(p=0.9), dict(p=0.995), dict(p=0.9, m=1e-4), dict(p=0.7, m=0.3), dict(k=5000, p=0.9),
+               dict(k=30000, p=0.5, m=1e-3), dict(k=V - 1, p=0.999)):
+        check(z, u, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(k=600), dict(k=900, p=0.97), dict(p=0.8), dict(k=200, p=0.5)])
+def test_likely_tokens_in_one_run_of_ids(kw):
+    z, u = logits(3, 150001, seed=25, scale=0.5)
+    z[0, 40000:41000] += 30
+    z[1, :1000] += 30
+    z[2, -1000:] += 30
+    check(z, u, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(p=0.9), dict(k=130), dict(k=400, p=0.6), dict(k=900), dict(m=0.02)])
+@pytest.mark.parametrize("V", [400, 1900])
+def test_few_different_values(V, kw):
+    check(*logits(4, V, seed=26, scale=1.0, digits=0), **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(k=20), dict(p=0.9), dict(k=3000)])
+def test_workspace_of_any_content(kw):
+    z, u = logits(5, 33001, seed=27)
+    names = dict(k="top_k", p="top_p")
+    kw2 = {names[k]: v for k, v in kw.items()}
+    ref = check(z, u, **kw)
+    for fill in (0, 255):
+        ws = torch.full_like(ref["workspace"], fill)
+        o = L.sample(z, u, ws=ws, **kw2)
+        assert torch.equal(o["tokens"], ref["tokens"]) and L.lmh_read_errors(ws) == 0
+    # left by a call of other sizes
+    small = L.sample(z[:2, :1000].contiguous(), u[:2], ws=ws, **kw2)
+    assert torch.equal(small["tokens"], check(z[:2, :1000].contiguous(), u[:2], **kw)["tokens"])
+
+
+def test_two_calls_at_once():
+    z, u = logits(30, 70001, seed=28)
+    ref = [L.sample(z, u, top_p=0.9), L.sample(z, u, top_k=3000)]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        o = [L.sample(z, u, top_p=0.9, stream=s[0]), L.sample(z, u, top_k=3000, stream=s[1])]
+        torch.cuda.synchronize()
+        for a, b in zip(o, ref):
+            assert torch.equal(a["tokens"], b["tokens"]) and torch.equal(a["logprob"], b["logprob"])
