@@ -538,7 +538,8 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  * scales [ceil(rows / B), ceil(d / 128)], one per block of B x 128 values (B = 1 for hidden
  * states, 128 for weights; the last block of a row or column may be partial). The value stood
  * for is q * scale. A block of values v has scale = max(amax |v|, 2^-100) / 448 and q = v /
- * scale rounded to nearest even, so its largest value becomes +-448. A block that holds a NaN
+ * scale (a quotient within 2^-21 of the exact one) rounded to nearest even, so its largest value
+ * becomes +-448. A block that holds a NaN
  * gets NaN scale and values; one that holds an infinity has an infinite scale, NaN at the
  * infinities and 0 elsewhere.
  *
@@ -566,7 +567,7 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *   LMH_ENTRY_RMS_NORM_BWD) with N and d in the shape (V any valid value).
  *
  * lmh_quantize_fp8 — x [rows, d] bf16 as an 8-bit matrix q, scale with blocks of block_rows x 128
- * (block_rows 1 or 128). No workspace.
+ * (block_rows 1 or 128). d up to 2^24, fewer than 2^31 rows and 2^31 scales. No workspace.
  *
  * lmh_fp8_logits — the logits of 8-bit hidden states and an 8-bit weight,
  *   z_nv = sum_b h_scale[n, b] w_scale[v / 128, b] sum_{k in block b} H8[n, k] W8[v, k],

@@ -136,7 +136,7 @@ extern "C" lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_ro
   // a warp a row where the rows fill the GPU, a block of threads a row where they do not
   const int per = rows < 8 * 148 ? 256 : 32;
   const int64_t grid = block_rows == 1 ? cdiv(rows, 256 / per) : cdiv(rows, kQBlock) * nb;
-  if (grid > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
+  if (cdiv(rows, block_rows) * nb > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
   int dev, sms;
   LMH_TRY(current_device(&dev, &sms));
   if (rows == 0) return LMH_OK;
