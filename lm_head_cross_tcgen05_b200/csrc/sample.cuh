@@ -12,9 +12,9 @@
 //    short prefix, everything that can be in it is collected and sorted (up to 2048 candidates):
 //    at least k logits lie at or above the k-th largest group maximum, so only groups whose
 //    maximum lies there are read again, 128 bytes for most of k candidates. A top-p prefix
-//    without top-k ends where the candidates' weight reaches a part of the whole sum; those of
-//    256 groups are tried, then, if they may suffice, those of 1024. A chain of short steps, each
-//    waiting for the one before: 256 rows take 21 us unfiltered, 29 with k = 50 and 62 with
+//    without top-k ends where the candidates' weight reaches a part of the whole sum; the weight of
+//    those maxima leads there (a lower bound), so one list is tried at most. A chain of short steps, each
+//    waiting for the one before: 256 rows take 13 us unfiltered, 20 with k = 50 and 46 with
 //    k = 1000, hardly more than one row does.
 //  * sample_row_kernel takes the rows left over (long prefixes), a cluster of 1 to 8 CTAs each,
 //    which hold the row in shared memory (where it fits; else they read it again). A prefix that
@@ -123,7 +123,7 @@ struct ListShared {
   };
   uint4 chist[kSampBuckets / 4];
   uint32_t list_n, queue_n;
-  int pick;
+  int pick, reach;
   u64 base;
 };
 struct alignas(16) RowShared {
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const S
 }
 
 template <class T>
-__global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampParams p) {
+__global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const SampParams p) {
   __shared__ ListShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long row = blockIdx.x;
@@ -596,14 +596,12 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
   for (int o = kSampWarps / 2; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
 
   const bool all_listed = p.V <= kSampList;
-  // top-p without top-k: few candidates first, then as many as there is room for
-  int want = f.k > 0 ? f.k : 256;
-  for (bool more = f.listed(p.V); more;) {
+  while (f.listed(p.V)) {  // once; break: the row is left
     // ---- candidates lie in the buckets up to b0
-    more = false;
     int b0 = kSampBuckets - 1;
     if (tid == 0) {
       sh.pick = kSampBuckets - 1;
+      sh.reach = kSampBuckets;
       sh.list_n = sh.queue_n = 0;
     }
     if (!all_listed && (f.k > 0 || f.use_p)) {
@@ -619,13 +617,43 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       const uint32_t hv[4] = {h.x, h.y, h.z, h.w};
       u64 pc, tc;
       block_scan(h.x + h.y + h.z + h.w, &pc, &tc, sh.red[0]);
+      if (f.k > 0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (pc < static_cast<u64>(want) && static_cast<u64>(want) <= pc + hv[j]) sh.pick = tid * 4 + j;
-        pc += hv[j];
+        for (int j = 0; j < 4; ++j) {
+          if (pc < static_cast<u64>(f.k) && static_cast<u64>(f.k) <= pc + hv[j]) sh.pick = tid * 4 + j;
+          pc += hv[j];
+        }
+      } else {
+        // Top-p alone. The maxima themselves weigh at least so much, in 2^-30 of the largest; where
+        // they reach the target, or a list of the largest size may, the list has a chance. With c
+        // of G groups reaching a bucket, logits in any order, G log(G / (G - c)) logits do. What
+        // is misjudged here costs time: the token is the same from either kernel.
+        u64 hw[4], pw, tw;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          double e, sc;
+          exp2_64(-64.0 * p.F / kSampBuckets * (tid * 4 + j + 1), 30, sh.table, &e, &sc);
+          hw[j] = hv[j] ? static_cast<u64>(hv[j] * (e * sc)) : 0;
+        }
+        block_scan(hw[0] + hw[1] + hw[2] + hw[3], &pw, &tw, sh.red[1]);
+        const float T = fmaxf(f.top_p * static_cast<float>(total) * 1073741824.f, 1.f), G = static_cast<float>(groups);
+        auto members = [&](u64 c) { return G * -log1pf(-fminf(static_cast<float>(c) / G, 0.9999f)); };
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const u64 c = pc + hv[j], w = pw + hw[j];
+          if (hv[j]) {
+            const float n = members(c);
+            if (static_cast<float>(pw) < T && T <= static_cast<float>(w) && n <= kSampList - 48) sh.reach = tid * 4 + j;
+            if (n > kSampList - 348 && (pc == 0 || members(pc) <= kSampList - 348))
+              sh.pick = n <= kSampList && static_cast<float>(w) * (n / c) >= 0.95f * T ? tid * 4 + j : -1;
+          }
+          pc = c;
+          pw = w;
+        }
       }
       __syncthreads();
-      b0 = sh.pick;
+      b0 = sh.reach < kSampBuckets ? sh.reach : sh.pick;
+      if (b0 < 0) break;
     }
     if (f.use_m && !f.use_p) {
       const double bm = -f.low64 / 64.0 * (kSampBuckets / static_cast<double>(p.F)) + 1.0;
@@ -664,26 +692,27 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
     // eight groups at a time, their candidates counted in one step (the counter is one address),
     // while the next eight are loaded
     float z[8];
-    uint32_t id[8];
     const uint32_t lane_at = (lane >> 2) * 32 + (lane & 3);
+    auto place = [&](int q) -> uint32_t {
+      const uint32_t g = sh.queue[q];
+      return g / kGroups * kBlock + g % kGroups * 4 + lane_at;
+    };
     auto load = [&](int q0) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int q = q0 + j * kSampWarps;
-        const uint32_t g = q < queued ? sh.queue[q] : 0;
-        id[j] = g / kGroups * kBlock + g % kGroups * 4 + lane_at;
-        z[j] = q < queued && id[j] < static_cast<uint32_t>(p.V) ? as_float(src[id[j]]) : -INFINITY;  // no candidate
+        const uint32_t id = q < queued ? place(q) : p.V;
+        z[j] = id < static_cast<uint32_t>(p.V) ? as_float(src[id]) : -INFINITY;  // no candidate
       }
     };
     if (warp < queued) load(warp);
 #pragma unroll 1
     for (int q0 = warp; q0 < queued; q0 += 8 * kSampWarps) {
       float y[8];
-      uint32_t mask[8], to[8], count = 0;
+      uint32_t mask[8], count = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         y[j] = z[j];
-        to[j] = id[j];
         mask[j] = __ballot_sync(0xffffffffu, up_to(y[j]));
         count += __popc(mask[j]);
       }
@@ -695,7 +724,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       for (int j = 0; j < 8; ++j) {
         if ((mask[j] >> lane) & 1) {
           const uint32_t slot = at + __popc(mask[j] & ((1u << lane) - 1));
-          if (slot < kSampList) sh.list[slot] = (static_cast<u64>(sort_key(y[j])) << 32) | ~to[j];
+          if (slot < kSampList) sh.list[slot] = (static_cast<u64>(sort_key(y[j])) << 32) | ~place(q0 + j * kSampWarps);
         }
         at += __popc(mask[j]);
       }
@@ -747,19 +776,7 @@ __global__ void __launch_bounds__(kSampThreads) sample_list_kernel(const SampPar
       if (at >= 0) {
         keep = min(keep, at + 1);
       } else if (!all_listed) {  // else all are listed, and the target past them by a rounding
-        // The weights' fall from half of the list to its end, w(i) ~ i^-s, continued: it falls faster, so
-        // that a list with no room for what is missing by this count has none (a choice of the
-        // kernel, not of the token).
-        if (f.k == 0 && want < kSampListK) {
-          const float w = static_cast<float>(max(sh.wlist[n - 1], 1ull));
-          const float s = log2f(static_cast<float>(sh.wlist[n / 2]) / w), l = log2f(static_cast<float>(kSampList) / n);
-          const float t = (1.f - s) * l * 0.6931471805599453f;  // integral of (i / n)^-s over i / n up to 2048 / n
-          const float part = fabsf(t) > 1e-3f ? (expf(t) - 1.f) / (1.f - s) : l * 0.6931471805599453f;
-          more = static_cast<float>(target - weight) < w * n * part;
-        }
-        want = kSampListK;
-        __syncthreads();  // the list is read before it is written again
-        continue;
+        break;
       }
     }
 
