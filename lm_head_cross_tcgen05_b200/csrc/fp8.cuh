@@ -310,10 +310,14 @@ struct FpMany {
   static constexpr int NBUF = 2, TMEM = 512;
   static constexpr int A_BYTES = kFpM * kFpK, B_BYTES = TV * kFpK, STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 3;
-  static constexpr int SLOTS = 8;         // blocks whose scales are in shared memory
+  // Barriers for "the MMAs of this block are done". A block that comes DONE later cannot be done
+  // before either waiter has seen this one: it is loaded, and its columns are freed, after that.
+  static constexpr int DONE = 8;
+  static_assert(DONE >= STAGES + NBUF, "a waiter is at most so many blocks behind");
+  static constexpr int GROUPS = 4;        // of four blocks, whose scales are in shared memory
   static constexpr int BOX = 2048;        // per epilogue warp: 32 tokens x 64 bytes (512-byte aligned)
-  static constexpr int SC = 132;          // floats per slot: 128 tokens', 2 vocabulary blocks'
-  static constexpr int SMEM = STAGES * STAGE + EPI * BOX + SLOTS * SC * 4 + 1024;
+  static constexpr int SC = 520;          // floats per group: 128 tokens' and 2 vocabulary blocks', by fours
+  static constexpr int SMEM = STAGES * STAGE + EPI * BOX + GROUPS * SC * 4 + 1024;
   // registers a thread: 640 x 96 at the launch, then 128 x 32 + 512 x 112, which is the same sum
   static constexpr int REG_LOAD = 32, REG_EPI = 112;
 };
@@ -321,11 +325,15 @@ struct FpMany {
 // An accumulator is held from its MMAs (512 cycles) until its last column is read, and two of them
 // are all that TMEM holds; so what bounds this kernel is the way round: commit, wake, read, arrive,
 // wake, MMAs. 16 warps read at once, 64 columns each with the sums in registers, which the loading
-// warps give up theirs for; the additions take two values an instruction; and a spare warp brings
-// the scales to shared memory, since a load of their own would make the reading warps wait.
-// (4096 x 32000 x 2048 to bf16: 349 us with eight warps of 128 columns, 306 with 16, and see below
-// for the scales. A copy without any TMEM reads took 302 us where this took 326, and pairs of CTAs
-// that share a 256 x 256 tile, whose ways round are longer, took 660.)
+// warps give up theirs for; the additions take two values an instruction; one commit a block both
+// frees its stage and hands over its columns; and a spare warp brings the scales to shared memory
+// four blocks at a time, up to 16 ahead, since loads of their own would make the reading warps wait.
+// 4096 x 32000 x 2048 to bf16: 349 us with eight warps of 128 columns, 311 with 16, 301 with the
+// scales by fours (1780 TFLOP/s, 54 percent of twice the measured bf16 rate). In copies for timing,
+// without the operands' loads it took 300 where this took 312, without the scales 285, without
+// TMEM reads 273, without output 287, and with none of these, one MMA a block and no additions 173:
+// the bare way round. Accumulators of 128 columns, whose way round would be shorter, took 367, and
+// pairs of CTAs that share a 256 x 256 tile 660.
 // TMA: the output goes out by TMA from staged boxes of 32 tokens x 64 bytes, where its rows are
 // 16-byte aligned; otherwise by transposes of 32 x 16 through shared memory.
 template <class Out, bool TMA>
@@ -334,11 +342,10 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
                     const __grid_constant__ CUtensorMap tmH,
                     const __grid_constant__ CUtensorMap tmOut, const FpParams p) {
   using C = FpMany;
-  constexpr int STAGES = C::STAGES, NBUF = C::NBUF, TV = C::TV;
+  constexpr int STAGES = C::STAGES, NBUF = C::NBUF, TV = C::TV, DONE = C::DONE;
   extern __shared__ uint8_t dsmem[];
-  __shared__ __align__(8) uint64_t full_bar[STAGES], empty_bar[STAGES], tfull_bar[NBUF],
-      tempty_bar[NBUF], drain_bar;
-  __shared__ __align__(8) uint64_t scale_bar[C::SLOTS];
+  __shared__ __align__(8) uint64_t full_bar[STAGES], done_bar[DONE], tempty_bar[NBUF], drain_bar;
+  __shared__ __align__(8) uint64_t sfull_bar[C::GROUPS], sfree_bar[C::GROUPS];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
 
@@ -348,15 +355,13 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = 0;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&full_bar[s]), 1 + 32);  // the loads' transaction, and the scales' 32 lanes
-      mbar_init(smem_u32(&empty_bar[s]), 1);
+    for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&full_bar[s]), 1);
+    for (int i = 0; i < DONE; ++i) mbar_init(smem_u32(&done_bar[i]), 1);
+    for (int b = 0; b < NBUF; ++b) mbar_init(smem_u32(&tempty_bar[b]), C::EPI);
+    for (int i = 0; i < C::GROUPS; ++i) {
+      mbar_init(smem_u32(&sfull_bar[i]), 32);
+      mbar_init(smem_u32(&sfree_bar[i]), C::EPI);
     }
-    for (int b = 0; b < NBUF; ++b) {
-      mbar_init(smem_u32(&tfull_bar[b]), 1);
-      mbar_init(smem_u32(&tempty_bar[b]), C::EPI);
-    }
-    for (int s = 0; s < C::SLOTS; ++s) mbar_init(smem_u32(&scale_bar[s]), 32);
     mbar_init(smem_u32(&drain_bar), 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
         const int v0 = (t / p.ntiles) * TV, n0 = (t % p.ntiles) * kFpM;
         for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
           const uint32_t s = kbg % STAGES;
-          if (!mbar_wait(smem_u32(&empty_bar[s]), ((kbg / STAGES) & 1u) ^ 1u, p.err)) {
+          if (kbg >= STAGES && !mbar_wait(smem_u32(&done_bar[(kbg - STAGES) % DONE]), ((kbg - STAGES) / DONE) & 1u, p.err)) {
             abort_flag = 1;
             break;
           }
@@ -405,47 +410,44 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
           for (int k = 0; k < kFpK / 32; ++k)
             mma_e4m3(tmem_base + b * TV, make_sw128_desc(h + k * 32, 16, 1024),
                      make_sw128_desc(w + k * 32, 16, 1024), idesc, k != 0);
-          mma_commit(smem_u32(&empty_bar[s]));
-          mma_commit(smem_u32(&tfull_bar[b]));
+          mma_commit(smem_u32(&done_bar[kbg % DONE]));
         }
       }
       mma_commit(smem_u32(&drain_bar));
       mbar_wait(smem_u32(&drain_bar), 0, p.err);
     } else if (warp == 2) {
-      // Scales of block kbg into slot kbg % SLOTS. That is free: stage kbg % STAGES being free, the
-      // MMAs of block kbg - STAGES are done, so they were begun, so the block NBUF before that was
-      // read, scales and all, and the slot's last block is older.
-      static_assert(C::SLOTS >= STAGES + NBUF + 1, "a slot's last block has been read");
-      uint32_t kbg = 0;
-      for (int t = blockIdx.x; t < tiles && !abort_flag; t += gridDim.x) {
-        const int vb = (t / p.ntiles) * (TV / kFpK), n0 = (t % p.ntiles) * kFpM;
-        const bool wv = lane < TV / kFpK && static_cast<long long>(vb + lane) * kFpK < p.V;
-        const float* ws = p.ws + (wv ? vb + lane : 0ll) * p.nb;
-        for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
-          const uint32_t s = kbg % STAGES, slot = kbg % C::SLOTS;
-          if (!mbar_wait(smem_u32(&empty_bar[s]), ((kbg / STAGES) & 1u) ^ 1u, p.err)) {
-            abort_flag = 1;
-            break;
-          }
+      // the scales of four blocks at a time, up to GROUPS * 4 blocks ahead of the epilogue
+      const bool wide = (p.nb & 3) == 0 && (reinterpret_cast<uintptr_t>(p.hs) & 15) == 0;
+      uint32_t gi = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+        const int v = (t / p.ntiles) * (TV / kFpK) + (lane >> 2), n0 = (t % p.ntiles) * kFpM;
+        const float* ws = p.ws + static_cast<long long>(v) * p.nb + (lane & 3);
+        const bool wv = lane < 4 * (TV / kFpK) && static_cast<long long>(v) * kFpK < p.V;
+        for (int kb = 0; kb < p.nb && ok; kb += 4, ++gi) {
+          const uint32_t slot = gi % C::GROUPS;
+          ok = !abort_flag && mbar_wait(smem_u32(&sfree_bar[slot]), ((gi / C::GROUPS) & 1u) ^ 1u, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
           const uint32_t dst = smem_base + STAGES * C::STAGE + C::EPI * C::BOX + slot * C::SC * 4;
 #pragma unroll
           for (int j = 0; j < kFpM / 32; ++j) {
             const int n = n0 + lane + 32 * j;
-            const int bytes = n < p.N ? 4 : 0;  // 0 past the last token
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + (lane + 32 * j) * 4),
-                         "l"(p.hs + (n < p.N ? static_cast<long long>(n) * p.nb + kb : 0ll)), "r"(bytes)
-                         : "memory");
+            const float* hs = p.hs + (n < p.N ? static_cast<long long>(n) * p.nb + kb : 0ll);
+            const uint32_t to = dst + (lane + 32 * j) * 16;
+            if (wide) {
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(hs), "r"(n < p.N ? 16 : 0) : "memory");
+            } else {
+              for (int i = 0; i < 4 && kb + i < p.nb; ++i)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * i), "l"(n < p.N ? hs + i : hs), "r"(n < p.N ? 4 : 0) : "memory");
+            }
           }
-          if (lane < TV / kFpK)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + (kFpM + lane) * 4),
-                         "l"(ws + kb), "r"(wv ? 4 : 0)
-                         : "memory");
-          // for the epilogue; and for the MMAs, which would otherwise run ahead of this warp, so
-          // that it would wait for a phase of empty_bar that lies two behind
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&scale_bar[slot])) : "memory");
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full_bar[s])) : "memory");
+          if (wv && kb + (lane & 3) < p.nb)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + (kFpM * 4 + lane) * 4), "l"(ws + kb) : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sfull_bar[slot])) : "memory");
         }
       }
+      if (!ok) abort_flag = 1;
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
     const uint32_t box = smem_base + STAGES * C::STAGE + (warp - 4) * C::BOX;
     const float* sc = reinterpret_cast<const float*>(dsmem + (smem_base - smem_u32(dsmem)) + STAGES * C::STAGE + C::EPI * C::BOX);
     Out* out = static_cast<Out*>(p.out);
-    uint32_t kbg = 0;
+    uint32_t kbg = 0, gi = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const long long v0 = static_cast<long long>(t / p.ntiles) * TV + c0;
       const long long r0 = static_cast<long long>(t % p.ntiles) * kFpM + q * 32;  // warp's tokens
@@ -463,30 +465,42 @@ __global__ void __launch_bounds__(FpMany::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < COLS / 2; ++i) acc[i] = 0;
       bool ok = true;
-      for (int kb = 0; kb < p.nb; ++kb, ++kbg) {
-        const uint32_t b = kbg % NBUF, slot = kbg % C::SLOTS;
-        ok = !abort_flag && mbar_wait(smem_u32(&scale_bar[slot]), (kbg / C::SLOTS) & 1u, p.err) &&
-             mbar_wait(smem_u32(&tfull_bar[b]), (kbg / NBUF) & 1u, p.err);
+      for (int kb = 0; kb < p.nb; kb += 4, ++gi) {
+        const uint32_t slot = gi % C::GROUPS;
+        ok = !abort_flag && mbar_wait(smem_u32(&sfull_bar[slot]), (gi / C::GROUPS) & 1u, p.err);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        tc_fence_after();
-        const float s = sc[slot * C::SC + q * 32 + lane] * sc[slot * C::SC + kFpM + c0 / kFpK];
-        uint64_t f;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(s)));
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TV + c0;
+        const float4 h4 = *reinterpret_cast<const float4*>(sc + slot * C::SC + (q * 32 + lane) * 4);
+        const float4 w4 = *reinterpret_cast<const float4*>(sc + slot * C::SC + (kFpM + c0 / kFpK) * 4);
+        const float s[4] = {h4.x * w4.x, h4.y * w4.y, h4.z * w4.z, h4.w * w4.w};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sfree_bar[slot]));
 #pragma unroll
-        for (int g = 0; g < COLS / 32; ++g) {
-          uint32_t v[32];
-          tmem_ld32_start(taddr + 32 * g, v);
-          tmem_landed(v);
-          if (g == COLS / 32 - 1) {  // all columns are read: the block after next may go here
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
+        for (int i4 = 0; i4 < 4; ++i4, ++kbg) {
+          if (kb + i4 >= p.nb) break;
+          const uint32_t b = kbg % NBUF;
+          ok = mbar_wait(smem_u32(&done_bar[kbg % DONE]), (kbg / DONE) & 1u, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          uint64_t f;
+          asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "r"(__float_as_uint(s[i4])));
+          const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * TV + c0;
+#pragma unroll
+          for (int g = 0; g < COLS / 32; ++g) {
+            uint32_t v[32];
+            tmem_ld32_start(taddr + 32 * g, v);
+            tmem_landed(v);
+            if (g == COLS / 32 - 1) {  // all columns are read: the block after next may go here
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&tempty_bar[b]));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) fma2(acc[g * 16 + i], v[2 * i], v[2 * i + 1], f);
           }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) fma2(acc[g * 16 + i], v[2 * i], v[2 * i + 1], f);
         }
+        if (!ok) break;
       }
       if (!ok) {
         abort_flag = 1;
