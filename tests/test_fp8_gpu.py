@@ -164,3 +164,27 @@ def test_stale_error_word_is_cleared():
     ws = torch.full((L.lmh_workspace_size(shape, L.ENTRY_FP8_LOGITS),), 255, dtype=torch.uint8, device="cuda")
     L.fp8_logits(*ops, ws=ws)
     assert L.lmh_read_errors(ws) == 0
+
+
+@pytest.mark.parametrize("N", [5, 130])
+@pytest.mark.parametrize("d", [512, 576])
+def test_scales_at_any_address(N, d):
+    """Scales aligned to 4 bytes only, H8 and W8 to 16; the logits the same as from aligned ones."""
+    ops = operands(N, 300, d, seed=9)
+    moved = []
+    for t, by in zip(ops, (16, 1, 16, 1)):
+        flat = torch.zeros(t.numel() + by, dtype=t.dtype, device="cuda")
+        flat[by:].copy_(t.flatten())
+        moved.append(flat[by:].view(t.shape))
+    assert torch.equal(L.fp8_logits(*moved)["logits"], L.fp8_logits(*ops)["logits"])
+
+
+def test_two_calls_at_once():
+    a, b = operands(40, 5000, 640, seed=10), operands(200, 5000, 640, seed=11)
+    ref = [L.fp8_logits(*x)["logits"] for x in (a, b)]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        z = [L.fp8_logits(*x, stream=t)["logits"] for x, t in zip((a, b), s)]
+        torch.cuda.synchronize()
+        assert torch.equal(z[0], ref[0]) and torch.equal(z[1], ref[1])

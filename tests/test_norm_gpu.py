@@ -245,3 +245,62 @@ def test_another_stream_and_graph():
     ref = L.rms_norm(x, w, r)
     rb = L.rms_norm_bwd(ref["sum"], w, ref["rstd"], dy)
     assert torch.equal(o["y"], ref["y"]) and torch.equal(b["dx"], rb["dx"]) and torch.equal(b["dweight"], rb["dweight"])
+
+
+def test_two_backward_passes_at_once():
+    """Each with its own workspace; and in a workspace of any content."""
+    N, d = 700, 1344
+    g = torch.Generator(device="cuda").manual_seed(31)
+    x, dy = (torch.randn(2, N, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    w = torch.rand(d, device="cuda", generator=g).bfloat16()
+    f = [L.rms_norm(x[i], w) for i in range(2)]
+    ref = [L.rms_norm_bwd(f[i]["sum"], w, f[i]["rstd"], dy[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [L.rms_norm_bwd(f[i]["sum"], w, f[i]["rstd"], dy[i], stream=s[i]) for i in range(2)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, ref):
+            assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dweight"], b["dweight"])
+    ws = torch.full((L.lmh_workspace_size(L.make_shape(N, d, 1), L.ENTRY_RMS_NORM_BWD),), 255, dtype=torch.uint8, device="cuda")
+    got = L.rms_norm_bwd(f[0]["sum"], w, f[0]["rstd"], dy[0], ws=ws)
+    assert torch.equal(got["dx"], ref[0]["dx"]) and torch.equal(got["dweight"], ref[0]["dweight"])
+
+
+def test_gradients_against_differences():
+    """The formula's gradient, which the kernels are tested against, against central differences of
+    the oracle's forward pass in fp64 (steps of 1e-5: both errors, of the step and of rounding,
+    are below 1e-8 of values of order one)."""
+    rng = np.random.default_rng(3)
+    N, d, eps = 3, 64, 1e-6
+    r, w, dy = rng.standard_normal((N, d)), rng.standard_normal(d), rng.standard_normal((N, d))
+
+    def loss(r, w):
+        return float((w * r / np.sqrt((r * r).mean(1, keepdims=True) + eps) * dy).sum())
+    rstd = 1 / np.sqrt((r * r).mean(1, keepdims=True) + eps)
+    n = r * rstd
+    dx = rstd * (w * dy - n * (w * dy * n).mean(1, keepdims=True))
+    dw = (dy * n).sum(0)
+    h = 1e-5
+    for j in (0, 17, 63):
+        e = np.zeros(d)
+        e[j] = h
+        assert abs((loss(r, w + e) - loss(r, w - e)) / (2 * h) - dw[j]) < 1e-7
+        for i in range(N):
+            m = np.zeros((N, d))
+            m[i, j] = h
+            assert abs((loss(r + m, w) - loss(r - m, w)) / (2 * h) - dx[i, j]) < 1e-7
+    # and the kernels' own, from bf16 inputs
+    b = lambda a: torch.tensor(a, device="cuda").bfloat16()
+    R, Wt, DY = b(r), b(w), b(dy)
+    f = L.rms_norm(R, Wt, eps=eps)
+    got = L.rms_norm_bwd(f["sum"], Wt, f["rstd"], DY)
+    r, w, dy = (t.double().cpu().numpy() for t in (R, Wt, DY))
+    num = np.zeros(d)
+    for j in range(d):
+        e = np.zeros(d)
+        e[j] = h
+        num[j] = (loss(r, w + e) - loss(r, w - e)) / (2 * h)
+    err = np.abs(got["dweight"].double().cpu().numpy() - num)
+    # one rounding to bf16 (2^-8), fp32 sums of three products, the differences' own 1e-7
+    assert np.all(err <= 2.0 ** -8 * np.abs(num) + 1e-5 * np.abs(dy * r).sum(0) + 1e-7)
