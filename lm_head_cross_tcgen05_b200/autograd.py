@@ -16,7 +16,13 @@ library, in one of two ways:
   keeps dH and dW, and the backward scales them by g on the device (``lmh_scale_bf16``; g = 1
   changes no bit). They hold dH and dW from the forward to the backward, like activations.
 
-No call synchronises the host, and all arithmetic runs in the library's kernels.
+``rms_norm`` is the final norm in front of them: its backward runs ``lmh_rms_norm_bwd`` from the
+stored sum and rstd.
+
+No call synchronises the host, and all arithmetic runs in the library's kernels. A backward pass
+may be captured into a CUDA graph while no eager autograd graph of the same leaves is alive:
+torch's gradient accumulators belong to the stream that made them first, and joining that one to
+a capture ends the process.
 """
 from __future__ import annotations
 

