@@ -55,6 +55,11 @@ def _arg(t, shape, dtype, what: str, dev: int):
     return t.data_ptr()
 
 
+def _own(t):
+    """The address of a tensor that a helper has just made, which needs no checks."""
+    return None if t is None else t.data_ptr()
+
+
 def _matrix(t, what: str):
     if t.dim() != 2:
         raise ValueError(f"{what} must be a matrix, got {t.dim()} dimensions")
@@ -189,13 +194,17 @@ def _row_arg(t, N: int, dtype, what: str):
     return at
 
 
+def _same_device(t, dev: int) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"a row parameter is on {t.device}, the logits on device {dev}")
+
+
 def lmh_sample(shape, opt, logits, u, tokens, logprob=None, *, workspace, stream=None,
                row_tensors=()) -> None:
     """row_tensors: the tensors that shape and opt point to, checked to be on the same device."""
     N, V, dev, dt = shape.N, shape.V, logits.get_device(), logits.dtype
     for t in row_tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"a row parameter is on {t.device}, the logits on device {dev}")
+        _same_device(t, dev)
     _call("lmh_sample", dev, stream, ctypes.byref(shape), ctypes.byref(opt),
           _arg(logits, (N, V), dt, "logits", dev), _logits_dtype(dt), _arg(u, (N,), _f32, "u", dev),
           _arg(tokens, (N,), _i32, "tokens", dev), _arg(logprob, (N,), _f32, "logprob", dev),
@@ -215,11 +224,14 @@ def rms_norm(x, weight, residual=None, *, eps: float = 1e-6, fp8: bool = False,
             out["q"] = torch.empty(N, d, dtype=_e4m3, device=dev)
             out["scale"] = torch.empty(N, _blocks(d), dtype=_f32, device=dev)
         else:
-            out["y"] = torch.empty(N, d, dtype=_bf, device=dev)
+            out["y"] = torch.empty_like(x)
             out["rstd"] = torch.empty(N, dtype=_f32, device=dev)
         new = keep_sum and residual is not None
-        out["sum"] = torch.empty(N, d, dtype=_bf, device=dev) if new else None
-    lmh_rms_norm(x, weight, residual, eps=eps, stream=stream, **out)
+        out["sum"] = torch.empty_like(x) if new else None
+    at, full, get = x.get_device(), (N, d), out.get
+    _call("lmh_rms_norm", at, stream, N, d, _arg(x, full, _bf, "x", at),
+          _arg(residual, full, _bf, "residual", at), _arg(weight, (d,), _bf, "weight", at), eps,
+          _own(out["sum"]), _own(get("y")), _own(get("q")), _own(get("scale")), _own(get("rstd")))
     if keep_sum and residual is None:
         out["sum"] = x
     return out
@@ -232,12 +244,15 @@ def rms_norm_bwd(sum, weight, rstd, dy, dsum=None, *, want_dx: bool = True,
     N, d = _matrix(sum, "sum")
     dev = sum.device
     with _allocating(stream, dev):
-        out = dict(dx=torch.empty(N, d, dtype=_bf, device=dev) if want_dx else None,
+        out = dict(dx=torch.empty_like(sum) if want_dx else None,
                    dweight=torch.empty(d, dtype=_bf, device=dev) if want_dweight else None)
         if ws is None:
             ws = torch.empty(_ws_bytes(ENTRY_RMS_NORM_BWD, N, d, 1), dtype=_u8, device=dev)
-    lmh_rms_norm_bwd(sum, weight, rstd, dy, dsum, out["dx"], out["dweight"], workspace=ws,
-                     stream=stream)
+    at, full = sum.get_device(), (N, d)
+    _call("lmh_rms_norm_bwd", at, stream, N, d, _arg(sum, full, _bf, "sum", at),
+          _arg(weight, (d,), _bf, "weight", at), _arg(rstd, (N,), _f32, "rstd", at),
+          _arg(dy, full, _bf, "dy", at), _arg(dsum, full, _bf, "dsum", at), _own(out["dx"]),
+          _own(out["dweight"]), *_space(ws, at))
     return out
 
 
@@ -259,13 +274,17 @@ def fp8_logits(H8, h_scale, W8, w_scale, *, dtype=torch.float32, ws=None, stream
     128 columns) and an 8-bit head weight [V, d] (scales per 128 x 128 block)."""
     N, d = _matrix(H8, "H8")
     V = _matrix(W8, "W8")[0]
-    _logits_dtype(dtype)
+    dt, nb = _logits_dtype(dtype), _blocks(d)
     shape, dev = lmh_shape(N, d, V, 0, 0, 0, 0.0, None), H8.device
     with _allocating(stream, dev):
         out = dict(logits=torch.empty(N, V, dtype=dtype, device=dev))
         if ws is None:
             ws = torch.empty(_ws_bytes(ENTRY_FP8_LOGITS, N, d, V), dtype=_u8, device=dev)
-    lmh_fp8_logits(shape, H8, h_scale, W8, w_scale, out["logits"], workspace=ws, stream=stream)
+    at = H8.get_device()
+    _call("lmh_fp8_logits", at, stream, ctypes.byref(shape), _arg(H8, (N, d), _e4m3, "H8", at),
+          _arg(h_scale, (N, nb), _f32, "h_scale", at), _arg(W8, (V, d), _e4m3, "W8", at),
+          _arg(w_scale, (_blocks(V), nb), _f32, "w_scale", at), _own(out["logits"]), dt,
+          *_space(ws, at))
     out["workspace"] = ws
     return out
 
@@ -278,7 +297,7 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, w
     token's log-probability at that temperature before the filters; -1 and 0 for a row with no
     logit above -inf or with a NaN or +inf."""
     N, V = _matrix(logits, "logits")
-    _logits_dtype(logits.dtype)
+    dt = _logits_dtype(logits.dtype)
     shape, dev = make_shape(N, 64, V, temperature=temperature), logits.device
     opt = make_sampling(N, top_k, top_p, min_p)
     with _allocating(stream, dev):
@@ -286,9 +305,13 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, w
                    logprob=torch.empty(N, dtype=_f32, device=dev))
         if ws is None:
             ws = torch.empty(_ws_bytes(ENTRY_SAMPLE, N, 64, V), dtype=_u8, device=dev)
-    rows = [t for t in (temperature, top_k, top_p, min_p) if isinstance(t, torch.Tensor)]
-    lmh_sample(shape, opt, logits, u, out["tokens"], out["logprob"], workspace=ws, stream=stream,
-               row_tensors=rows)
+    at = logits.get_device()
+    for t in (temperature, top_k, top_p, min_p):
+        if isinstance(t, torch.Tensor):
+            _same_device(t, at)
+    _call("lmh_sample", at, stream, ctypes.byref(shape), ctypes.byref(opt),
+          _arg(logits, (N, V), logits.dtype, "logits", at), dt, _arg(u, (N,), _f32, "u", at),
+          _own(out["tokens"]), _own(out["logprob"]), *_space(ws, at))
     out["workspace"] = ws
     return out
 
