@@ -636,16 +636,16 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
           hw[j] = hv[j] ? static_cast<u64>(hv[j] * (e * sc)) : 0;
         }
         block_scan(hw[0] + hw[1] + hw[2] + hw[3], &pw, &tw, sh.red[1]);
-        const float T = fmaxf(f.top_p * static_cast<float>(total) * 1073741824.f, 1.f), G = static_cast<float>(groups);
+        const float goal = fmaxf(f.top_p * static_cast<float>(total) * 1073741824.f, 1.f), G = static_cast<float>(groups);
         auto members = [&](u64 c) { return G * -log1pf(-fminf(static_cast<float>(c) / G, 0.9999f)); };
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const u64 c = pc + hv[j], w = pw + hw[j];
           if (hv[j]) {
             const float n = members(c);
-            if (static_cast<float>(pw) < T && T <= static_cast<float>(w) && n <= kSampList - 48) sh.reach = tid * 4 + j;
+            if (static_cast<float>(pw) < goal && goal <= static_cast<float>(w) && n <= kSampList - 48) sh.reach = tid * 4 + j;
             if (n > kSampList - 348 && (pc == 0 || members(pc) <= kSampList - 348))
-              sh.pick = n <= kSampList && static_cast<float>(w) * (n / c) >= 0.95f * T ? tid * 4 + j : -1;
+              sh.pick = n <= kSampList && static_cast<float>(w) * (n / c) >= 0.95f * goal ? tid * 4 + j : -1;
           }
           pc = c;
           pw = w;
