@@ -33,11 +33,11 @@ constexpr int kFewBlocks = 64;
 template <int TN>
 struct FpFew {
   static constexpr int THREADS = 192;
-  static constexpr int NBUF = 4;  // TMEM accumulators
+  static constexpr int NBUF = 8;  // TMEM accumulators (128256 x 4096, 64 tokens: 103 us with 4, 98 with 8)
   static constexpr int TMEM = TN * NBUF;
   // A stage is KB blocks: the MMA thread's wait and commit per stage hold up the next loads.
   // 128256 x 4096, 1 / 64 tokens: one block a stage 100.6 / 116 us, two 87.3 / 104.5, four (two
-  // stages) 87.1 / 102.5.
+  // stages) 87.1 / 102.5 (with four accumulators).
   static constexpr int KB = 2, A_BYTES = kFpM * kFpK, B_BYTES = TN * kFpK, STAGE = KB * (A_BYTES + B_BYTES);
   static constexpr int STAGES = TN == 64 ? 4 : 5;
   static constexpr int HS = kFewBlocks * TN * 4;  // the tokens' scales
@@ -104,8 +104,7 @@ __device__ __forceinline__ void add_scaled(uint64_t& acc, float a, float b, uint
 }
 
 // Bound by the stream of W8: 128256 x 4096 takes 87 us for one token (6.0 TB/s of the 6.5 that a
-// copy reaches) and 105 for 64 (with 33 MB of logits, 5.3 TB/s; the accumulators' way round as in
-// the kernel for many tokens, of a third of the length). 32000 x 2048 takes 18.5 us: the launch,
+// copy reaches) and 98 for 64 (with 33 MB of logits, 5.7 TB/s). 32000 x 2048 takes 18.5 us: the launch,
 // the first loads' way and two tiles for most SMs where 1.7 would do. The token scales are read
 // from shared memory, since they are the same for every tile; a tile's 128 x nb vocabulary scales
 // are one per block, broadcast by a shuffle.
