@@ -304,3 +304,32 @@ def test_gradients_against_differences():
     err = np.abs(got["dweight"].double().cpu().numpy() - num)
     # one rounding to bf16 (2^-8), fp32 sums of three products, the differences' own 1e-7
     assert np.all(err <= 2.0 ** -8 * np.abs(num) + 1e-5 * np.abs(dy * r).sum(0) + 1e-7)
+
+
+def test_one_tensor_as_x_and_residual():
+    """The same tensor twice; and two leaves' gradients are not one tensor."""
+    N, d = 33, 320
+    x, w, g = rand(N, d, seed=32), rand(d, seed=33), rand(N, d, seed=34)
+    f = L.rms_norm(x, w, x)
+    b = L.rms_norm_bwd(f["sum"], w, f["rstd"], g)
+    assert torch.equal(f["sum"], x + x)
+    lx = x.clone().requires_grad_()
+    A.rms_norm(lx, w, lx)[0].backward(g)
+    assert torch.equal(lx.grad, b["dx"] + b["dx"])
+    l1, l2 = x.clone().requires_grad_(), x.clone().requires_grad_()
+    A.rms_norm(l1, w, l2)[0].backward(g)
+    l1.grad.mul_(2)
+    assert torch.equal(l2.grad, b["dx"]) and torch.equal(l1.grad, 2 * b["dx"])
+
+
+def test_inputs_that_are_views():
+    """Rows inside a larger buffer: contiguous, aligned to 16 bytes and no more."""
+    N, d = 37, 192
+    flat = [rand(1, N * d + 8, seed=35 + i).flatten() for i in range(3)]
+    x, r, dy = (t[8:].view(N, d) for t in flat)
+    w = rand(1, d + 8, seed=40).flatten()[8:]
+    f, ref = L.rms_norm(x, w, r), L.rms_norm(x.clone(), w.clone(), r.clone())
+    b, rb = (L.rms_norm_bwd(o["sum"], w, o["rstd"], dy) for o in (f, ref))
+    q, rq = L.rms_norm(x, w, r, fp8=True), L.rms_norm(x.clone(), w.clone(), r.clone(), fp8=True)
+    assert torch.equal(f["y"], ref["y"]) and torch.equal(b["dx"], rb["dx"]) and torch.equal(b["dweight"], rb["dweight"])
+    assert torch.equal(q["q"].view(torch.uint8), rq["q"].view(torch.uint8)) and torch.equal(q["scale"], rq["scale"])

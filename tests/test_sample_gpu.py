@@ -330,3 +330,19 @@ def test_two_calls_at_once():
         torch.cuda.synchronize()
         for a, b in zip(o, ref):
             assert torch.equal(a["tokens"], b["tokens"]) and torch.equal(a["logprob"], b["logprob"])
+
+
+@pytest.mark.parametrize("dtype", [f32, torch.bfloat16])
+@pytest.mark.parametrize("by", [1, 3, 5])
+def test_logits_at_any_address(dtype, by):
+    """Aligned to their element only; u, tokens and parameters to theirs."""
+    z, u = logits(4, 40000, seed=29, dtype=dtype)
+    flat = torch.full((z.numel() + by + 7,), 50.0, device="cuda", dtype=dtype)  # what lies beside is never read as a logit
+    flat[by:by + z.numel()].copy_(z.flatten())
+    moved = flat[by:by + z.numel()].view(z.shape)
+    uu = torch.zeros(5, device="cuda")
+    uu[1:].copy_(u)
+    for kw in (dict(), dict(k=40), dict(p=0.9), dict(k=4000, p=0.8)):
+        ref = check(z, u, **kw)
+        o = check(moved, uu[1:], **kw)
+        assert torch.equal(o["tokens"], ref["tokens"]) and torch.equal(o["logprob"], ref["logprob"])
