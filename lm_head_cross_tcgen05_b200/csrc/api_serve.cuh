@@ -133,7 +133,8 @@ extern "C" lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_ro
   if (rows > 0 && (!x || !q || !scale)) return LMH_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return LMH_ERR_ALIGNMENT;
   const int64_t nb = cdiv(d, kQBlock);
-  // a warp a row where the rows fill the GPU, a block of threads a row where they do not
+  // A warp a row where the rows fill the GPU, a block of threads a row where they do not: d = 4096,
+  // 600 rows 10.9 us by warps, 8.9 by blocks; 4096 rows 16.8 and 19.6.
   const int per = rows < 8 * 148 ? 256 : 32;
   const int64_t grid = block_rows == 1 ? cdiv(rows, 256 / per) : cdiv(rows, kQBlock) * nb;
   if (cdiv(rows, block_rows) * nb > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
@@ -216,6 +217,9 @@ lmh_status launch_many(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t
   return last_launch();
 }
 
+// The kernel with few columns of tokens as far as it goes: 128256 x 4096 from cold caches, 1 / 32 / 64
+// tokens 108 / 108 / 113 us, by the other kernel 120 / 115 / 118. The narrowest that holds the
+// tokens: with 64 columns 1 / 16 / 32 tokens took 113 / 107 / 110 us, with their own 108 / 106 / 108.
 template <class Out>
 lmh_status launch_fp8(const FpParams& p, const uint8_t* H8, const uint8_t* W8, int64_t d, int dev,
                       int sms, cudaStream_t st) {
@@ -265,7 +269,8 @@ extern "C" lmh_status lmh_fp8_logits(const lmh_shape* shape, const uint8_t* H8,
 namespace {
 
 // CTAs per row of the row kernel: 1, 2, 4 or 8, at least 4096 logits each. No result depends on
-// it. How many rows are left to that kernel only the device knows; it is made for few.
+// it. How many rows are left to that kernel only the device knows; it is made for few: thirty rows of
+// 151936 took 218 / 71 / 66 us with 1 / 4 / 8, some of 33 of 50001 68 / 44 / 40.
 int sample_cluster(int64_t V) {
   int C = 1;
   while (C < kSampMaxC && V / (2 * C) >= 4096) C *= 2;
