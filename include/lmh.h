@@ -595,6 +595,8 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  * Weights are computed in fp64 and added as whole numbers of 2^-F of the largest, F = min(50,
  * 62 - ceil(log2 V)), so the token does not depend on any order of addition, on N, on the other
  * rows or on the device. A token below 2^-F of the most likely one's probability is never drawn.
+ * (Where nothing is filtered, the running weight up to a run of 256 ids is that of such runs, each
+ * added in fp64 in a fixed order and rounded once; a run in which no token may be drawn has none.)
  *   logits [N, V] of type dtype, row-major and contiguous, aligned to their element; -inf marks a
  *   token that cannot be drawn. u [N] fp32 in [0, 1). tokens [N] int32 out. logprob [N] fp32 out,
  *   nullable: z_token / tau_i - log sum_v exp(z_v / tau_i) over the whole row before the filters,

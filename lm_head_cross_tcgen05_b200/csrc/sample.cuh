@@ -522,12 +522,14 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
   if (no_sum(p, row, zmax, tid == 0)) return;
   if (f.flag && tid == 0) atomicOr(p.err, f.flag);
   const SampRow R = samp_row(p, zmax, f.tau, sh.table);
+  auto block_max = [&](int b) -> float {
+    const float4 u = reinterpret_cast<const float4*>(gmax)[b * 2], v = reinterpret_cast<const float4*>(gmax)[b * 2 + 1];
+    return fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+  };
   // block b's sum of exponentials relative to the row's maximum
   auto block_sum = [&](int b) -> double {
     const double s = gsum[b];
-    const float4 u = reinterpret_cast<const float4*>(gmax)[b * 2], v = reinterpret_cast<const float4*>(gmax)[b * 2 + 1];
-    const float m = fmaxf(fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)), fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-    const double y = R.y64(m);
+    const double y = R.y64(block_max(b));
     if (!(s > 0.0) || y < -64.0 * 100) return 0.0;  // less than 2^-100 of the largest weight
     double e, sc;
     exp2_64(y, 0, sh.table, &e, &sc);
@@ -535,19 +537,31 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
   };
 
   if (f.off()) {
-    // whole numbers of 2^-F again; each thread has a run of blocks
+    // whole numbers of 2^-F again; each thread has a run of blocks. A block none of whose logits has
+    // a weight is not drawn from, whatever they weigh together: every other one holds a token that
+    // may be drawn, its largest. For the log-prob it counts.
     const double up = __hiloint2double((1023 + p.F) << 20, 0);
     const int run = (p.blocks + kSampThreads - 1) / kSampThreads;
     const int r0 = min(p.blocks, tid * run), r1 = min(p.blocks, r0 + run);
-    auto block_weight = [&](int b) -> u64 { return __double2ull_rn(block_sum(b) * up); };
+    auto block_weight = [&](int b, double sum) -> u64 {
+      return R.weight(block_max(b)) > 0 ? __double2ull_rn(sum * up) : 0;
+    };
     u64 s = 0, before, total;
-    for (int b = r0; b < r1; ++b) s += block_weight(b);
+    double all = 0.0;
+    for (int b = r0; b < r1; ++b) {
+      const double x = block_sum(b);
+      s += block_weight(b, x);
+      all += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) sh.dred[warp] = all;
     block_scan(s, &before, &total, sh.red[1]);
     const u64 r = f.draw_at(total);
     if (before <= r && r < before + s) {
       int b = r0;
       for (; b < r1 - 1; ++b) {
-        const u64 w = block_weight(b);
+        const u64 w = block_weight(b, block_sum(b));
         if (r < before + w) break;
         before += w;
       }
@@ -556,6 +570,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
     }
     __syncthreads();
     if (warp != 0) return;
+    all = sh.dred[lane & (kSampWarps - 1)];
+#pragma unroll
+    for (int o = kSampWarps / 2; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
     // within the block, 8 adjacent logits a lane; its weights' sum is its rounded sum up to their
     // own roundings, so a remainder past the last goes to the last that can be drawn
     const long long i0 = static_cast<long long>(sh.pick) * kBlock + lane * 8;
@@ -577,11 +594,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
     }
     const uint32_t found = __ballot_sync(0xffffffffu, hit >= 0);
     const uint32_t can = __ballot_sync(0xffffffffu, last >= 0);
-    const int owner = found ? __ffs(found) - 1 : (can ? 31 - __clz(can) : 0);
+    const int owner = found ? __ffs(found) - 1 : 31 - __clz(can);  // the block's largest can
     if (lane == owner) {
-      const long long id = i0 + (found ? hit : max(last, 0));
+      const long long id = i0 + (found ? hit : last);
       p.tokens[row] = static_cast<int>(id);
-      if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), static_cast<double>(total) / up);
+      if (p.logprob) p.logprob[row] = samp_logprob(R, as_float(src[id]), all);
     }
     return;
   }

@@ -346,3 +346,37 @@ def test_logits_at_any_address(dtype, by):
         ref = check(z, u, **kw)
         o = check(moved, uu[1:], **kw)
         assert torch.equal(o["tokens"], ref["tokens"]) and torch.equal(o["logprob"], ref["logprob"])
+
+
+def below(V, bits, dtype):
+    """A logit of the type that is next to `bits` above or below 2^-F of a largest one of 0; F as in lmh.h."""
+    F = min(50, 62 - int(np.ceil(np.log2(V))))
+    return F, float(torch.tensor(-(F - bits) * np.log(2.0)).to(dtype))
+
+
+ALL_FILTERS = [dict(), dict(k=50), dict(k=2000), dict(p=0.9), dict(m=1e-30), dict(m=0.05), dict(k=40, p=0.8), dict(k=1500, p=0.9, m=1e-30)]
+
+
+@pytest.mark.parametrize("kw", ALL_FILTERS)
+@pytest.mark.parametrize("dtype", [f32, torch.bfloat16])
+@pytest.mark.parametrize("V", [768, 5000, 151936])
+def test_blocks_of_weightless_logits_are_passed_over(V, dtype, kw):
+    """256 logits, each too small to be drawn though all of them together are not: u at their place."""
+    F, low = below(V, -1.45, dtype)
+    e = np.exp(low)
+    assert e < 2.0 ** -(F + 1) and 250 * e > 2.0 ** -F
+    z = torch.full((5, V), -torch.inf, device="cuda")
+    z[0, 1:256], z[0, 256:] = low, 0.0           # id 0 masked, and the first block weightless
+    z[1, :256], z[1, 256:] = low, 0.0
+    z[2, 256:512], z[2, 600:] = low, 0.0         # nothing, a weightless block, then the rest
+    z[3, 7], z[3, 256:512], z[3, 700] = 0.0, low, 0.0
+    z[4, 7], z[4, 512:768], z[4, 300] = 0.0, low, 0.0  # behind the last that can be drawn
+    u = torch.tensor([0.0, 0.0, 0.0, 0.5, 1 - 2.0 ** -24], device="cuda")
+    z = z.to(dtype)
+    names = dict(k="top_k", p="top_p", m="min_p")
+    o = L.sample(z, u, **{names[a]: v for a, v in kw.items()})
+    # with k = 40 of equal ones p = 0.8 keeps 32, which start with the first; u = 0.5 halves two
+    want = [256, 256, 600, 700, 300]
+    assert L.lmh_read_errors(o["workspace"]) == 0 and o["tokens"].tolist() == want
+    lp = -np.log(np.exp(f64(z)).sum(1))
+    assert np.all(np.abs(f64(o["logprob"]) - lp) <= 2.0 ** -24 * (np.abs(lp) + 1) + 2.0 ** -22)
