@@ -33,7 +33,7 @@
 // Where a token depends on sums of weights, the weights are whole numbers, so that no order of
 // addition can change it: w(z) = round(2^F exp((z - zmax) / tau)), computed in fp64, with 2^F as
 // large as V weights can be added in 63 bits (F = 44 for a vocabulary of 152 thousand, at most
-// 50). A token whose probability is below 2^-F of the most likely one's counts as impossible.
+// 50). A token whose probability is below 2^-F of the most likely one's has none.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -189,11 +189,14 @@ struct SampRow {
   }
   // 64 log2 of the probability over the largest one's
   __device__ __forceinline__ double y64(float z) const { return (widen(z) - zmaxd) * c64; }
-  // 2^F 2^(y / 64) as a whole number, read from the low bits of a sum with 2^52: an addition
-  // where a conversion of 64-bit types runs at a fraction of that rate
+  // whether a token with this y64() may be drawn: its probability is at least 2^-F of the largest
+  __device__ __forceinline__ bool may_draw(double y) const { return y >= -64.0 * F; }
+  // 2^F 2^(y / 64) as a whole number (1 at least where the token may be drawn, else 0), read from
+  // the low bits of a sum with 2^52: an addition where a conversion of 64-bit types runs at a
+  // fraction of that rate
   __device__ __forceinline__ u64 weight(float z) const {
     const double y = y64(z);
-    if (y < -64.0 * (F + 1) || !(z > -INFINITY)) return 0;
+    if (!may_draw(y) || !(z > -INFINITY)) return 0;
     double e, sc;
     exp2_64(y, F, table, &e, &sc);
     return static_cast<u64>(__double_as_longlong(fma(e, sc, 4503599627370496.0))) - 0x4330000000000000ull;
@@ -537,14 +540,13 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
   };
 
   if (f.off()) {
-    // whole numbers of 2^-F again; each thread has a run of blocks. A block none of whose logits has
-    // a weight is not drawn from, whatever they weigh together: every other one holds a token that
-    // may be drawn, its largest. For the log-prob it counts.
+    // whole numbers of 2^-F again; each thread has a run of blocks. A block whose largest logit may
+    // not be drawn is passed over, whatever they weigh together. For the log-prob it counts.
     const double up = __hiloint2double((1023 + p.F) << 20, 0);
     const int run = (p.blocks + kSampThreads - 1) / kSampThreads;
     const int r0 = min(p.blocks, tid * run), r1 = min(p.blocks, r0 + run);
     auto block_weight = [&](int b, double sum) -> u64 {
-      return R.weight(block_max(b)) > 0 ? __double2ull_rn(sum * up) : 0;
+      return R.may_draw(R.y64(block_max(b))) ? __double2ull_rn(sum * up) : 0;
     };
     u64 s = 0, before, total;
     double all = 0.0;

@@ -380,3 +380,21 @@ def test_blocks_of_weightless_logits_are_passed_over(V, dtype, kw):
     assert L.lmh_read_errors(o["workspace"]) == 0 and o["tokens"].tolist() == want
     lp = -np.log(np.exp(f64(z)).sum(1))
     assert np.all(np.abs(f64(o["logprob"]) - lp) <= 2.0 ** -24 * (np.abs(lp) + 1) + 2.0 ** -22)
+
+
+@pytest.mark.parametrize("kw", ALL_FILTERS)
+@pytest.mark.parametrize("dtype", [f32, torch.bfloat16])
+@pytest.mark.parametrize("V", [768, 5000, 151936])
+def test_the_least_probability_that_is_drawn(V, dtype, kw):
+    """At u = 0 the first id whose probability is at least 2^-F of the largest is drawn."""
+    F, under = below(V, -0.5, dtype)
+    _, over = below(V, 0.25, dtype)
+    assert np.exp(under) < 2.0 ** -(F + 0.25) and np.exp(over) > 2.0 ** -F
+    z = torch.full((3, V), -torch.inf, device="cuda")
+    z[0, 0], z[0, 300] = under, 0.0
+    z[1, :256], z[1, 300] = under, 0.0
+    z[2, 0], z[2, 5], z[2, 300] = under, over, 0.0
+    names = dict(k="top_k", p="top_p", m="min_p")
+    o = L.sample(z.to(dtype), torch.zeros(3, device="cuda"), **{names[a]: v for a, v in kw.items()})
+    far = 300 if kw.get("p") or kw.get("m") == 0.05 else 5  # top-p and min-p leave the largest alone
+    assert o["tokens"].tolist() == [300, 300, far]
