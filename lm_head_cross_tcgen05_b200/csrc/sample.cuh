@@ -150,11 +150,15 @@ struct alignas(16) RowShared {
 };
 static_assert(sizeof(RowShared) % 16 == 0, "the row's copy follows, in 16-byte vectors");
 
-// A float as a double by its bits: a conversion runs at a quarter of this rate. Zeros and subnormal
-// numbers come out below 2^-125, infinities as +-2^128.
-__device__ __forceinline__ double widen(float x) {
+// A float as a double by its bits: a conversion runs at a quarter of this rate. Infinities come out
+// as +-2^128. Not for zeros and subnormal numbers, whose bits mean something else.
+__device__ __forceinline__ double widen_normal(float x) {
   const uint32_t b = __float_as_uint(x);
   return __hiloint2double(static_cast<int>((b & 0x80000000u) | (((b & 0x7fffffffu) >> 3) + 0x38000000u)), static_cast<int>(b << 29));
+}
+constexpr float kLeastNormal = 1.17549435e-38f;  // 2^-126
+__device__ __forceinline__ double widen(float x) {
+  return fabsf(x) < kLeastNormal ? static_cast<double>(x) : widen_normal(x);
 }
 
 // 2^up 2^(y / 64) as e * sc: with n the whole number next to y and g = (y - n) ln2 / 64, the
@@ -471,13 +475,21 @@ __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const S
     if (fabsf(m) <= 3.402823466e38f) {  // else no finite logit, or the row has no finite sum
       if (exact) {
         const double md = widen(m);
+        auto add = [&](auto wide) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const double y = (widen(z[q][j]) - md) * c64;
-          double e = 0.0, sc = 0.0;
-          if (y > -64.0 * 100 && z[q][j] > -INFINITY) exp2_64(y, 0, table, &e, &sc);  // less cannot be drawn
-          s = fma(e, sc, s);
-        }
+          for (int j = 0; j < 8; ++j) {
+            const double y = (wide(z[q][j]) - md) * c64;
+            double e = 0.0, sc = 0.0;
+            if (y > -64.0 * 100 && z[q][j] > -INFINITY) exp2_64(y, 0, table, &e, &sc);  // less cannot be drawn
+            s = fma(e, sc, s);
+          }
+        };
+        // one look at eight logits (256 x 151936: 83.7 us; 83.3 without, 86 with one at each)
+        float least = fabsf(z[q][0]);
+#pragma unroll
+        for (int j = 1; j < 8; ++j) least = fminf(least, fabsf(z[q][j]));
+        if (least >= kLeastNormal) add([](float x) { return widen_normal(x); });
+        else add([](float x) { return widen(x); });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       } else {

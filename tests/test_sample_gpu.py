@@ -398,3 +398,21 @@ def test_the_least_probability_that_is_drawn(V, dtype, kw):
     o = L.sample(z.to(dtype), torch.zeros(3, device="cuda"), **{names[a]: v for a, v in kw.items()})
     far = 300 if kw.get("p") or kw.get("m") == 0.05 else 5  # top-p and min-p leave the largest alone
     assert o["tokens"].tolist() == [300, 300, far]
+
+
+@pytest.mark.parametrize("kw", [dict(m=1.0), dict(m=2.0), dict(m=0.5), dict(k=3000, m=1.0), dict(p=0.9, m=1.0), dict(p=0.5), dict()])
+@pytest.mark.parametrize("V", [300, 40000])
+@pytest.mark.parametrize("dtype", [f32, torch.bfloat16])
+def test_zeros_of_both_signs_are_equal(dtype, V, kw):
+    z, u = logits(8, V, seed=30)
+    z = torch.where(z > 2, 0.0, torch.where(z > 0, -0.0, -z.abs()))
+    for tau in (None, 1e-38):
+        check(z.to(dtype), u, tau=tau, **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(p=0.6)])
+@pytest.mark.parametrize("V", [300, 40000])
+def test_subnormal_logits_at_tiny_temperatures(V, kw):
+    z, u = logits(4, V, seed=31, scale=4e-39)
+    check(z, u, tau=2e-39, **kw)
+    check(z, u, tau=1.5e-38, **kw)
