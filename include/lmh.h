@@ -604,7 +604,7 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *   A row whose log-sum-exp is not finite (no logit above -inf, a NaN, a +inf) gets token -1 (an
  *   ignored label) and logprob 0, and sets LMH_DEVERR_NONFINITE. A NaN top_p or min_p of a row is
  *   off, a u below 0 or NaN counts as 0, one of 1 or more draws the last kept id; each sets
- *   LMH_DEVERR_SAMPLING. A NaN scalar is refused.
+ *   LMH_DEVERR_SAMPLING, in rows of token -1 too. A NaN scalar is refused.
  *   shape: N < 2^28, V, the temperature. Workspace: lmh_workspace_size(shape, LMH_ENTRY_SAMPLE).
  */
 typedef struct lmh_sampling {

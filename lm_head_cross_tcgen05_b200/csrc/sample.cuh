@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
   if (lane == 0) sh.red[0][warp] = __float_as_uint(tmax);
   __syncthreads();
   const float zmax = warp_max_nan(__uint_as_float(static_cast<uint32_t>(sh.red[0][lane & (kSampWarps - 1)])));
-  if (no_sum(p, row, zmax, tid == 0)) return;
   if (f.flag && tid == 0) atomicOr(p.err, f.flag);
+  if (no_sum(p, row, zmax, tid == 0)) return;
   const SampRow R = samp_row(p, zmax, f.tau, sh.table);
   auto block_max = [&](int b) -> float {
     const float4 u = reinterpret_cast<const float4*>(gmax)[b * 2], v = reinterpret_cast<const float4*>(gmax)[b * 2 + 1];

@@ -416,3 +416,21 @@ def test_subnormal_logits_at_tiny_temperatures(V, kw):
     z, u = logits(4, V, seed=31, scale=4e-39)
     check(z, u, tau=2e-39, **kw)
     check(z, u, tau=1.5e-38, **kw)
+
+
+def test_parameters_of_rows_without_a_sum_are_flagged():
+    z, u = logits(3, 500, seed=32)
+    z[1] = -torch.inf
+    nan = float("nan")
+    good = torch.full((3,), 0.9, device="cuda")
+    bad = good.clone()
+    bad[1] = nan
+    for kw in (dict(u=u), dict(u=u, top_p=good)):
+        o = L.sample(z, **kw)
+        assert L.lmh_read_errors(o["workspace"]) == L.DEVERR_NONFINITE
+    for kw, flag in ((dict(top_p=bad), L.DEVERR_SAMPLING), (dict(min_p=bad), L.DEVERR_SAMPLING), (dict(temperature=bad), L.DEVERR_TEMPERATURE)):
+        o = L.sample(z, u, **kw)
+        assert L.lmh_read_errors(o["workspace"]) == L.DEVERR_NONFINITE | flag
+        assert o["tokens"][1] == -1 and o["logprob"][1] == 0
+    u[1] = 1.5
+    assert L.lmh_read_errors(L.sample(z, u)["workspace"]) == L.DEVERR_NONFINITE | L.DEVERR_SAMPLING
