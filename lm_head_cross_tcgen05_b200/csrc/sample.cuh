@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const S
     __syncthreads();
   }
   const double c64 = exact ? 64.0 * 1.4426950408889634 / (static_cast<double>(tau) * p.tau) : 0.0;
-  // 2 log2(e) / tau, kept off 0 so that masked logits stay at 2^-inf
-  const float c2 = fmaxf(fminf(2.8853900817779268f / p.tau / tau, 3e38f), 1.2e-38f);
+  // 2 log2(e) / tau, kept off 0 so that masked logits stay at 2^-inf; of the product, since one
+  // factor alone may leave the range that 2 log2(e) / tau is in
+  const float c2 = fmaxf(fminf(2.8853900817779268f / (p.tau * tau), 3e38f), 1.2e-38f);
 #pragma unroll
   for (int q = 0; q < kGroupPer; ++q) {
     if (b0 + q >= p.blocks) break;

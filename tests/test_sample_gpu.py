@@ -434,3 +434,26 @@ def test_parameters_of_rows_without_a_sum_are_flagged():
         assert o["tokens"][1] == -1 and o["logprob"][1] == 0
     u[1] = 1.5
     assert L.lmh_read_errors(L.sample(z, u)["workspace"]) == L.DEVERR_NONFINITE | L.DEVERR_SAMPLING
+
+
+@pytest.mark.parametrize("scalar,row", [(1e-44, 2.9e38), (2.9e38, 1e-38)])
+def test_product_of_far_apart_temperatures(scalar, row):
+    """Only their product counts, and it is an ordinary number."""
+    N, V = 5, 3000
+    scalar, row = float(np.float32(scalar)), float(np.float32(row))
+    z, u = logits(N, V, seed=33, scale=3 * scalar * row)
+    rows = torch.full((N,), row, device="cuda")
+    shape = L.make_shape(N, 64, V, temperature=rows)
+    shape.temperature = scalar
+    for kw in (dict(), dict(top_k=9), dict(min_p=0.01), dict(top_p=0.5)):
+        tok, lp = torch.empty(N, dtype=torch.int32, device="cuda"), torch.empty(N, device="cuda")
+        ws = L.workspace(shape, L.ENTRY_SAMPLE, "cuda")
+        L.lmh_sample(shape, L.make_sampling(N, **kw), z, u, tok, lp, workspace=ws)
+        exact = {a: v if a == "top_k" else float(np.float32(v)) for a, v in kw.items()}
+        zz, uu, tau = f64(z), f64(u), scalar * row
+        for i in range(N):
+            t, w = S.sample(zz[i], uu[i], tau, **exact)
+            t0 = (zz[i] - zz[i].max()) / tau
+            away = -(np.exp(t0) * t0).sum() / np.exp(t0).sum()
+            # as in check(); y has one rounding more, that of the product
+            assert tok[i] == t and abs(float(lp[i]) - w) <= 2.0 ** -24 * (abs(w) + 1) + 2.0 ** -22 + 4 * 2.0 ** -24 * away + V * 2.0 ** -41
