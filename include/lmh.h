@@ -554,12 +554,14 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *   these overlap no input. rstd [N] fp32 out, nullable. No workspace.
  *   A row that holds a NaN gives NaN; one that holds an infinity gives NaN there and 0
  *   elsewhere. A row of finite values whose fp32 sum of squares overflows (|r| around 1e18 and
- *   more) gives 0.
+ *   more) gives 0, with rstd 0; with eps = 0 one whose sum underflows (|r| around 1e-20 and less, a
+ *   row of zeros) gives infinities and NaN.
  *
  * lmh_rms_norm_bwd — its gradients, from sum = r and rstd as the forward gave them: with
  * n_j = r_j rstd and c = mean_j(weight_j dy_j n_j),
  *   dx = rstd (weight dy - n c) + dsum   (the gradient of x and of residual alike),
  *   dweight_j = sum over the rows of dy_j n_j.
+ *   Where the forward gave rstd = 0, n = 0: dx is dsum.
  *   dy [N, d] bf16: dL/dy. dsum [N, d] bf16, nullable: the gradient that reaches r by another
  *   way than y. dx [N, d] and dweight [d] bf16 out, each nullable but not both; dx may be dy or
  *   dsum themselves. dweight is summed in fp32 over fixed slices of the rows (a function of N),

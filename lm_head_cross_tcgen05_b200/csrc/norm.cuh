@@ -273,14 +273,13 @@ __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) rms_norm_bwd_kernel(con
       unpack8(w[j], wf);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float dr = dy[e] * r[e];
-        c = fmaf(wf[e], dr, c);
-        acc[j][e] = fmaf(dr, rstd, acc[j][e]);
+        const float dn = dy[e] * (r[e] * rstd);  // n is of order one, whatever the row's size
+        c = fmaf(wf[e], dn, c);
+        acc[j][e] += dn;
       }
     }
     if (!p.dx) continue;
-    // dx = rstd w dy - r rstd^3 mean(w dy r) + dsum
-    c = row_sum(c, sh[flip]) * p.inv_d * rstd * rstd * rstd;
+    c = row_sum(c, sh[flip]) * p.inv_d;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = threadIdx.x + j * blockDim.x;
@@ -291,7 +290,7 @@ __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) rms_norm_bwd_kernel(con
       unpack8(w[j], wf);
       unpack8(p.dsum ? ld_shared_v4(mine + at * stage + j * blockDim.x * 16 + 2 * tensor) : make_uint4(0, 0, 0, 0), ds);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ds[e] = fmaf(rstd, wf[e] * dy[e], fmaf(-c, r[e], ds[e]));
+      for (int e = 0; e < 8; ++e) ds[e] = fmaf(rstd, fmaf(-c, r[e] * rstd, wf[e] * dy[e]), ds[e]);
       p.dx[base + v] = pack8(ds);
     }
   }

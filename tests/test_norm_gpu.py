@@ -333,3 +333,33 @@ def test_inputs_that_are_views():
     q, rq = L.rms_norm(x, w, r, fp8=True), L.rms_norm(x.clone(), w.clone(), r.clone(), fp8=True)
     assert torch.equal(f["y"], ref["y"]) and torch.equal(b["dx"], rb["dx"]) and torch.equal(b["dweight"], rb["dweight"])
     assert torch.equal(q["q"].view(torch.uint8), rq["q"].view(torch.uint8)) and torch.equal(q["scale"], rq["scale"])
+
+
+def test_backward_of_rows_far_from_one():
+    """Rows so large that the forward gives 0 (rstd = 0): dx = dsum there and no share of dweight.
+    And small rows with small gradients, whose products r dy would be subnormal."""
+    N, d = 6, 192
+    x, w, dy, ds = rand(N, d, seed=41), rand(d, seed=42), rand(N, d, seed=43, scale=30), rand(N, d, seed=44)
+    x[2], x[4] = 3e38, -2e38
+    f = L.rms_norm(x, w)
+    assert torch.all(f["rstd"][[2, 4]] == 0) and torch.all(f["y"][[2, 4]] == 0)
+    b = L.rms_norm_bwd(f["sum"], w, f["rstd"], dy, ds)
+    assert torch.equal(b["dx"][[2, 4]], ds[[2, 4]])
+    rest = [0, 1, 3, 5]
+    part = L.rms_norm_bwd(f["sum"][rest].clone(), w, f["rstd"][rest].clone(), dy[rest].clone(), ds[rest].clone())
+    assert torch.equal(b["dx"][rest], part["dx"])
+    r, wf, g = f64(x[rest]), f64(w), f64(dy[rest])
+    _, dw = S.rms_norm_bwd(r, wf, 1e-6, g)
+    n = r / np.sqrt((r * r).mean(1, keepdims=True) + 1e-6)
+    assert np.all(np.abs(f64(b["dweight"]) - dw) <= BF * np.abs(dw) + 2 * E32 * (np.abs(g * n)).sum(0))
+
+    x, dy = rand(N, d, seed=45, scale=1e-15), rand(N, d, seed=46, scale=1e-27)
+    f = L.rms_norm(x, w, eps=0.0)
+    b = L.rms_norm_bwd(f["sum"], w, f["rstd"], dy)
+    r, g = f64(x), f64(dy)
+    dx, dw = S.rms_norm_bwd(r, wf, 0.0, g)
+    rstd = 1 / np.sqrt((r * r).mean(1, keepdims=True))
+    n = np.abs(r * rstd)
+    terms = rstd * (np.abs(wf * g) + n * (np.abs(wf * g) * n).mean(1, keepdims=True))
+    assert np.all(np.abs(f64(b["dx"]) - dx) <= BF * np.abs(dx) + 3 * E32 * terms)
+    assert np.all(np.abs(f64(b["dweight"]) - dw) <= BF * np.abs(dw) + 2 * E32 * (np.abs(g) * n).sum(0))
