@@ -175,6 +175,13 @@ def support_kl(H, W, ids, ref_logp, *, reduction: str = "mean", chunk_rows: int 
     return _SupportKL.apply(H, W, ids, ref_logp, reduction, chunk_rows, temperature, renorm)
 
 
+def _aligned(g):
+    """An upstream gradient lies where torch has it, in a larger buffer maybe: contiguous and at
+    a multiple of 16 bytes, as the entries need it."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
 class _RMSNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
@@ -190,8 +197,8 @@ class _RMSNorm(torch.autograd.Function):
         if dy is None:  # y took no part in the loss
             return dsum if need_x else None, None, dsum if need_r else None, None
         total, weight, rstd = ctx.saved_tensors
-        out = rms_norm_bwd(total, weight, rstd, dy.contiguous(),
-                           None if dsum is None else dsum.contiguous(), want_dx=need_x or need_r,
+        out = rms_norm_bwd(total, weight, rstd, _aligned(dy),
+                           None if dsum is None else _aligned(dsum), want_dx=need_x or need_r,
                            want_dweight=need_w)
         return (out["dx"] if need_x else None, out["dweight"], out["dx"] if need_r else None,
                 None)

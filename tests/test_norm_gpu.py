@@ -363,3 +363,20 @@ def test_backward_of_rows_far_from_one():
     terms = rstd * (np.abs(wf * g) + n * (np.abs(wf * g) * n).mean(1, keepdims=True))
     assert np.all(np.abs(f64(b["dx"]) - dx) <= BF * np.abs(dx) + 3 * E32 * terms)
     assert np.all(np.abs(f64(b["dweight"]) - dw) <= BF * np.abs(dw) + 2 * E32 * (np.abs(g) * n).sum(0))
+
+
+@pytest.mark.parametrize("both", [False, True])
+def test_autograd_of_gradients_at_any_address(both):
+    """An upstream gradient is wherever torch has it: here one element behind an aligned address."""
+    N, d = 5, 128
+    x, r, w = rand(N, d, seed=47), rand(N, d, seed=48), rand(d, seed=49)
+    first = torch.zeros(1, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    lx, lr, lw = (t.clone().requires_grad_() for t in (x, r, w))
+    H, total = A.rms_norm(lx, lw, lr)
+    parts = [first, H.flatten()] + ([total.flatten()] if both else [])
+    g = rand(1, 1 + (len(parts) - 1) * N * d, seed=50).flatten()
+    torch.cat(parts).backward(g)
+    f = L.rms_norm(x, w, r)
+    dy = g[1:1 + N * d].clone().view(N, d)
+    b = L.rms_norm_bwd(f["sum"], w, f["rstd"], dy, g[1 + N * d:].clone().view(N, d) if both else None)
+    assert torch.equal(lx.grad, b["dx"]) and torch.equal(lr.grad, b["dx"]) and torch.equal(lw.grad, b["dweight"])
