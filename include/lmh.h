@@ -564,8 +564,8 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *   Where the forward gave rstd = 0, n = 0: dx is dsum.
  *   dy [N, d] bf16: dL/dy. dsum [N, d] bf16, nullable: the gradient that reaches r by another
  *   way than y. dx [N, d] and dweight [d] bf16 out, each nullable but not both; dx may be dy or
- *   dsum themselves. dweight is summed in fp32 over fixed slices of the rows (a function of N),
- *   in a fixed order, and rounded once; N = 0 gives 0. Workspace: lmh_workspace_size(shape,
+ *   dsum themselves. dweight is summed in fp32 over fixed slices of the rows (a function of N
+ *   and d), in a fixed order, and rounded once; N = 0 gives 0. Workspace: lmh_workspace_size(shape,
  *   LMH_ENTRY_RMS_NORM_BWD) with N and d in the shape (V any valid value).
  *
  * lmh_quantize_fp8 — x [rows, d] bf16 as an 8-bit matrix q, scale with blocks of block_rows x 128
@@ -574,7 +574,8 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  * lmh_fp8_logits — the logits of 8-bit hidden states and an 8-bit weight,
  *   z_nv = sum_b h_scale[n, b] w_scale[v / 128, b] sum_{k in block b} H8[n, k] W8[v, k],
  * b over blocks of 128 columns: each block's products are summed on the tensor cores, times its
- * scale added in fp32 in ascending b, and the logit rounded once to its type. The value of a
+ * scale (the two scales' product, formed in fp32) added in fp32 in ascending b, and the logit
+ * rounded once to its type. The value of a
  * logit depends on N (few or many rows are summed by different kernels) but not on the device.
  *   H8 [N, d] and h_scale [N, ceil(d / 128)] as lmh_rms_norm or lmh_quantize_fp8 (block_rows 1)
  *   gives them; W8 [V, d] and w_scale [ceil(V / 128), ceil(d / 128)] as lmh_quantize_fp8

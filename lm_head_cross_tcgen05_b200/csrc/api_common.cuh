@@ -172,8 +172,10 @@ void norm_threads(int64_t d, int* vpt, int* threads) {
   *threads = static_cast<int>(cdiv(cdiv(nv, *vpt), 32) * 32);
 }
 // Row slices of the norm's backward pass, each with an fp32 share of dweight: what 148 SMs hold at
-// once (1024 threads each where a thread has one vector, 640 where it has more and the registers
-// bound it), at most N. By N and d alone, so that dweight does not depend on the device.
+// once by their threads (1024 each where a thread has one vector, 640 where it has more and the
+// registers bound it), at most N. By N and d alone, so that dweight does not depend on the device.
+// For d = 9280 .. 10240 two blocks' rings (120 KB each) are more than an SM has: the 296 slices run
+// as two waves (4096 x 9600: 70 us, 67 with one slice an SM).
 // (8192 x 2048: 38 us with 2 slices an SM, 32 with these 4; 4096 x 5120: 52 with 64 registers a
 // thread, 37 with what it needs.)
 int norm_slices(int64_t N, int64_t d) {

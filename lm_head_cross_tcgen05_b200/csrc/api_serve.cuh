@@ -134,7 +134,8 @@ extern "C" lmh_status lmh_quantize_fp8(int64_t rows, int64_t d, int32_t block_ro
   if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return LMH_ERR_ALIGNMENT;
   const int64_t nb = cdiv(d, kQBlock);
   // A warp a row where the rows fill the GPU, a block of threads a row where they do not: d = 4096,
-  // 600 rows 10.9 us by warps, 8.9 by blocks; 4096 rows 16.8 and 19.6.
+  // 600 rows 10.9 us by warps, 8.9 by blocks; 4096 rows 16.8 and 19.6 (from cold caches; 4096 rows by
+  // warps take 9.9 in a loop over 34 MB, which L2 holds).
   const int per = rows < 8 * 148 ? 256 : 32;
   const int64_t grid = block_rows == 1 ? cdiv(rows, 256 / per) : cdiv(rows, kQBlock) * nb;
   if (cdiv(rows, block_rows) * nb > 0x7fffffffLL) return LMH_ERR_INVALID_ARG;
@@ -218,7 +219,8 @@ lmh_status launch_many(FpParams p, const uint8_t* H8, const uint8_t* W8, int64_t
 }
 
 // The kernel with few columns of tokens as far as it goes: 128256 x 4096 from cold caches, 1 / 32 / 64
-// tokens 108 / 108 / 113 us, by the other kernel 120 / 115 / 118. The narrowest that holds the
+// tokens 108 / 108 / 113 us, by the other kernel 120 / 115 / 118. (A weight that L2 holds may be faster by
+// the other: 32000 x 2048 in a loop, 64 tokens 21.9 us, 65 by the other 16.4.) The narrowest that holds the
 // tokens: with 64 columns 1 / 16 / 32 tokens took 113 / 107 / 110 us, with their own 108 / 106 / 108.
 template <class Out>
 lmh_status launch_fp8(const FpParams& p, const uint8_t* H8, const uint8_t* W8, int64_t d, int dev,

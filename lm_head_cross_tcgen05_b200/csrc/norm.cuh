@@ -2,7 +2,7 @@
 // per row and 128 columns), its backward pass, and the e4m3 quantisation of matrices by blocks.
 // All are HBM bound: each row is held in registers between its two uses, so every tensor crosses
 // memory once. Sums are fp32 in a fixed order (a thread's elements in ascending order, then a
-// butterfly over the warp, then the warps in ascending order): no result depends on the device.
+// butterfly over the warp, then one over the warps): no result depends on the device.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -97,7 +97,8 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {  // all but the last N groups have landed
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Rows of the ring, that under work included: up to 96 KB, or 192 KB for the longest rows.
+// Rows of the ring, that under work included. Forward: 64 KB a block at most where a thread has one
+// vector, 96 KB with two, 192 KB with four; backward: 96, 144 and 192 KB.
 __host__ __device__ constexpr int norm_stages(int vpt) { return vpt == 1 ? 4 : 3; }
 __host__ __device__ constexpr int norm_bwd_stages(int vpt) { return vpt == 1 ? 4 : (vpt == 2 ? 3 : 2); }
 

@@ -26,9 +26,10 @@
 //    repeated with all buckets if the prefix does not end in the window. The draw then starts
 //    from the sums above the window. A bucket with too many members (equal logits, mostly) is
 //    split again by the bits of its keys until they fit or are all equal; equal ones are counted
-//    in vocabulary order. One row of 151936 takes some 40 us, 30 rows 55, all 256 about 270: of a
-//    pass's 20 thousand cycles with 40 percent kept, 8 go to finding the kept, 4 to their fp64
-//    weights, 4 to the window's atomics.
+//    in vocabulary order. A call of one such row of 151936 takes 50 to 58 us, of 30 rows 70 to 84,
+//    of 256 480 to 575 (top-p 0.9, logits of standard deviation 2.5 to 0.5): of a pass's 20 thousand
+//    cycles with 40 percent kept, 8 go to finding the kept, 4 to their fp64 weights, 4 to the
+//    window's atomics.
 //
 // Where a token depends on sums of weights, the weights are whole numbers, so that no order of
 // addition can change it: w(z) = round(2^F exp((z - zmax) / tau)), computed in fp64, with 2^F as
@@ -280,7 +281,9 @@ __device__ __forceinline__ void sort_desc(u64* a, int n) {
 
 // The same for up to 2048 values, bucket(x) from 0 to 2047 never falling as x does: by a histogram of
 // the buckets, then within each, unless one has more than 64. 330 values take 3000 cycles and 1400 values 5000,
-// where counting took 5500 and the network 29000.
+// where counting took 5500 and the network 29000. Up to 128 counting is as fast or faster (256 rows
+// of 151936, top-k 50 / 100 / 200: 47.4 / 49.3 / 53.3 us; with 32 for the 128 49.4 / 50.4 / 53.2, with 64
+// 47.4 / 50.4 / 53.3, with 256 47.4 / 49.3 / 55.3).
 template <class B>
 __device__ __forceinline__ void sort_buckets(u64* a, int n, uint4* chist, u64* red, B bucket) {
   const int tid = threadIdx.x;
@@ -661,7 +664,11 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_list_kernel(const Samp
         // Top-p alone. The maxima themselves weigh at least so much, in 2^-30 of the largest; where
         // they reach the target, or a list of the largest size may, the list has a chance. With c
         // of G groups reaching a bucket, logits in any order, G log(G / (G - c)) logits do. What
-        // is misjudged here costs time: the token is the same from either kernel.
+        // is misjudged here costs time: the token is the same from either kernel. 256 rows of
+        // 50001 / 151936, standard deviations 2 to 8, p = 0.5: 65.5 / 184 us; 103 / 182 if the list
+        // is taken only where the maxima reach the target. Of the constants, 0 or 200 for the 48
+        // and 0.8 or 1.05 for the 0.95 make 2 percent at most; 150 for the 348 66 / 165, but 75 / 116
+        // in 64 rows of bf16 with p = 0.9 that take 73 / 114; 700 62 / 181 and 72 / 123.
         u64 hw[4], pw, tw;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1091,7 +1098,9 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
   // or weight reaches the target; 0 if all of them do not reach it. whole: the weight of all of them.
   int top_lo = 0;  // sh.top has the weights of the buckets below it
   auto prefix = [&](bool by_w, u64 from, u64 target, u64 whole) -> u64 {
-    // a window of buckets from an eighth of the row; all buckets for a short one
+    // a window of buckets from an eighth of the row; all buckets for a short one (32 rows, top-p 0.9
+    // / top-k 3000, without and with: 20000 logits 36.3 / 25.4 and 36.7 / 27.3 us, 30000 40.3 / 27.0
+    // and 39.4 / 28.4, 40000 64.4 / 35.3 and 50.9 / 37.0, 60000 69 / 37.3 and 54.8 / 39.4)
     int lo = 0, hi = kSampBuckets - 1;
     if (p.V > 32768) {
       zero(false);
@@ -1126,6 +1135,10 @@ __global__ void __launch_bounds__(kSampThreads, 2) sample_row_kernel(const SampP
                           static_cast<double>(sampled) / p.V;
       const double t = by_w ? static_cast<double>(all) - rest
                             : static_cast<double>(target) * static_cast<double>(sampled) / p.V;
+      // Margins, 64 rows of 151936. Weights: 0.5, 1, 2 and 5 percent take 142, 144, 145 and 149 us
+      // for p = 0.9 and logits of standard deviation 1.5; with 0.5 percent p = 0.5 misses and takes
+      // 155 where the others take 125 to 129. Counts: without the 16 k = 1100 misses (104 us for 91),
+      // with half the 10 percent k = 5000 does (108 for 98); twice either costs nothing.
       const double t0 = by_w ? t - 0.02 * static_cast<double>(all) : 0.9 * t - 16.0;
       const double t1 = by_w ? t + 0.02 * static_cast<double>(all) : 1.1 * t + 16.0;
 #pragma unroll
