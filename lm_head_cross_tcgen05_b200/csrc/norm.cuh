@@ -219,8 +219,8 @@ struct NormBwdParams {
 };
 
 // A slice of rows per block of threads, which holds dweight's share of its columns in registers.
-// With n = r rstd: dx = rstd (w dy - n mean(w dy n)) + dsum. 8192 x 4096 with dsum: 48 us (268 MB,
-// 5.6 TB/s) and 7 us for the sum over the slices.
+// With n = r rstd: dx = rstd (w dy - n mean(w dy n)) + dsum. 8192 x 4096 with dsum: 49 us (268 MB,
+// 5.5 TB/s) and 7 us for the sum over the slices.
 template <int VPT>
 __global__ void __launch_bounds__(512, VPT == 1 ? 2 : 1) rms_norm_bwd_kernel(const NormBwdParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
