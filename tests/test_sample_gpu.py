@@ -457,3 +457,25 @@ def test_product_of_far_apart_temperatures(scalar, row):
             away = -(np.exp(t0) * t0).sum() / np.exp(t0).sum()
             # as in check(); y has one rounding more, that of the product
             assert tok[i] == t and abs(float(lp[i]) - w) <= 2.0 ** -24 * (abs(w) + 1) + 2.0 ** -22 + 4 * 2.0 ** -24 * away + V * 2.0 ** -41
+
+
+@pytest.mark.parametrize("scalar,row,scale", [(1.0, 1e-40, 2e-40), (1.0, 5e-39, 1e-38), (1e-20, 1e-22, 1e-42), (1e19, 1e20, 1e38), (1e38, 2.9e38, 1e38)])
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=300), dict(min_p=0.01), dict(top_p=0.5)])
+def test_logprob_at_temperatures_whose_inverse_is_no_normal_number(scalar, row, scale, kw):
+    N, V = 4, 2500
+    z, u = logits(N, V, seed=34, scale=1.0)
+    z = z.clamp(-3, 3) * scale
+    z[0, ::2] = -3 * scale
+    rows = torch.full((N,), row, device="cuda")
+    shape = L.make_shape(N, 64, V, temperature=rows)
+    shape.temperature = scalar
+    tok, lp = torch.empty(N, dtype=torch.int32, device="cuda"), torch.empty(N, device="cuda")
+    ws = L.workspace(shape, L.ENTRY_SAMPLE, "cuda")
+    L.lmh_sample(shape, L.make_sampling(N, **kw), z, u, tok, lp, workspace=ws)
+    assert L.lmh_read_errors(ws) == 0
+    exact = {a: v if a == "top_k" else float(np.float32(v)) for a, v in kw.items()}
+    zz, uu, tau = f64(z), f64(u), float(np.float32(scalar)) * float(rows[0])
+    for i in range(N):
+        t, w = S.sample(zz[i], uu[i], tau, **exact)
+        # the sum is in fp64 here: the log-prob has its own rounding alone
+        assert tok[i] == t and abs(float(lp[i]) - w) <= 2.0 ** -24 * (abs(w) + 1) + V * 2.0 ** -41
