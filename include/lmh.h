@@ -554,8 +554,8 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *   these overlap no input. rstd [N] fp32 out, nullable. No workspace.
  *   A row that holds a NaN gives NaN; one that holds an infinity gives NaN there and 0
  *   elsewhere. A row of finite values whose fp32 sum of squares overflows (|r| around 1e18 and
- *   more) gives 0, with rstd 0; with eps = 0 one whose sum underflows (|r| around 1e-20 and less, a
- *   row of zeros) gives infinities and NaN.
+ *   more) gives 0, with rstd 0; with eps = 0 one whose sum underflows (|r| around 1e-23 and less, a
+ *   row of zeros) gives infinities and NaN, and up to |r| around 1e-18 rstd has fewer bits.
  *
  * lmh_rms_norm_bwd — its gradients, from sum = r and rstd as the forward gave them: with
  * n_j = r_j rstd and c = mean_j(weight_j dy_j n_j),
@@ -574,8 +574,8 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  * lmh_fp8_logits — the logits of 8-bit hidden states and an 8-bit weight,
  *   z_nv = sum_b h_scale[n, b] w_scale[v / 128, b] sum_{k in block b} H8[n, k] W8[v, k],
  * b over blocks of 128 columns: each block's products are summed on the tensor cores, times its
- * scale (the two scales' product, formed in fp32) added in fp32 in ascending b, and the logit
- * rounded once to its type. The value of a
+ * scale (the two scales' product, formed in fp32: scales whose product leaves its normal numbers
+ * lose bits or overflow) added in fp32 in ascending b, and the logit rounded once to its type. The value of a
  * logit depends on N (few or many rows are summed by different kernels) but not on the device.
  *   H8 [N, d] and h_scale [N, ceil(d / 128)] as lmh_rms_norm or lmh_quantize_fp8 (block_rows 1)
  *   gives them; W8 [V, d] and w_scale [ceil(V / 128), ceil(d / 128)] as lmh_quantize_fp8
