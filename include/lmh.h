@@ -575,8 +575,9 @@ LMH_API lmh_status lmh_scale_bf16(lmh_bf16* x, int64_t n, const float* g, void* 
  *   z_nv = sum_b h_scale[n, b] w_scale[v / 128, b] sum_{k in block b} H8[n, k] W8[v, k],
  * b over blocks of 128 columns: each block's products are summed on the tensor cores, times its
  * scale (the two scales' product, formed in fp32: scales whose product leaves its normal numbers
- * lose bits or overflow) added in fp32 in ascending b, and the logit rounded once to its type. The value of a
- * logit depends on N (few or many rows are summed by different kernels) but not on the device.
+ * lose bits or overflow) added in fp32 in ascending b, and the logit rounded once to its type.
+ * The value of a logit depends on N (few or many rows are summed by different kernels) but not on
+ * the device.
  *   H8 [N, d] and h_scale [N, ceil(d / 128)] as lmh_rms_norm or lmh_quantize_fp8 (block_rows 1)
  *   gives them; W8 [V, d] and w_scale [ceil(V / 128), ceil(d / 128)] as lmh_quantize_fp8
  *   (block_rows 128) does, once per weight. logits [N, V] out, row-major and contiguous, of type

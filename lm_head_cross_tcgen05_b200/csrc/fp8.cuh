@@ -331,15 +331,16 @@ struct FpMany {
 // are all that TMEM holds, so the way round counts: commit, wake, read, arrive, wake, MMAs. It is
 // not what bounds this kernel, though: bare, it takes 173 us of 301 in the case below, 6 percent
 // over the MMAs' own time. What lies on top does: the readers' waits, scales, additions and the
-// tile's output, with the tensor pipe active 41 percent of the time. 16 warps read at once, 64 columns each with the sums in registers, which the loading
-// warps give up theirs for; the additions take two values an instruction; one commit a block both
-// frees its stage and hands over its columns; and a spare warp brings the scales to shared memory
-// four blocks at a time, up to 16 ahead, since loads of their own would make the reading warps wait.
-// 4096 x 32000 x 2048 to bf16: 349 us with eight warps of 128 columns, 311 with 16, 301 with the
-// scales by fours (1780 TFLOP/s, 54 percent of twice the measured bf16 rate). In copies for timing,
-// without the operands' loads it took 300 where this took 312, without the scales 285, without
-// TMEM reads 273, without output 287, and with none of these, one MMA a block and no additions 173. Accumulators of 128 columns, whose way round would be shorter, took 367, and
-// pairs of CTAs that share a 256 x 256 tile 660.
+// tile's output, with the tensor pipe active 41 percent of the time. 16 warps read at once, 64
+// columns each with the sums in registers, which the loading warps give up theirs for; the
+// additions take two values an instruction; one commit a block both frees its stage and hands over
+// its columns; and a spare warp brings the scales to shared memory four blocks at a time, up to 16
+// ahead, since loads of their own would make the reading warps wait. 4096 x 32000 x 2048 to bf16:
+// 349 us with eight warps of 128 columns, 311 with 16, 301 with the scales by fours (1780 TFLOP/s,
+// 54 percent of twice the measured bf16 rate). In copies for timing, without the operands' loads it
+// took 300 where this took 312, without the scales 285, without TMEM reads 273, without output 287,
+// and with none of these, one MMA a block and no additions 173. Accumulators of 128 columns, whose
+// way round would be shorter, took 367, and pairs of CTAs that share a 256 x 256 tile 660.
 // TMA: the output goes out by TMA from staged boxes of 32 tokens x 64 bytes, where its rows are
 // 16-byte aligned; otherwise by transposes of 32 x 16 through shared memory.
 template <class Out, bool TMA>

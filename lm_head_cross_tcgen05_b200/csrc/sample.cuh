@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(32 * kGroupWarps) sample_groups_kernel(const S
   // Of the product, since one factor alone may leave the range that 2 log2(e) / tau is in. Where that
   // is no normal number, the sums are in fp64.
   const float product = p.tau * tau;
-  const bool exact = samp_exact(p, row) || !(product > 1e-38f && product < 2e38f);  // of the whole block of threads
+  // the same for the whole block of threads
+  const bool exact = samp_exact(p, row) || !(product > 1e-38f && product < 2e38f);
   if (exact) {
     if (threadIdx.x < 64) table[threadIdx.x] = exp2(threadIdx.x / 64.0);
     __syncthreads();
